@@ -399,6 +399,169 @@ int awq_keep_fp16_ablation(const void* W, const void* X, int64_t N, int64_t K, i
                            int32_t* keep_act, int32_t* keep_wt, double* loss,
                            void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Experts: the W4A16 product grouped by expert, with its router and sum.
+ *
+ * A layer of E experts holds E matrices in the packed format, one after the
+ * other (packed [E][N][K/8] at 4 bits, scales [E][N][K/g], zeros
+ * [E][N][ceil(K/g/2)]).  A plan sorts the pairs p = t * top_k + j (token t,
+ * its j-th expert) by expert, pairs of one expert in order of p:
+ *   offsets  device int32 [E+1]      expert e has rows offsets[e] ..
+ *                                    offsets[e+1] - 1 of the ragged batch
+ *   rows     device int32 [T*top_k]  pair of each row; after the last
+ *                                    expert's rows the dropped pairs
+ *   pos      device int32 [T*top_k]  row of each pair, -1 for a dropped one
+ * ------------------------------------------------------------------------ */
+#define AWQ_MAX_EXPERTS 1024
+#define AWQ_MAX_PAIRS (1LL << 24)
+
+/*
+ * awq_moe_plan -- the plan of the given choices.
+ *   experts    device int32 [T][top_k]   an id outside [0, E) drops the pair
+ *   workspace  device, >= awq_moe_workspace_bytes(T, E, top_k) bytes
+ * Requires 1 <= E <= AWQ_MAX_EXPERTS, 1 <= top_k <= 64, T >= 1,
+ * T * top_k <= AWQ_MAX_PAIRS.
+ */
+size_t awq_moe_workspace_bytes(int64_t T, int32_t E, int32_t top_k);
+int awq_moe_plan(const int32_t* experts, int64_t T, int32_t E, int32_t top_k, int32_t* offsets, int32_t* rows,
+                 int32_t* pos, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * awq_moe_route -- each token's top_k experts, their softmax weights, and the
+ * plan.  The experts of a token are those of its top_k largest logits, largest
+ * first and the lower index first where logits are equal; the weights are the
+ * softmax over all E (renormalize = 0) or over the chosen ones (1), in fp32.
+ * A logit of -infinity (a masked expert) or NaN is never chosen and has no
+ * part in the softmax: where fewer than top_k are left, the last choices are
+ * expert -1 with weight 0, and the plan drops them.
+ *   logits     device [T][E], fp16 (logit_bytes = 2) or fp32 (4)
+ *   experts    device int32 [T][top_k]   out
+ *   weights    device fp32 [T][top_k]    out
+ *   offsets, rows, pos                   out, as awq_moe_plan
+ * Requires what awq_moe_plan requires, and top_k <= E.  A logit of +infinity
+ * is outside the contract (unspecified weights).
+ */
+int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E, int32_t top_k, int32_t renormalize,
+                  int32_t* experts, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/*
+ * awq_gemm_grouped -- row i of the ragged batch times its expert's matrix:
+ *   y[i][n] = sum_k xs_i[k] * w_hat_e[n][k],   offsets[e] <= i < offsets[e+1]
+ * with xs_i = x[rows[i] / top_k] (rows as a plan's: the tokens are gathered by
+ * the product itself) or x[i] (rows NULL), divided by s[e] and rounded to fp16
+ * as by awq_scale_input when s is given.
+ *   x        device fp16 [x_rows][K]
+ *   rows     device int32 [R] or NULL; an entry that leads outside x reads
+ *            some row of x instead
+ *   top_k    divisor of the entries of rows (1: they are rows of x)
+ *   offsets  device int32 [E+1], in order, within [0, R]
+ *   s        device fp32 [E][K] or NULL
+ *   packed, scales, zeros   device, the E matrices
+ *   y        device fp16 [R][N]; rows from offsets[E] on are left as they were
+ *   workspace  device, >= awq_gemm_grouped_workspace_bytes(R, K, s given)
+ *            bytes: R * K * 2 rounded up to 256 with s, 0 (may be NULL) without
+ * Accumulation is fp32 and y is rounded to fp16 once; code - zero is exact and
+ * the group's scale is applied in fp32, so no weight is rounded.  The sizes of
+ * the groups stay on the device; the result does not depend on timing.
+ * Requires R, x_rows in [1, 2^24] (x_rows >= R without rows), E in
+ * [1, AWQ_MAX_EXPERTS], bits 4 or 3, group == AWQ_GROUP, K % group == 0,
+ * K <= 2^20.
+ */
+size_t awq_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int32_t scaled);
+int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t top_k, const int32_t* offsets,
+                     const float* s, const void* packed, const void* scales, const void* zeros, void* y, int64_t R,
+                     int32_t E, int64_t N, int64_t K, int32_t group, int32_t bits, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * awq_moe_combine -- out[t] = sum_j weights[t][j] * y[pos[t * top_k + j]], in
+ * fp32 in order of j, rounded to fp16 once.  Pairs with pos outside [0, R)
+ * (dropped ones) add nothing.
+ *   y        device fp16 [R][N]
+ *   out      device fp16 [T][N]
+ * Requires N % 8 == 0, 8 <= N <= 2^20, and T, top_k, R as above.
+ */
+int awq_moe_combine(const void* y, int64_t R, const int32_t* pos, const float* weights, int64_t T, int32_t top_k,
+                    int64_t N, void* out, void* stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * Key-value cache.  Keys and values of a decoder are quantised as they are
+ * written, with awq_pack's quantizer: the D channels of one (token, head) row
+ * are one group, at 4 or 8 bits.  A cache has `pages` pages of `page` slots
+ * (a power of two, 16 .. 1024); slot number = page number * page + place.  Keys
+ * and values are stored alike:
+ *   codes   uint32 [pages][H][page][D*bits/32]   4 bits: the words of the packed
+ *                                       weight format; 8 bits: channel 4w+i in
+ *                                       byte i of word w
+ *   params  fp16   [pages][H][page][2]  scale, zero point (a whole number)
+ * At D = 128 that is 4.25 bits per value (8.25 at 8 bits).
+ * ------------------------------------------------------------------------ */
+#define AWQ_MAX_KV_TOKENS (1LL << 22)
+#define AWQ_MAX_KV_LENGTH (1LL << 25)
+size_t awq_kv_codes_bytes(int64_t pages, int32_t H, int32_t page, int32_t D, int32_t bits);
+size_t awq_kv_params_bytes(int64_t pages, int32_t H, int32_t page);
+
+/*
+ * awq_kv_write -- quantises T tokens' keys and values into their slots.  Per
+ * row (float32, round-to-nearest-even): lo = min(0, min v); hi = max(0, max v);
+ * scale = fp16(max((hi - lo) / q, 2^-14)) with q = 15 or 255; zero =
+ * clamp(rint(-lo / scale), 0, q); code = clamp(rint(v / scale) + zero, 0, q).
+ *   k, v      device fp16; token t's H rows of D start at k + t * k_stride
+ *             (elements, a multiple of 8, >= H * D): slices of a fused q/k/v
+ *             product need no copy
+ *   slots     device int32 [T]; a token whose slot is outside the cache
+ *             (padding: -1) is not written.  Slots of one call are distinct; of
+ *             tokens that share a slot, which one's values end there (row by
+ *             row, or a mix of them) is unspecified
+ * Other slots are left as they were.
+ */
+int awq_kv_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slots, void* k_codes,
+                 void* k_params, void* v_codes, void* v_params, int64_t T, int32_t H, int32_t D, int64_t pages,
+                 int32_t page, int32_t bits, void* stream);
+
+/*
+ * awq_kv_read -- the values T slots hold: fp16((code - zero) * scale), rounded
+ * once; 0 for a slot outside the cache.
+ *   k, v      device fp16 [T][H][D]   out
+ */
+int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, const void* v_params,
+                const int32_t* slots, void* k, void* v, int64_t T, int32_t H, int32_t D, int64_t pages, int32_t page,
+                int32_t bits, void* stream);
+
+/*
+ * awq_kv_attention -- attention of one new token of each of B sequences over
+ * the cache: out[b][h] = sum_t p_t v_t, p = softmax_t(scale * q[b][h] . k_t)
+ * over the sequence's first lengths[b] tokens, k_t and v_t the dequantised rows
+ * of key-value head h / (Hq / Hkv).  (The new token's own key and value are
+ * written first, and counted in lengths.)
+ *   q           device fp16; sequence b's Hq rows of D start at q + b * q_stride
+ *               (elements, a multiple of 8, >= Hq * D)
+ *   page_table  device int32 [B][table_width]: page of the sequence's tokens
+ *               page * i .. page * i + page - 1.  Entries past the length are
+ *               not read; the tokens of an entry outside [0, pages) count as
+ *               absent
+ *   lengths     device int32 [B]; at most table_width * page and max_len are
+ *               used.  A sequence with no tokens gets out = 0
+ *   out         device fp16 [B][Hq][D]
+ *   max_len     host bound on the lengths (0: table_width * page): the split
+ *               over the length is made for it.  At most AWQ_MAX_KV_LENGTH
+ *   workspace   device, >= awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, the
+ *               bound) bytes; it needs no clearing and keeps nothing
+ * Scores, softmax statistics and sums are fp32; a weight p_t enters the
+ * products with 22 bits.  Chunks of a long sequence are joined in order, so the
+ * result does not depend on timing.
+ * Requires D 64, 128 or 256, Hq a multiple of Hkv, 1 <= B <= 65535, finite scale.
+ */
+size_t awq_kv_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t max_len);
+int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const void* k_params, const void* v_codes,
+                     const void* v_params, const int32_t* page_table, int64_t table_width, const int32_t* lengths,
+                     void* out, int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t pages, int32_t page,
+                     int32_t bits, float scale, int64_t max_len, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
 /* Message for a status code; message for the calling thread's last failure. */
 const char* awq_status_string(int status);
 const char* awq_last_error(void);

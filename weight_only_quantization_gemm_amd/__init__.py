@@ -32,3 +32,18 @@ from .api import (  # noqa: F401
     empty_packed,
     packed_words,
 )
+from .serve import (  # noqa: F401
+    KV_BITS,
+    KV_HEAD_DIMS,
+    awq_gemm_grouped,
+    awq_gemm_grouped_workspace_bytes,
+    awq_kv_attention,
+    awq_kv_attention_workspace_bytes,
+    awq_kv_read,
+    awq_kv_write,
+    awq_moe_combine,
+    awq_moe_plan,
+    awq_moe_route,
+    awq_moe_workspace_bytes,
+    empty_kv_cache,
+)

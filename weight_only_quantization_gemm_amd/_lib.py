@@ -46,6 +46,23 @@ SIGNATURES = {
                                        c_vp, c_size, c_vp]),
     "awq_gemm_scaled_static": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i32, c_i32,
                                               c_vp]),
+    "awq_moe_workspace_bytes": (c_size, [c_i64, c_i32, c_i32]),
+    "awq_moe_plan": (ctypes.c_int, [c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "awq_moe_route": (ctypes.c_int, [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                     c_size, c_vp]),
+    "awq_gemm_grouped_workspace_bytes": (c_size, [c_i64, c_i64, c_i32]),
+    "awq_gemm_grouped": (ctypes.c_int, [c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32,
+                                        c_i64, c_i64, c_i32, c_i32, c_vp, c_size, c_vp]),
+    "awq_moe_combine": (ctypes.c_int, [c_vp, c_i64, c_vp, c_vp, c_i64, c_i32, c_i64, c_vp, c_vp]),
+    "awq_kv_codes_bytes": (c_size, [c_i64, c_i32, c_i32, c_i32, c_i32]),
+    "awq_kv_params_bytes": (c_size, [c_i64, c_i32, c_i32]),
+    "awq_kv_write": (ctypes.c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_i64,
+                                    c_i32, c_i32, c_vp]),
+    "awq_kv_read": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_i64, c_i32, c_i32,
+                                   c_vp]),
+    "awq_kv_attention_workspace_bytes": (c_size, [c_i64, c_i32, c_i32, c_i32, c_i64]),
+    "awq_kv_attention": (ctypes.c_int, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i32,
+                                        c_i32, c_i32, c_i64, c_i32, c_i32, ctypes.c_float, c_i64, c_vp, c_size, c_vp]),
     "awq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "awq_last_error": (ctypes.c_char_p, []),
     "awq_version": (ctypes.c_int, []),

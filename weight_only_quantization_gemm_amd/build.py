@@ -15,7 +15,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libawq.so")
 CEILINGS_LIB = os.path.join(PKG, "libawq_ceilings.so")
 
-SOURCES = ["awq_api.hip", "stats.hip", "gram.hip", "quant.hip", "loss.hip", "gemv.hip", "skinny.hip", "gemm.hip", "gemm_pipe.hip"]
+SOURCES = ["awq_api.hip", "awq_api_serve.hip", "stats.hip", "gram.hip", "quant.hip", "loss.hip", "gemv.hip", "skinny.hip",
+           "gemm.hip", "gemm_pipe.hip", "moe.hip", "grouped.hip", "kv_cache.hip", "kv_attention.hip"]
 CEILINGS_SOURCES = ["ceilings.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kv_common.h"
+
 namespace awq {
 
 constexpr int kMaxAlphas = 64;
@@ -93,6 +95,35 @@ hipError_t launch_gemv3(const void* x, const void* packed, const void* scales, c
                         int64_t M, int64_t N, int64_t K, hipStream_t st);
 hipError_t launch_gemm3(const void* x, const void* packed, const void* scales, const void* zeros, void* y,
                         int64_t M, int64_t N, int64_t K, void* ws, hipStream_t st);
+
+// moe.hip: routing, the plan of the ragged groups (counts: moe_plan_workspace bytes of scratch), the weighted sum
+hipError_t launch_moe_route(const void* logits, int bytes, int64_t T, int E, int top_k, int renorm, int32_t* experts,
+                            float* weights, hipStream_t st);
+size_t moe_plan_workspace(int64_t pairs, int E);
+hipError_t launch_moe_plan(const int32_t* experts, int64_t pairs, int E, int32_t* offsets, int32_t* rows, int32_t* pos,
+                           int32_t* counts, hipStream_t st);
+hipError_t launch_moe_combine(const void* y, int64_t R, const int32_t* pos, const float* weights, int64_t T, int top_k,
+                              int64_t N, void* out, hipStream_t st);
+
+// grouped.hip: products grouped by expert (ws: R x K halfs when s is given)
+bool gemm_grouped_fits(int64_t R, int64_t E, int64_t N);
+hipError_t launch_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
+                               const float* s, const void* packed, const void* scales, const void* zeros, void* y,
+                               int64_t R, int E, int64_t N, int64_t K, int bits, void* ws, hipStream_t st);
+
+// kv_cache.hip, kv_attention.hip: one half (keys or values) of the paged cache
+struct KvHalf {
+  uint32_t* codes;   // [pages][H][P][D * bits / 32]
+  uint32_t* params;  // [pages][H][P]: fp16 scale in the low half, fp16 zero point in the high half
+};
+hipError_t launch_kv_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                           KvHalf kc, KvHalf vc, int64_t T, int D, int bits, KvShape sh, hipStream_t st);
+hipError_t launch_kv_read(KvHalf kc, KvHalf vc, const int32_t* slots, void* k, void* v, int64_t T, int D, int bits,
+                          KvShape sh, hipStream_t st);
+size_t kv_attention_workspace(int64_t B, int64_t Hkv, int ratio, int D, int64_t max_len);
+hipError_t launch_kv_attention(const void* q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* table,
+                               int64_t width, const int32_t* lengths, int64_t B, int ratio, int D, int bits,
+                               float scale, int64_t max_len, KvShape sh, void* out, void* ws, hipStream_t st);
 
 // Dry runs of the product dispatch.  While a KernelPlan is installed on the
 // calling thread, each product launcher writes the kernel it would launch (its
