@@ -467,7 +467,7 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
  * the groups stay on the device; the result does not depend on timing.
  * Requires R, x_rows in [1, 2^24] (x_rows >= R without rows), E in
  * [1, AWQ_MAX_EXPERTS], bits 4 or 3, group == AWQ_GROUP, K % group == 0,
- * K <= 2^20.
+ * K <= 2^17.
  */
 size_t awq_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int32_t scaled);
 int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t top_k, const int32_t* offsets,

@@ -60,7 +60,7 @@ BAD = {
     "awq_moe_route": [dict(T=0), dict(E=0), dict(E=1025), dict(top_k=9), dict(top_k=0), dict(logit_bytes=8),
                       dict(renormalize=2)],
     "awq_gemm_grouped": [dict(R=0), dict(x_rows=0), dict(x_rows=9, rows=None), dict(top_k=0), dict(E=0), dict(E=1025),
-                         dict(N=0), dict(K=100), dict(group=64), dict(bits=8), dict(R=(1 << 24) + 1), dict(K=1 << 21),
+                         dict(N=0), dict(K=100), dict(group=64), dict(bits=8), dict(R=(1 << 24) + 1), dict(K=1 << 21), dict(K=(1 << 17) + 128),
                          dict(R=1 << 24, N=1 << 20, s=None)],
     "awq_moe_combine": [dict(T=0), dict(R=0), dict(top_k=0), dict(N=12), dict(N=0), dict(T=1 << 24, N=1 << 20)],
     "awq_kv_write": [dict(T=0), dict(T=(1 << 22) + 1), dict(H=0), dict(H=1025), dict(D=96), dict(page=24), dict(page=8),

@@ -37,6 +37,7 @@ FLAGS = [
 # load at each wave's start is on its critical path; gfx950 can preload the
 # arguments into SGPRs at dispatch instead.
 FILE_FLAGS = {"gemm_pipe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+              "grouped.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
               "gemv.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"],
               "skinny.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"]}
 

@@ -16,6 +16,8 @@ using awq::check_bits;
 using awq::check_layer;
 using awq::device_status;
 
+constexpr int64_t kMaxGroupedK = 1 << 17;  // a block holds its weight rows' scales and zeros in LDS
+
 int check_pairs(int64_t T, int32_t E, int32_t top_k) {
   AWQ_REQUIRE(T >= 1 && T <= (int64_t(1) << 24), AWQ_ERROR_INVALID_VALUE, "T=%lld outside [1, 2^24]", (long long)T);
   AWQ_REQUIRE(E >= 1 && E <= AWQ_MAX_EXPERTS, AWQ_ERROR_INVALID_VALUE, "E=%d outside [1, %d]", E, AWQ_MAX_EXPERTS);
@@ -100,7 +102,7 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
 }
 
 size_t awq_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int32_t scaled) {
-  if (R < 1 || R > AWQ_MAX_PAIRS || K < 1 || K > (int64_t(1) << 20) || K % AWQ_GROUP != 0 || scaled == 0) return 0;
+  if (R < 1 || R > AWQ_MAX_PAIRS || K < 1 || K > kMaxGroupedK || K % AWQ_GROUP != 0 || scaled == 0) return 0;
   return ((size_t)R * (size_t)K * 2 + 255) / 256 * 256;
 }
 
@@ -114,6 +116,7 @@ int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t
   int st = check_layer(N, K, group);
   if (st == AWQ_OK) st = check_bits(bits);
   if (st != AWQ_OK) return st;
+  AWQ_REQUIRE(K <= kMaxGroupedK, AWQ_ERROR_INVALID_VALUE, "K=%lld exceeds 2^17", (long long)K);
   AWQ_REQUIRE(R >= 1 && R <= AWQ_MAX_PAIRS, AWQ_ERROR_INVALID_VALUE, "R=%lld outside [1, 2^24]", (long long)R);
   AWQ_REQUIRE(E >= 1 && E <= AWQ_MAX_EXPERTS, AWQ_ERROR_INVALID_VALUE, "E=%d outside [1, %d]", E, AWQ_MAX_EXPERTS);
   AWQ_REQUIRE(top_k >= 1, AWQ_ERROR_INVALID_VALUE, "top_k must be >= 1 (got %d)", top_k);

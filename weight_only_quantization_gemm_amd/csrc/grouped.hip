@@ -11,12 +11,27 @@
 // scale applied in fp32, one rounding of y to fp16.
 #include "awq_common.h"
 #include "awq_internal.h"
+#include "mfma_pipe.h"
+
+#include <type_traits>
 
 namespace awq {
 
 struct RowTile {
   int expert, row, rows;  // first row of the ragged batch, rows of the tile; rows = 0: no such tile
 };
+
+// Inclusive sum over the lanes up to this one: within rows of 16 by shifts, then
+// the rows' last sums broadcast to the rows above.
+__device__ inline int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
+  return v;
+}
 
 // Tile number `tile` (of BM rows) of the ragged batch; the same in every lane.
 // Offsets are clamped to [0, R] and to order, so a tile never leaves the batch.
@@ -33,12 +48,7 @@ __device__ inline RowTile find_tile(const int32_t* __restrict__ offsets, int E, 
       n = z - a;
     }
     const int mine = (n + BM - 1) / BM;
-    int upto = mine;  // inclusive scan over the lanes
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(upto, off, kWave);
-      if (lane >= off) upto += o;
-    }
+    const int upto = wave_scan(mine);
     const uint64_t past = __ballot(upto > tile);
     if (past) {
       const int at = __ffsll((unsigned long long)past) - 1;
@@ -49,6 +59,21 @@ __device__ inline RowTile find_tile(const int32_t* __restrict__ offsets, int E, 
     tile -= __builtin_amdgcn_readlane(upto, 63);
   }
   return {0, 0, 0};
+}
+
+// Pairs 4 s .. 4 s + 3 of 32 channels' three words, as code - zero.
+template <typename Words>
+__device__ __forceinline__ f16x8 three_bit_pairs(const Words& w, int s, uint32_t bias, ZeroForms zf) {
+  f16x2 q[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int p = 4 * s + u;
+    const uint32_t bits = p < 15 ? ((w[p / 5] >> (3 * (p % 5))) & 0x00070007u)
+                                 : (((w[0] >> 15) & 0x00010001u) | ((w[1] >> 14) & 0x00020002u) |
+                                    ((w[2] >> 13) & 0x00040004u));
+    q[u] = as_f16x2(bits | bias) - zf.zb1;
+  }
+  return f16x8{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
 }
 
 // Row of x that row i of the ragged batch reads.
@@ -79,73 +104,498 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const f16* __restrict__
   }
 }
 
-// 16 rows of the batch x 16 weight rows per block; four waves take the
-// 128-channel groups in turn and are summed through LDS in a fixed order.
-constexpr int kGrpWaves = 4;
+// Bytes [at, at + len) of src into LDS, byte at + i at the returned offset + i
+// of dst: whole 16-byte pieces of src by direct loads, the rest by plain ones.
+// src is 16-byte aligned; `waves` waves share the work, and a direct load may
+// not be waited for here.
+__device__ __forceinline__ int stage_bytes(unsigned char* dst, const unsigned char* __restrict__ src, int64_t at,
+                                           int64_t len, ScaleSwizzle sw, int waves, int wave,
+                                           int lane, int tid) {
+  const int skew = (int)(at & 15);
+  src += at - skew;
+  len += skew;
+  const int64_t n16 = len / 16;
+  if (tid < len - n16 * 16) dst[n16 * 16 + tid] = src[n16 * 16 + tid];
+  __asm__ volatile("" ::: "memory");
+  for (int64_t base = (int64_t)wave * 64; base < n16; base += 64 * waves) {
+    const int64_t i = base + lane;
+    if (i < n16)
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(src + 16 * sw.piece_src(i)),
+                                       (lds_ptr_t)(dst + 16 * base), 16, 0, 0);
+  }
+  return skew;
+}
 
-template <int BITS>
-__global__ __launch_bounds__(64 * kGrpWaves) void grouped_kernel(
+// ---------------------------------------------------------------------------
+// Few rows per expert (decoding): tiles of 16 rows x 16 RW weight rows, all of K
+// per block, its 128-channel groups dealt to the block's waves in turn.  The
+// kernel is bound by reading the weights once.  A wave owns a ring of S stages
+// in LDS: a stage is one group of the weight rows (RW tiles of 16 rows x 64 or
+// 48 bytes), moved there directly, S - 1 stages ahead, with the x fragments of
+// that group in registers; the block's scales and zeros go to LDS once.  (Reading
+// them and the weights row by row into registers instead asks the L1 for 16 lines
+// per instruction, which alone takes longer than the memory.)  The waves' tiles
+// are summed through LDS in a fixed order.
+template <int BITS, int RW, int S>
+struct RingShape {
+  static constexpr int NW = BITS == 4 ? RW : (3 * RW + 3) / 4;  // 1 KB loads of a stage
+  static constexpr int STAGE = NW * 1024, LOADS = NW + 4;        // and the x fragment's four
+  // scales and zeros, each with room for the bytes before them in their first 16
+  static __host__ __device__ constexpr int scales_at(int waves) { return waves * S * STAGE; }
+  static __host__ __device__ constexpr int zeros_at(int waves, int G) {
+    return scales_at(waves) + (RW * 32 * G + 15 + 1024) / 1024 * 1024;
+  }
+  static __host__ __device__ constexpr int bytes(int waves, int G) {
+    const int ring = zeros_at(waves, G) + (RW * 16 * ((G + 1) / 2) + 15 + 1024) / 1024 * 1024;
+    const int sum = waves * 16 * (16 * RW + 1) * 4;  // the sum over the waves takes the rings' place
+    return ring > sum ? ring : sum;
+  }
+};
+
+template <int BITS, int RW, int S>
+__global__ __launch_bounds__(512) void grouped_ring_kernel(
     const f16* __restrict__ x, int64_t x_rows, const int32_t* __restrict__ rows, int top_k,
     const int32_t* __restrict__ offsets, const uint32_t* __restrict__ packed, const f16* __restrict__ scales,
-    const uint8_t* __restrict__ zeros, f16* __restrict__ y, int R, int E, int64_t N, int64_t K) {
-  __shared__ float red[kGrpWaves][16][17];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nl = lane & 15, kq = lane >> 4;
-  const int nt = (int)((N + 15) / 16), mb = (int)blockIdx.x / nt;
+    const uint8_t* __restrict__ zeros, f16* __restrict__ y, int R, int E, int64_t N, int64_t K, int nt, int waves) {
+  using Q = RingShape<BITS, RW, S>;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  const int G = (int)(K / kGroup), P2 = (G + 1) / 2;
+  const int lane = threadIdx.x & 63, nl = lane & 15, kq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mb = (int)blockIdx.x / nt;
   const RowTile tile = find_tile(offsets, E, R, mb, 16);
   if (tile.rows == 0) return;
-  const int64_t G = K / kGroup, P2 = (G + 1) / 2, W = BITS == 4 ? K / 8 : 3 * (K / 32);
-  const int64_t n0 = (int64_t)((int)blockIdx.x - mb * nt) * 16;
-  const int64_t n = (int64_t)tile.expert * N + (n0 + nl < N ? n0 + nl : N - 1);
-  const f16* xr = x + x_row(rows, tile.row + (nl < tile.rows ? nl : tile.rows - 1), top_k, x_rows) * K + kq * 32;
-  const uint32_t bias = bias_in_vgpr();
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t g = wave; g < G; g += kGrpWaves) {
-    const ZeroForms zf = zero_forms((zeros[n * P2 + (g >> 1)] >> (4 * (g & 1))) & 0xFu);
-    const float sc = (float)scales[n * G + g];
-    f32x4 d = {0.f, 0.f, 0.f, 0.f};
-    f16x8 b[4];
-    if constexpr (BITS == 4) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(packed + n * W + g * 16 + kq * 4);
+  const int64_t W = BITS == 4 ? K / 8 : 3 * (K / 32);
+  const int64_t n0 = (int64_t)((int)blockIdx.x - mb * nt) * (16 * RW), first = (int64_t)tile.expert * N + n0;
+  const int cols = N - n0 < 16 * RW ? (int)(N - n0) : 16 * RW;
+
+  // Sources of this lane's 16-byte pieces, less the group's offset.  4 bits: piece
+  // slot ^ (r / 4 % 4) of row r, so that 16 rows at one piece lie in all banks;
+  // 3 bits: rows of three pieces back to back do so by themselves.  Rows past N
+  // and past the tile repeat the last; they are never stored.
+  const uint32_t* ws[Q::NW];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) b[s] = word_minus_zero(w[s], bias, zf);
+  for (int q = 0; q < Q::NW; ++q) {
+    int r, word;
+    if (BITS == 4) {
+      r = 16 * q + (lane >> 2);
+      word = 4 * ((lane & 3) ^ ((r >> 2) & 3));
     } else {
-      const uint32_t* wp = packed + n * W + g * 12 + kq * 3;
-      const uint32_t w[3] = {wp[0], wp[1], wp[2]};
-      f16x2 q[16];
-#pragma unroll
-      for (int p = 0; p < 15; ++p) q[p] = as_f16x2(((w[p / 5] >> (3 * (p % 5))) & 0x00070007u) | bias) - zf.zb1;
-      q[15] = as_f16x2(((w[0] >> 15) & 0x00010001u) | ((w[1] >> 14) & 0x00020002u) | ((w[2] >> 13) & 0x00040004u) |
-                       bias) -
-              zf.zb1;
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        b[s] = f16x8{q[4 * s].x,     q[4 * s].y,     q[4 * s + 1].x, q[4 * s + 1].y,
-                     q[4 * s + 2].x, q[4 * s + 2].y, q[4 * s + 3].x, q[4 * s + 3].y};
+      const int pc = q * 64 + lane < 48 * RW ? q * 64 + lane : 48 * RW - 1;
+      r = pc / 3;
+      word = 4 * (pc % 3);
     }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-      d = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const f16x8*>(xr + g * kGroup + 8 * s), b[s], d, 0,
-                                                 0, 0);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] = fmaf(sc, d[r], acc[r]);
+    ws[q] = packed + (first + (r < cols ? r : cols - 1)) * W + word;
   }
+  unsigned char* ring = smem + wave * (S * Q::STAGE);
+
+  const ScaleSwizzle ssw(G);
+  unsigned char* sl = smem + Q::scales_at(waves);
+  unsigned char* zl = smem + Q::zeros_at(waves, G);
+  sl += stage_bytes(sl, reinterpret_cast<const unsigned char*>(scales), first * G * 2, (int64_t)cols * G * 2,
+                    ssw, waves, wave, lane, threadIdx.x);
+  zl += stage_bytes(zl, zeros, first * P2, (int64_t)cols * P2, ScaleSwizzle(0), waves, wave, lane, threadIdx.x);
+  const f16* xs = x + x_row(rows, tile.row + (nl < tile.rows ? nl : tile.rows - 1), top_k, x_rows) * K + kq * 32;
+  struct Fragment {
+    f16x8 a[4];
+  };
+  auto issue = [&](int g, int slot, Fragment& f) {
+    g = g < G ? g : G - 1;  // past the last group: reloaded, not used
+    unsigned char* st = ring + slot * Q::STAGE;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) red[wave][4 * kq + r][nl] = acc[r];
+    for (int q = 0; q < Q::NW; ++q)
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(ws[q] + g * (4 * BITS)), (lds_ptr_t)(st + q * 1024), 16, 0, 0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) f.a[s] = *reinterpret_cast<const f16x8*>(xs + g * kGroup + 8 * s);
+  };
+  Fragment f[S];
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) issue(wave + s * waves, s, f[s]);
+
+  int row[RW], sx[RW];
+#pragma unroll
+  for (int t = 0; t < RW; ++t) {
+    row[t] = 16 * t + nl < cols ? 16 * t + nl : cols - 1;
+    sx[t] = ssw.xor_of(row[t]);
+  }
+  const uint32_t bias = bias_in_vgpr();
+  f32x4 acc[RW];
+#pragma unroll
+  for (int t = 0; t < RW; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  wait_vmcnt<(S - 2) * Q::LOADS>();  // the scales and zeros (issued first), and the first stage
+  lds_barrier();
+  const int turns = (G + waves - 1) / waves;  // stages of this wave; the last may lie past the end
+  for (int j0 = 0; j0 < turns; j0 += S)
+#pragma unroll
+    for (int u = 0; u < S; ++u) {  // slot u
+      if (j0 + u >= turns) break;
+      const int g = wave + (j0 + u) * waves;
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads of the slot refilled now are done
+      __builtin_amdgcn_sched_barrier(0);
+      issue(g + (S - 1) * waves, (u + S - 1) % S, f[(u + S - 1) % S]);
+      wait_vmcnt<(S - 1) * Q::LOADS>();
+      __builtin_amdgcn_sched_barrier(0);
+      const unsigned char* st = ring + u * Q::STAGE;
+      const int gc = g < G ? g : G - 1;
+      uint32_t w[RW][BITS], z[RW];
+      float sc[RW];
+#pragma unroll
+      for (int t = 0; t < RW; ++t) {
+        if constexpr (BITS == 4) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(st + t * 1024 + nl * 64 + ((kq ^ ((nl >> 2) & 3)) << 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[t][i] = v[i];
+        } else {
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(st + (16 * t + nl) * 48 + kq * 12);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) w[t][i] = v[i];
+        }
+        z[t] = (zl[row[t] * P2 + (gc >> 1)] >> (4 * (gc & 1))) & 0xFu;
+        sc[t] = (float)reinterpret_cast<const f16*>(sl)[row[t] * G + (gc ^ sx[t])];
+      }
+#pragma unroll
+      for (int t = 0; t < RW; ++t) {
+        const ZeroForms zf = zero_forms(z[t]);
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          f16x8 b;
+          if constexpr (BITS == 4) b = word_minus_zero(w[t][s], bias, zf);
+          else b = three_bit_pairs(w[t], s, bias, zf);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[u].a[s], b, d, 0, 0, 0);
+        }
+        const float scale = g < G ? sc[t] : 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(scale, d[r], acc[t][r]);
+      }
+    }
+  // the rings become the place of the sum: lane holds rows 4 kq + r of column 16 t + nl
+  wait_vmcnt<0>();  // the reloads past the end have landed
   __syncthreads();
-  const int m = threadIdx.x >> 4, c = threadIdx.x & 15;
-  if (m < tile.rows && n0 + c < N) {
-    float v = 0.f;
+  constexpr int NC = 16 * RW, PITCH = NC + 1;
+  float* red = reinterpret_cast<float*>(smem);  // [waves][16][PITCH]
 #pragma unroll
-    for (int w = 0; w < kGrpWaves; ++w) v += red[w][m][c];
-    y[(int64_t)(tile.row + m) * N + n0 + c] = (f16)v;
+  for (int t = 0; t < RW; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      red[(wave * 16 + 4 * kq + r) * PITCH + 16 * t + nl] = acc[t][r];
+  __syncthreads();
+  for (int i = threadIdx.x; i < tile.rows * NC; i += waves * 64) {
+    const int m = i / NC, c = i - m * NC;
+    float v = 0.f;
+    for (int u = 0; u < waves; ++u) v += red[(u * 16 + m) * PITCH + c];
+    if (n0 + c < N) y[(int64_t)(tile.row + m) * N + n0 + c] = (f16)v;
   }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows per expert: output tiles of BM x 256 on the 32 x 32 x 16 matrix
+// instructions.  Four waves side by side along N (times WMW along M) each own
+// a 32 AB x 64 tile of it.  A stage is 64 channels (half a group): the x tile
+// (rows gathered from x, BM x 128 bytes) and the packed weights (256 rows of 32
+// or 24 bytes) go straight into an LDS ring, the tile's group scales and zeros
+// once before the loop.  A weight fragment is unpacked by the wave that uses
+// it, to the exact code - zero, and feeds AB matrix instructions; a stage's sum
+// of a 32 x 32 block enters the accumulator times the group's scale, in fp32.
+constexpr int kGBN = 256, kGXcds = 8;
+
+template <int BITS, int AB, int WMW, int STAGES>
+struct GroupedShape {
+  static constexpr int NW = 4 * WMW, BM = 32 * AB * WMW, JB = 2;
+  static constexpr int A_BYTES = BM * 128;
+  static constexpr int B_BYTES = kGBN * (BITS == 4 ? 32 : 24);
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int XL = BM / 8 / NW;                     // x loads per wave per stage (1 KB each)
+  static constexpr int WL = BITS == 4 ? B_BYTES / 1024 / NW : B_BYTES / 256 / NW;  // weight loads (1 KB / 256 B)
+  static_assert(BM % (8 * NW) == 0 && XL >= 1 && WL >= 1, "tile rows must split over the waves");
+  static constexpr int LOADS = XL + WL;
+};
+
+__host__ __device__ constexpr int64_t grouped_meta_bytes(int64_t G) {
+  return ((int64_t)kGBN * G * 2 + 31) / 16 * 16 + ((int64_t)kGBN * ((G + 1) / 2) + 31) / 16 * 16;
+}
+
+// Word w of 32 channels whose codes all are z.
+template <int BITS>
+__device__ inline uint32_t zero_word(uint32_t z, int w) {
+  if (BITS == 4) return z * 0x11111111u;
+  return z * 0x12491249u + ((z >> w) & 1u) * 0x80008000u;  // five fields in either half, then bit w of the last pair
+}
+
+template <int BITS, int AB, int WMW, int STAGES>
+__global__ __launch_bounds__(256 * WMW) void grouped_pipe_kernel(
+    const f16* __restrict__ x, int64_t x_rows, const int32_t* __restrict__ rows, int top_k,
+    const int32_t* __restrict__ offsets, const uint32_t* __restrict__ packed, const f16* __restrict__ scales,
+    const uint8_t* __restrict__ zeros, f16* __restrict__ y, int R, int E, int64_t N, int64_t K, int nt, int tiles) {
+  using S = GroupedShape<BITS, AB, WMW, STAGES>;
+  constexpr int D = STAGES - 1;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, l32 = lane & 31;
+
+  // Blocks b, b + 8, ... run on one XCD and take runs of 16 tiles, n fastest.
+  constexpr int kRun = 16;
+  const int b = (int)blockIdx.x, xcd = b % kGXcds, i = b / kGXcds;
+  const int t = (i / kRun * kGXcds + xcd) * kRun + i % kRun;
+  if (t >= tiles) return;
+  const int mb = t / nt, nb = t - mb * nt;
+  const RowTile tile = find_tile(offsets, E, R, mb, S::BM);
+  if (tile.rows == 0) return;
+
+  const int G = (int)(K / kGroup), P2 = (G + 1) / 2;
+  const int64_t W = BITS == 4 ? K / 8 : 3 * (K / 32);  // words per weight row
+  const int64_t n0 = (int64_t)nb * kGBN, e0 = (int64_t)tile.expert * N;
+  const int ncols = N - n0 < kGBN ? (int)(N - n0) : kGBN;
+
+  // this lane's source of every load of a stage (rows past the tile's end repeat its last)
+  const f16* xsrc[S::XL];
+#pragma unroll
+  for (int j = 0; j < S::XL; ++j) {
+    const int r = (wave * S::XL + j) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((r >> 1) & 7);
+    const int64_t xr = x_row(rows, tile.row + (r < tile.rows ? r : tile.rows - 1), top_k, x_rows);
+    xsrc[j] = x + xr * K + chunk * 8;
+  }
+  const uint32_t* wsrc[S::WL];
+#pragma unroll
+  for (int j = 0; j < S::WL; ++j) {
+    int r, word;
+    if (BITS == 4) {  // 32 rows of two 16-byte pieces per load
+      r = (wave * S::WL + j) * 32 + (lane >> 1);
+      word = 4 * ((lane & 1) ^ ((r >> 3) & 1));
+    } else {  // 64 words of rows of six
+      const int at = (wave * S::WL + j) * 64 + lane;
+      r = at / 6;
+      word = at - 6 * r;
+    }
+    wsrc[j] = packed + (e0 + n0 + (r < ncols ? r : ncols - 1)) * W + word;
+  }
+  const int last = 2 * G - 1;  // last stage
+  auto issue = [&](int g, int slot) {
+    g = g < last ? g : last;  // past the end: reloaded into a free slot, so every step issues the same loads
+    unsigned char* st = smem + slot * S::STAGE;
+#pragma unroll
+    for (int j = 0; j < S::XL; ++j)
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(xsrc[j] + (int64_t)g * 64),
+                                       (lds_ptr_t)(st + (wave * S::XL + j) * 1024), 16, 0, 0);
+#pragma unroll
+    for (int j = 0; j < S::WL; ++j) {
+      if constexpr (BITS == 4)
+        __builtin_amdgcn_global_load_lds((global_ptr_t)(wsrc[j] + (int64_t)g * 8),
+                                         (lds_ptr_t)(st + S::A_BYTES + (wave * S::WL + j) * 1024), 16, 0, 0);
+      else
+        __builtin_amdgcn_global_load_lds((global_ptr_t)(wsrc[j] + (int64_t)g * 6),
+                                         (lds_ptr_t)(st + S::A_BYTES + (wave * S::WL + j) * 256), 4, 0, 0);
+    }
+  };
+
+  const ScaleSwizzle ssw(G);
+  unsigned char* msc = smem + STAGES * S::STAGE;
+  unsigned char* mz = msc + ((int64_t)kGBN * G * 2 + 31) / 16 * 16;
+  msc += stage_bytes(msc, reinterpret_cast<const unsigned char*>(scales), (e0 + n0) * G * 2,
+                            (int64_t)ncols * G * 2, ssw, S::NW, wave, lane, tid);
+  mz += stage_bytes(mz, zeros, (e0 + n0) * P2, (int64_t)ncols * P2, ScaleSwizzle(0), S::NW, wave, lane, tid);
+#pragma unroll
+  for (int s = 0; s < D; ++s) issue(s, s);
+
+  int mrow[S::JB], msx[S::JB];  // staged row of the lane's weight rows, its scale xor
+#pragma unroll
+  for (int j = 0; j < S::JB; ++j) {
+    const int r = wn * 64 + j * 32 + l32;
+    mrow[j] = r < ncols ? r : ncols - 1;
+    msx[j] = ssw.xor_of(mrow[j]);
+  }
+  f32x16 acc[AB][S::JB];
+#pragma unroll
+  for (int a = 0; a < AB; ++a)
+#pragma unroll
+    for (int j = 0; j < S::JB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][j][r] = 0.f;
+  const uint32_t magic = bias_in_vgpr();
+  ZeroForms zf[S::JB];
+  uint32_t zz[S::JB];
+  bool empty[S::JB];
+  float sc[S::JB] = {1.f, 1.f};  // scale of the group the accumulators are in units of
+  const int blocks = (tile.rows + 31) / 32;  // 32-row blocks that hold a row; wave wm takes blocks wm, wm + WMW, ...
+
+  // NA: the wave's row blocks that hold a row.  Every wave loads and meets the
+  // barriers alike; which products it makes is settled outside the loop (a
+  // branch around them inside it costs the accumulators their registers).
+  auto multiply = [&](auto count) {
+  constexpr int NA = decltype(count)::value;
+  int cur = 0, nxt = D;
+  for (int g = 0; g <= last; ++g) {
+    wait_vmcnt<(D - 1) * S::LOADS>();  // stage g (and, at g = 0, the scales and zeros) has landed
+    lds_barrier();                     // for every wave; stage g - 1 is no longer read
+    issue(g + D, nxt);
+    nxt = nxt + 1 == STAGES ? 0 : nxt + 1;
+    const unsigned char* st = smem + cur * S::STAGE;
+    cur = cur + 1 == STAGES ? 0 : cur + 1;
+    const f16* At = reinterpret_cast<const f16*>(st);
+    const unsigned char* Bt = st + S::A_BYTES;
+    u32x4 wv[S::JB];
+#pragma unroll
+    for (int j = 0; j < S::JB; ++j) {
+      const int r = wn * 64 + j * 32 + l32;
+      if constexpr (BITS == 4) {
+        wv[j] = *reinterpret_cast<const u32x4*>(Bt + r * 32 + ((h ^ ((r >> 3) & 1)) << 4));
+      } else {
+        const uint32_t* wp = reinterpret_cast<const uint32_t*>(Bt) + r * 6 + h * 3;
+        wv[j] = u32x4{wp[0], wp[1], wp[2], 0u};
+      }
+    }
+    if ((g & 1) == 0) {
+      const int gr = g >> 1;
+#pragma unroll
+      for (int j = 0; j < S::JB; ++j) {
+        zz[j] = (mz[mrow[j] * P2 + (gr >> 1)] >> (4 * (gr & 1))) & 0xFu;
+        zf[j] = zero_forms(zz[j]);
+        const float was = sc[j], now = (float)reinterpret_cast<const f16*>(msc)[mrow[j] * G + (gr ^ msx[j])];
+        sc[j] = now != 0.f ? now : was;
+        empty[j] = now == 0.f;
+        const float ratio = was * __builtin_amdgcn_rcpf(sc[j]);
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[a][j][r] *= ratio;
+      }
+    }
+    // a group of scale 0 adds nothing: its codes become its zero point
+    if (__ballot(empty[0] || empty[1])) {
+#pragma unroll
+      for (int j = 0; j < S::JB; ++j)
+#pragma unroll
+        for (int w = 0; w < (BITS == 4 ? 4 : 3); ++w) wv[j][w] = empty[j] ? zero_word<BITS>(zz[j], w) : wv[j][w];
+    }
+    auto unpack = [&](int s, f16x8(&bq)[S::JB]) {
+#pragma unroll
+      for (int j = 0; j < S::JB; ++j) {
+        if constexpr (BITS == 4) bq[j] = word_minus_zero(wv[j][s], magic, zf[j]);
+        else bq[j] = three_bit_pairs(wv[j], s, magic, zf[j]);
+      }
+    };
+    f16x8 av[2][NA > 0 ? NA : 1], bq[2][S::JB];
+#pragma unroll
+    for (int a = 0; a < NA; ++a) av[0][a] = frag(At, (a * WMW + wm) * 32 + l32, 4 * h);
+    if (NA > 0) unpack(0, bq[0]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int c = s & 1, n = c ^ 1;
+      if (s < 3) {
+#pragma unroll
+        for (int a = 0; a < NA; ++a) av[n][a] = frag(At, (a * WMW + wm) * 32 + l32, 4 * h + s + 1);
+      }
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int j = 0; j < S::JB; ++j)
+          acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[c][a], bq[c][j], acc[a][j], 0, 0, 0);
+      if (s < 3 && NA > 0) unpack(s + 1, bq[n]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  };
+  const int mine = (blocks - wm + WMW - 1) / WMW;
+  if (mine >= AB) multiply(std::integral_constant<int, AB>{});
+  else if (AB > 3 && mine == 3) multiply(std::integral_constant<int, AB < 3 ? AB : 3>{});
+  else if (AB > 2 && mine == 2) multiply(std::integral_constant<int, AB < 2 ? AB : 2>{});
+  else if (AB > 1 && mine == 1) multiply(std::integral_constant<int, 1>{});
+  else multiply(std::integral_constant<int, 0>{});
+  wait_vmcnt<0>();  // the tail's reloads have landed before the block's LDS is given back
+
+  // register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+#pragma unroll
+  for (int a = 0; a < AB; ++a)
+#pragma unroll
+    for (int j = 0; j < S::JB; ++j) {
+      const int64_t n = n0 + wn * 64 + j * 32 + l32;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int m = (a * WMW + wm) * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
+        if (m < tile.rows && n < N) y[(tile.row + m) * N + n] = (f16)(acc[a][j][r] * sc[j]);
+      }
+    }
 }
 
 // The most tiles of BM rows that R rows in E groups can make.
 static int64_t row_tiles(int64_t R, int64_t E, int64_t BM) { return (R + (E < R ? E : R) * (BM - 1)) / BM; }
 
 bool gemm_grouped_fits(int64_t R, int64_t E, int64_t N) {
-  return (N + 15) / 16 * row_tiles(R, E, 16) * (64 * kGrpWaves) < (int64_t(1) << 32);  // a grid's threads
+  return (N + 15) / 16 * row_tiles(R, E, 16) < (int64_t(1) << 23);  // blocks; a grid has at most 2^32 threads
+}
+
+constexpr int64_t kGrpLds = 160 * 1024;
+
+template <int BITS, int AB, int WMW, int STAGES>
+static hipError_t pipe_stages(const f16* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
+                              const void* packed, const void* scales, const void* zeros, void* y, int64_t R, int E,
+                              int64_t N, int64_t K, hipStream_t st) {
+  using S = GroupedShape<BITS, AB, WMW, STAGES>;
+  const int64_t nt = (N + kGBN - 1) / kGBN, tiles = nt * row_tiles(R, E, S::BM);
+  const size_t lds = (size_t)(STAGES * S::STAGE + grouped_meta_bytes(K / kGroup));
+  const dim3 grid((unsigned)((tiles + 127) / 128 * 128)), block(256 * WMW);
+  grouped_pipe_kernel<BITS, AB, WMW, STAGES><<<grid, block, lds, st>>>(
+      x, x_rows, rows, top_k, offsets, reinterpret_cast<const uint32_t*>(packed), reinterpret_cast<const f16*>(scales),
+      reinterpret_cast<const uint8_t*>(zeros), reinterpret_cast<f16*>(y), (int)R, E, N, K, (int)nt, (int)tiles);
+  return hipGetLastError();
+}
+
+// Stages of the ring that leave LDS for the tile's scales and zeros (below 2: the tile cannot run).
+template <int AB, int WMW>
+static int pipe_stages_that_fit(int64_t G, int bits) {
+  const int64_t stage = bits == 4 ? GroupedShape<4, AB, WMW, 2>::STAGE : GroupedShape<3, AB, WMW, 2>::STAGE;
+  const int64_t n = (kGrpLds - grouped_meta_bytes(G)) / stage;
+  return n < 3 ? (int)n : 3;
+}
+
+template <int BITS, int AB, int WMW>
+static hipError_t pipe_launch(const f16* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
+                              const void* packed, const void* scales, const void* zeros, void* y, int64_t R, int E,
+                              int64_t N, int64_t K, hipStream_t st) {
+  if (pipe_stages_that_fit<AB, WMW>(K / kGroup, BITS) == 3)
+    return pipe_stages<BITS, AB, WMW, 3>(x, x_rows, rows, top_k, offsets, packed, scales, zeros, y, R, E, N, K, st);
+  return pipe_stages<BITS, AB, WMW, 2>(x, x_rows, rows, top_k, offsets, packed, scales, zeros, y, R, E, N, K, st);
+}
+
+template <int BITS, int RW>
+static hipError_t ring_launch(const f16* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
+                              const void* packed, const void* scales, const void* zeros, void* y, int64_t R, int E,
+                              int64_t N, int64_t K, hipStream_t st) {
+  constexpr int S = 2;  // deeper rings cost blocks per compute unit: 3 and 4 stages were 2 .. 30 % slower
+  const int G = (int)(K / kGroup);
+  const int64_t nt = (N + 16 * RW - 1) / (16 * RW), blocks = nt * row_tiles(R, E, 16);
+  // Waves per block: ten for each compute unit in all, or eight a block.  One token through 2 of 8
+  // experts of 11008 x 4096: 17.2, 14.8, 12.6, 13.1 us with 1, 2, 4, 8; 45 tokens x 6 over 64 3-bit
+  // experts of 2048 x 1408: 23.0, 23.5, 30.0, 36.7 us.
+  int waves = 1;
+  while (waves < 8 && 2 * waves <= G && blocks * waves < 2500) waves *= 2;
+  grouped_ring_kernel<BITS, RW, S><<<dim3((unsigned)blocks), dim3(64 * waves), RingShape<BITS, RW, S>::bytes(waves, G),
+                                     st>>>(
+      x, x_rows, rows, top_k, offsets, reinterpret_cast<const uint32_t*>(packed), reinterpret_cast<const f16*>(scales),
+      reinterpret_cast<const uint8_t*>(zeros), reinterpret_cast<f16*>(y), (int)R, E, N, K, (int)nt, waves);
+  return hipGetLastError();
+}
+
+// Which kernel, by the rows an expert has on average (the sizes themselves are
+// on the device).  Measured over E = 8, 16, 64 experts of 2048 x 1408 (3 bits),
+// 2048 x 2048, 11008 x 4096, 4096 x 11008 and 1000 x 4096 at 0.25 .. 700 rows an
+// expert (us):
+//   ring kernel, 4 weight tiles a wave against 2: 11.6 / 9.7, 17.4 / 15.4, 20.7 /
+//     16.3 at 0.25 rows; 28.9 / 34.5, 26.1 / 28.7 at 1; 55 / 66, 72 / 86 at 16
+//   ring against 64-row tiles: 43 / 41, 55 / 65, 50 / 101 at 8; 55 / 43, 72 / 63
+//     at 16, but 69 / 101 and 19 / 38 where 256-column tiles are fewer than the
+//     compute units (4096 x 11008, 8 experts; 1000 x 4096, 16), which at 32 is
+//     122 / 114 and 26 / 48
+//   64-row tiles against 256-row ones: 112 / 130, 154 / 180 at 128; 186 / 192,
+//     252 / 281, 346 / 273 at 256; 465 / 429, 603 / 545, 718 / 566 at 700
+enum class Kernel { ring2, ring4, rows64, rows256 };
+
+static Kernel grouped_choice(int64_t R, int64_t E, int64_t N, int64_t K, int bits) {
+  const int64_t G = K / kGroup, nt = (N + kGBN - 1) / kGBN;
+  const bool few = R <= 10 * E || (R <= 40 * E && nt * E < 256);
+  if (!few && R >= 384 * E && pipe_stages_that_fit<4, 2>(G, bits) >= 2) return Kernel::rows256;
+  if (!few && pipe_stages_that_fit<2, 1>(G, bits) >= 2) return Kernel::rows64;
+  return R > E && RingShape<4, 4, 2>::bytes(8, (int)G) <= kGrpLds ? Kernel::ring4 : Kernel::ring2;
 }
 
 hipError_t launch_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
@@ -160,16 +610,17 @@ hipError_t launch_gemm_grouped(const void* x, int64_t x_rows, const int32_t* row
     x_rows = R;
     rows = nullptr;
   }
-  const dim3 grid((unsigned)((N + 15) / 16 * row_tiles(R, E, 16))), block(64 * kGrpWaves);
-  auto pp = reinterpret_cast<const uint32_t*>(packed);
-  auto sp = reinterpret_cast<const f16*>(scales);
-  auto zp = reinterpret_cast<const uint8_t*>(zeros);
-  auto yp = reinterpret_cast<f16*>(y);
-  if (bits == 4)
-    grouped_kernel<4><<<grid, block, 0, st>>>(xp, x_rows, rows, top_k, offsets, pp, sp, zp, yp, (int)R, E, N, K);
-  else
-    grouped_kernel<3><<<grid, block, 0, st>>>(xp, x_rows, rows, top_k, offsets, pp, sp, zp, yp, (int)R, E, N, K);
-  return hipGetLastError();
+#define AWQ_GROUPED(launch, ...)                                                                          \
+  return bits == 4 ? launch<4, __VA_ARGS__>(xp, x_rows, rows, top_k, offsets, packed, scales, zeros, y, R, E, N, K, st) \
+                   : launch<3, __VA_ARGS__>(xp, x_rows, rows, top_k, offsets, packed, scales, zeros, y, R, E, N, K, st)
+  switch (grouped_choice(R, E, N, K, bits)) {
+    case Kernel::ring2: AWQ_GROUPED(ring_launch, 2);
+    case Kernel::ring4: AWQ_GROUPED(ring_launch, 4);
+    case Kernel::rows64: AWQ_GROUPED(pipe_launch, 2, 1);
+    case Kernel::rows256: AWQ_GROUPED(pipe_launch, 4, 2);
+  }
+#undef AWQ_GROUPED
+  return hipErrorInvalidValue;
 }
 
 }  // namespace awq
