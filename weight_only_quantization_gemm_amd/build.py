@@ -38,6 +38,7 @@ FLAGS = [
 # arguments into SGPRs at dispatch instead.
 FILE_FLAGS = {"gemm_pipe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
               "grouped.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+              "kv_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
               "gemv.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"],
               "skinny.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"]}
 

@@ -53,7 +53,7 @@ extern "C" {
 size_t awq_moe_workspace_bytes(int64_t T, int32_t E, int32_t top_k) {
   if (T < 1 || E < 1 || E > AWQ_MAX_EXPERTS || top_k < 1 || top_k > 64 || T > AWQ_MAX_PAIRS || T * top_k > AWQ_MAX_PAIRS)
     return 0;
-  return (awq::moe_plan_workspace(T * top_k, E) + 255) / 256 * 256;
+  return (awq::moe_plan_workspace(T * top_k, E, top_k) + 255) / 256 * 256;
 }
 
 int awq_moe_plan(const int32_t* experts, int64_t T, int32_t E, int32_t top_k, int32_t* offsets, int32_t* rows,
@@ -68,7 +68,7 @@ int awq_moe_plan(const int32_t* experts, int64_t T, int32_t E, int32_t top_k, in
   const size_t need = awq_moe_workspace_bytes(T, E, top_k);
   AWQ_REQUIRE(workspace_bytes >= need, AWQ_ERROR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes,
               need);
-  return device_status(awq::launch_moe_plan(experts, T * top_k, E, offsets, rows, pos,
+  return device_status(awq::launch_moe_plan(experts, T, E, top_k, offsets, rows, pos,
                                             reinterpret_cast<int32_t*>(workspace), as_stream(stream)),
                        "awq_moe_plan");
   AWQ_GUARD_END
@@ -92,12 +92,9 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
   const size_t need = awq_moe_workspace_bytes(T, E, top_k);
   AWQ_REQUIRE(workspace_bytes >= need, AWQ_ERROR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes,
               need);
-  hipError_t e = awq::launch_moe_route(logits, logit_bytes, T, E, top_k, renormalize, experts, weights,
-                                       as_stream(stream));
-  if (e == hipSuccess)
-    e = awq::launch_moe_plan(experts, T * top_k, E, offsets, rows, pos, reinterpret_cast<int32_t*>(workspace),
-                             as_stream(stream));
-  return device_status(e, "awq_moe_route");
+  return device_status(awq::launch_moe_route(logits, logit_bytes, T, E, top_k, renormalize, experts, weights, offsets,
+                                             rows, pos, reinterpret_cast<int32_t*>(workspace), as_stream(stream)),
+                       "awq_moe_route");
   AWQ_GUARD_END
 }
 

@@ -96,12 +96,13 @@ hipError_t launch_gemv3(const void* x, const void* packed, const void* scales, c
 hipError_t launch_gemm3(const void* x, const void* packed, const void* scales, const void* zeros, void* y,
                         int64_t M, int64_t N, int64_t K, void* ws, hipStream_t st);
 
-// moe.hip: routing, the plan of the ragged groups (counts: moe_plan_workspace bytes of scratch), the weighted sum
+// moe.hip: routing, the plan of the ragged groups (ws: moe_plan_workspace bytes of scratch), the weighted sum
+size_t moe_plan_workspace(int64_t pairs, int E, int top_k);
 hipError_t launch_moe_route(const void* logits, int bytes, int64_t T, int E, int top_k, int renorm, int32_t* experts,
-                            float* weights, hipStream_t st);
-size_t moe_plan_workspace(int64_t pairs, int E);
-hipError_t launch_moe_plan(const int32_t* experts, int64_t pairs, int E, int32_t* offsets, int32_t* rows, int32_t* pos,
-                           int32_t* counts, hipStream_t st);
+                            float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, int32_t* ws,
+                            hipStream_t st);
+hipError_t launch_moe_plan(const int32_t* experts, int64_t T, int E, int top_k, int32_t* offsets, int32_t* rows,
+                           int32_t* pos, int32_t* ws, hipStream_t st);
 hipError_t launch_moe_combine(const void* y, int64_t R, const int32_t* pos, const float* weights, int64_t T, int top_k,
                               int64_t N, void* out, hipStream_t st);
 

@@ -29,7 +29,9 @@
 #include "awq_common.h"
 #include "awq_internal.h"
 #include "kv_common.h"
+#include "mfma_pipe.h"
 
+#include <cstdlib>
 namespace awq {
 
 constexpr int kAttWaves = 4;
@@ -37,6 +39,8 @@ constexpr int kAttStep = 32;       // tokens a wave takes at a time
 constexpr int kAttHeads = 16;      // query heads of a block: columns of a product
 constexpr float kSlack = 8.f;      // a score may pass the running maximum by this (log2) before all is rescaled
 constexpr float kTwo24 = 16777216.f;
+constexpr int kNonTemporal = 2;    // cache policy of the code loads: every line is used once (54 against 61 us on long sequences)
+constexpr int kAttWindows = 4;     // 64-tile runs of the pages of a chunk: 4096 tokens at most
 
 // Channel of the cache row that product row n of tile c of the output stands for.
 template <int D, int BITS>
@@ -55,13 +59,20 @@ __host__ __device__ constexpr bool att_times16(int c) {
 
 __device__ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); }
 
+// A stage of a wave's ring: 32 tokens' keys, values and parameters, moved
+// straight into LDS.  Keys: rows of RB bytes, piece c (16 bytes) of row r in slot
+// c ^ f(r), so that 16 rows at one piece lie in all banks.  Values: within a
+// tile of 16, token 4 b + j in row 4 j + b, so that one read of the four lane
+// groups b is contiguous.  Parameters: keys' of 32 tokens, then values'.
 template <int D, int BITS>
-struct AttStep {
-  static constexpr int KW = D * BITS / 128;              // words of a lane's K row quarter
-  static constexpr int VW = D * BITS / 512 > 0 ? D * BITS / 512 : 1;  // words of a lane's channels of a V row
-  uint32_t k[2][KW];
-  uint32_t v[8][VW];
-  u32x4 kp[2], vp[2];
+struct AttStage {
+  static constexpr int RB = D * BITS / 8, PIECES = RB / 16;
+  static constexpr int HALF = kAttStep * RB, NI = HALF / 1024;  // bytes, 1 KB loads of keys (and of values)
+  static constexpr int BYTES = 2 * HALF + 256, LOADS = 2 * NI + 1;
+  static constexpr int KW = RB / 16;                     // words of a lane's quarter of a key row
+  static constexpr int S = 2;                            // stages of a ring
+  static constexpr int RING = S * BYTES;
+  static __host__ __device__ constexpr int slot_xor(int r) { return (r / (256 / RB)) & (PIECES - 1); }
 };
 
 template <int D, int BITS>
@@ -69,8 +80,8 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
     const f16* __restrict__ q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* __restrict__ table, int width,
     const int32_t* __restrict__ lengths, int64_t max_len, KvShape sh, int ratio, float scale_log2, int chunk,
     int chunks, f16* __restrict__ out, float* __restrict__ part_o, float* __restrict__ part_ml) {
-  constexpr int W = D * BITS / 32, TILES = D / 16;
-  using Step = AttStep<D, BITS>;
+  using A = AttStage<D, BITS>;
+  constexpr int TILES = D / 16, RB = A::RB;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
 
   const int lane = threadIdx.x & 63, n = lane & 15, b = lane >> 4;
@@ -81,161 +92,180 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
   const int heads = ratio - h0 < kAttHeads ? ratio - h0 : kAttHeads;  // query heads of this block
   const int Hq = sh.heads * ratio;
 
-  const int64_t len = kv_length(sh, lengths[seq], width, max_len);
+  // Pages of the chunk: lane i of window k holds that of the chunk's tile 64 k + i
+  // of 16 tokens, -1 where there is none.  The entries are fetched along with the
+  // length, those past it too (within the table's row), and dropped afterwards.
   const int64_t t0 = (int64_t)blockIdx.y * chunk;
+  int page_of[kAttWindows];
+#pragma unroll
+  for (int k = 0; k < kAttWindows; ++k) {
+    const int t = 16 * (64 * k + lane);
+    const int64_t entry = (t0 + t) >> sh.ps;
+    page_of[k] = t < chunk && entry < width ? table[(int64_t)seq * width + entry] : -1;
+  }
+  const int64_t len = kv_length(sh, lengths[seq], width, max_len);
   if (t0 >= len && blockIdx.y > 0) return;  // the first chunk of an empty sequence stores its zeros
   const int count = (int)(len - t0 < chunk ? (len - t0 > 0 ? len - t0 : 0) : chunk);
+#pragma unroll
+  for (int k = 0; k < kAttWindows; ++k) page_of[k] = 16 * (64 * k + lane) < count ? kv_page(sh, page_of[k]) : -1;
+  auto page = [&](int tile) {
+    int p = __builtin_amdgcn_readlane(page_of[0], tile & 63);
+#pragma unroll
+    for (int k = 1; k < kAttWindows; ++k) p = tile >> 6 == k ? __builtin_amdgcn_readlane(page_of[k], tile & 63) : p;
+    return p;
+  };
 
-  // Pages of the chunk: lane i holds that of the chunk's tokens 16 i .. 16 i + 15
-  // (a chunk has at most 64 such tiles), -1 where there is none.
-  int page_of = -1;
-  if (16 * lane < count) page_of = kv_page(sh, table[(int64_t)seq * width + ((t0 + 16 * lane) >> sh.ps)]);
+  unsigned char* ring = smem + wave * A::RING;
+  auto issue = [&](int i, int slot) {
+    unsigned char* st = ring + slot * A::BYTES;
+    int64_t row[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) row[u] = kv_tile_row(sh, page(2 * i + u), t0 + 16 * (2 * i + u), hk);
+#pragma unroll
+    for (int k = 0; k < A::NI; ++k) {
+      const int r = (k * 64 + lane) / A::PIECES, slot_of = lane % A::PIECES;  // row of the step, 16-byte slot
+      const int64_t base = RB == 32 ? (lane < 32 ? row[0] : row[1]) : row[k * 1024 / RB / 16];
+      const int tr = r & 15;
+      const unsigned char* ks = reinterpret_cast<const unsigned char*>(kc.codes) + base * RB;
+      const unsigned char* vs = reinterpret_cast<const unsigned char*>(vc.codes) + base * RB;
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(ks + tr * RB + ((slot_of ^ A::slot_xor(tr)) << 4)),
+                                       (lds_ptr_t)(st + k * 1024), 16, 0, kNonTemporal);
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(vs + (4 * (tr & 3) + (tr >> 2)) * RB + (slot_of << 4)),
+                                       (lds_ptr_t)(st + A::HALF + k * 1024), 16, 0, kNonTemporal);
+    }
+    const uint32_t* ps = (lane < 32 ? kc.params : vc.params) + (lane & 16 ? row[1] : row[0]) + n;
+    __builtin_amdgcn_global_load_lds((global_ptr_t)ps, (lds_ptr_t)(st + 2 * A::HALF), 4, 0, 0);
+  };
+  const int steps = (count + kAttStep - 1) / kAttStep;
+  const int turns = steps > wave ? (steps - wave + kAttWaves - 1) / kAttWaves : 0;
+#pragma unroll
+  for (int s = 0; s < A::S - 1; ++s)
+    if (s < turns) issue(wave + s * kAttWaves, s);
 
-  // q: columns past the block's heads repeat the last one and are never stored
+  // q: columns past the block's heads repeat the last one and are never stored.  A negative
+  // factor goes to q's sign, so that larger sums are larger scores; one of 0 is taken as
+  // 2^-100, which leaves a masked score (-infinity) what it is.
+  const float factor = fmaxf(fabsf(scale_log2) * kTwo24, 7.888609e-31f);
   const int hn = n < heads ? n : heads - 1;
   const f16* qrow = q + seq * q_stride + (int64_t)(hk * ratio + h0 + hn) * D;
   f16x8 qf[D / 32];
-  float qsum = 0.f;
+  float qz = 0.f;
 #pragma unroll
   for (int s = 0; s < D / 32; ++s) {
-    const f16x8 x = *reinterpret_cast<const f16x8*>(qrow + b * (D / 4) + 8 * s);
+    f16x8 x = *reinterpret_cast<const f16x8*>(qrow + b * (D / 4) + 8 * s);
+    if (scale_log2 < 0.f) x = -x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) qsum += (float)x[j];
+    for (int j = 0; j < 8; ++j) qz += (float)x[j];
     const f16 t = (f16)0.0625f;
     if (BITS == 4) qf[s] = f16x8{x[0], x[1], x[2] * t, x[3] * t, x[4], x[5], x[6] * t, x[7] * t};
     else qf[s] = f16x8{x[0], x[2], x[1], x[3], x[4], x[6], x[5], x[7]};
   }
-  qsum += __shfl_xor(qsum, 16, kWave);
-  qsum += __shfl_xor(qsum, 32, kWave);
-  const float qz = qsum * (1.f / kTwo24);
-  const float sfac = scale_log2 * kTwo24;
+  qz += __shfl_xor(qz, 16, kWave);
+  qz += __shfl_xor(qz, 32, kWave);
+  qz *= -1.f / kTwo24;
 
+  // Weights are kept as 2^(factor x - ref), ref following the largest score less
+  // the exponent F that brings the largest value scale to 2^6 .. 2^7: a weight
+  // times a value scale then uses fp16's range from the top.
   f32x4 o[TILES], oz = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < TILES; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
-  float F = 0.f;  // power of two that brings the largest scale seen so far to 2^6 .. 2^7; 0: none seen
+  float ref = 0.f, l = 0.f;
+  float top_seen = -INFINITY, limit = -INFINITY;  // largest sum seen; the one past which ref has to move
+  float wide_limit = 0.f;                         // largest value scale that F allows for
+  int F = 0;
 
-  const int steps = (count + kAttStep - 1) / kAttStep;
-  auto load = [&](int i, Step& st) {
+  auto compute = [&](int i, const unsigned char* st) {
+    float s[8];
+    uint32_t vp[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int tile = 2 * i + u;
-      const int64_t row = kv_tile_row(sh, __builtin_amdgcn_readlane(page_of, tile & 63), t0 + 16 * tile, hk);
-      const uint32_t* ks = kc.codes + row * W + n * W + b * Step::KW;
-      if constexpr (Step::KW == 2) {
-        const u32x2 x = *reinterpret_cast<const u32x2*>(ks);
-        st.k[u][0] = x.x;
-        st.k[u][1] = x.y;
+      const u32x4 kp = *reinterpret_cast<const u32x4*>(st + 2 * A::HALF + u * 64 + b * 16);
+      const u32x4 vq = *reinterpret_cast<const u32x4*>(st + 2 * A::HALF + 128 + u * 64 + b * 16);
+      uint32_t w[A::KW];
+      if constexpr (A::KW == 2) {
+        const int at = n * RB + b * 8;  // the lane's half of piece b / 2
+        const u32x2 x = *reinterpret_cast<const u32x2*>(st + u * 16 * RB + (at ^ (A::slot_xor(n) << 4)));
+        w[0] = x.x;
+        w[1] = x.y;
       } else {
 #pragma unroll
-        for (int j = 0; j < Step::KW / 4; ++j) {
-          const u32x4 x = reinterpret_cast<const u32x4*>(ks)[j];
+        for (int j = 0; j < A::KW / 4; ++j) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(
+              st + u * 16 * RB + n * RB + (((b * (A::KW / 4) + j) ^ A::slot_xor(n)) << 4));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) st.k[u][4 * j + e] = x[e];
+          for (int e = 0; e < 4; ++e) w[4 * j + e] = x[e];
         }
       }
-      const uint32_t* vs = vc.codes + (row + 4 * b) * W;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = 4 * u + j;
-        if constexpr (D * BITS == 256) {
-          st.v[at][0] = reinterpret_cast<const uint16_t*>(vs + j * W)[n];
-        } else if constexpr (Step::VW == 1) {
-          st.v[at][0] = (vs + j * W)[n];
-        } else if constexpr (Step::VW == 2) {
-          const u32x2 x = reinterpret_cast<const u32x2*>(vs + j * W)[n];
-          st.v[at][0] = x.x;
-          st.v[at][1] = x.y;
-        } else {
-          const u32x4 x = reinterpret_cast<const u32x4*>(vs + j * W)[n];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) st.v[at][e] = x[e];
-        }
-      }
-      st.kp[u] = *reinterpret_cast<const u32x4*>(kc.params + row + 4 * b);
-      st.vp[u] = *reinterpret_cast<const u32x4*>(vc.params + row + 4 * b);
-    }
-  };
-
-  auto compute = [&](int i, Step& st) {
-    // tokens past the chunk's end or of a page that is none: no score, scale and zero point 0
-    bool live[8];
-    const bool page0 = __builtin_amdgcn_readlane(page_of, (2 * i) & 63) >= 0;
-    const bool page1 = __builtin_amdgcn_readlane(page_of, (2 * i + 1) & 63) >= 0;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        live[4 * u + r] = (u ? page1 : page0) && kAttStep * i + 16 * u + 4 * b + r < count;
-
-    float s[8];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
         u32x4 a;
         if (BITS == 4) {
-          const uint32_t w = st.k[u][t], w8 = w >> 8;
-          a = u32x4{w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
+          const uint32_t w8 = w[t] >> 8;
+          a = u32x4{w[t] & 0x000F000Fu, w[t] & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
         } else {
-          const uint32_t w0 = st.k[u][2 * t], w1 = st.k[u][2 * t + 1];
-          a = u32x4{w0 & 0x00FF00FFu, (w0 >> 8) & 0x00FF00FFu, w1 & 0x00FF00FFu, (w1 >> 8) & 0x00FF00FFu};
+          a = u32x4{w[2 * t] & 0x00FF00FFu, (w[2 * t] >> 8) & 0x00FF00FFu, w[2 * t + 1] & 0x00FF00FFu,
+                    (w[2 * t + 1] >> 8) & 0x00FF00FFu};
         }
         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), qf[t], acc, 0, 0, 0);
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const f16x2 p = as_f16x2(st.kp[u][r]);
-        const float x = fmaf(-(float)p.y, qz, acc[r]) * ((float)p.x * sfac);
-        s[4 * u + r] = live[4 * u + r] ? x : -INFINITY;
+        const f16x2 p = as_f16x2(kp[r]);
+        s[4 * u + r] = fmaf((float)p.y, qz, acc[r]) * (float)p.x;
+        vp[4 * u + r] = vq[r];
       }
     }
-    float vscale[8];
-    float top = s[0], wide = 0.f;
-    uint32_t vz[8];
+    // tokens past the chunk's end or of a page that is none: no score, value scale and zero point 0
+    const bool page0 = page(2 * i) >= 0, page1 = page(2 * i + 1) >= 0;
+    if (!page0 || !page1 || kAttStep * (i + 1) > count) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool live = (j < 4 ? page0 : page1) && kAttStep * i + 16 * (j >> 2) + 4 * b + (j & 3) < count;
+        s[j] = live ? s[j] : -INFINITY;
+        vp[j] = live ? vp[j] : 0u;
+      }
+    }
+    float vscale[8], top = s[0], wide = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t p = live[j] ? st.vp[j >> 2][j & 3] : 0u;
-      vscale[j] = (float)as_f16x2(p).x;
-      vz[j] = p;
+      vscale[j] = (float)as_f16x2(vp[j]).x;
       top = fmaxf(top, s[j]);
       wide = fmaxf(wide, vscale[j]);
     }
-    // rarely: a new maximum or a larger scale; every lane then rescales what it holds
-    if (__ballot((top > m + kSlack) || (wide * F > 128.f) || (wide > 0.f && F == 0.f))) {
+    // rarely: a new maximum or a larger value scale; every lane then rescales what it holds
+    if (__ballot(top > limit || wide > wide_limit)) {
       top = fmaxf(top, __shfl_xor(top, 16, kWave));
       top = fmaxf(top, __shfl_xor(top, 32, kWave));
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) wide = fmaxf(wide, __shfl_xor(wide, off, kWave));
-      const float m2 = fmaxf(m, top);
-      const float alpha = m == m2 ? 1.f : exp2f(m - m2);  // m = -inf: 0
-      m = m2;
-      float f2 = F;
-      if (wide > 0.f) {
+      const bool first = top_seen == -INFINITY;
+      top_seen = fmaxf(top_seen, top);
+      limit = top_seen == -INFINITY ? -INFINITY : top_seen + kSlack / factor;
+      if (wide > wide_limit) {
         int e;
         frexpf(wide, &e);  // wide in [2^(e - 1), 2^e)
-        const float fw = ldexpf(1.f, 7 - e);
-        f2 = F == 0.f ? fw : fminf(F, fw);
+        F = 7 - e;
+        wide_limit = ldexpf(1.f, e);
       }
-      const float beta = F == 0.f ? alpha : alpha * (f2 / F);
-      F = f2;
+      const float now = top_seen == -INFINITY ? 0.f : fmaf(top_seen, factor, -(float)F);
+      const float alpha = first ? 0.f : exp2f(ref - now);
+      ref = now;
       l *= alpha;
 #pragma unroll
       for (int c = 0; c < TILES; ++c)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[c][r] *= beta;
+        for (int r = 0; r < 4; ++r) o[c][r] *= alpha;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) oz[r] *= beta;
+      for (int r = 0; r < 4; ++r) oz[r] *= alpha;
     }
-    const float mm = m == -INFINITY ? 0.f : m;
     f16x8 whi, wlo;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float p = __builtin_amdgcn_exp2f(s[j] - mm);
+      const float p = __builtin_amdgcn_exp2f(fmaf(s[j], factor, -ref));
       l += p;
-      const float w = p * (vscale[j] * F);
+      const float w = p * vscale[j];
       whi[j] = (f16)w;
       wlo[j] = (f16)(w - (float)whi[j]);
     }
@@ -247,16 +277,35 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
     {
       u32x4 a;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = perm(vz[2 * j + 1], vz[2 * j], 0x07060302u);  // the upper halves
+      for (int j = 0; j < 4; ++j) a[j] = perm(vp[2 * j + 1], vp[2 * j], 0x07060302u);  // the zero points
       mac(a, oz);
+    }
+    constexpr int LB = RB / 16;  // bytes of a lane's channels of a value row: 2, 4, 8 or 16
+    uint32_t v[8][LB < 4 ? 1 : LB / 4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const unsigned char* src = st + A::HALF + (16 * (j >> 2) + 4 * (j & 3) + b) * RB + n * LB;
+      if constexpr (LB == 2) {
+        v[j][0] = *reinterpret_cast<const uint16_t*>(src);
+      } else if constexpr (LB == 4) {
+        v[j][0] = *reinterpret_cast<const uint32_t*>(src);
+      } else if constexpr (LB == 8) {
+        const u32x2 x = *reinterpret_cast<const u32x2*>(src);
+        v[j][0] = x.x;
+        v[j][1] = x.y;
+      } else {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(src);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][e] = x[e];
+      }
     }
     if constexpr (BITS == 4) {
 #pragma unroll
-      for (int g = 0; g < (D * BITS == 256 ? 1 : 2 * Step::VW); ++g) {  // halves of the lane's words
+      for (int g = 0; g < TILES / 4; ++g) {  // halves of the lane's words
         u32x4 x, x8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[j] = perm(st.v[2 * j + 1][g / 2], st.v[2 * j][g / 2], g % 2 ? 0x07060302u : 0x05040100u);
+          x[j] = perm(v[2 * j + 1][g / 2], v[2 * j][g / 2], g % 2 ? 0x07060302u : 0x05040100u);
           x8[j] = x[j] >> 8;
         }
         mac(x & 0x000F000Fu, o[4 * g]);
@@ -270,84 +319,132 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
         u32x4 a;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          a[j] = perm(st.v[2 * j + 1][c / 4], st.v[2 * j][c / 4], 0x0C040C00u + 0x00010001u * (c % 4));
+          a[j] = perm(v[2 * j + 1][c / 4], v[2 * j][c / 4], 0x0C040C00u + 0x00010001u * (c % 4));
         mac(a, o[c]);
       }
     }
   };
 
-  Step cur;
-  for (int i = wave; i < steps; i += kAttWaves) {
-    load(i, cur);
-    compute(i, cur);
+  int cur = 0, nxt = A::S - 1;
+  for (int j = 0; j < turns; ++j) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads of the slot refilled now are done
+    __builtin_amdgcn_sched_barrier(0);
+    const int i = wave + j * kAttWaves;
+    if (j + A::S - 1 < turns) {
+      issue(i + (A::S - 1) * kAttWaves, nxt);
+      nxt = nxt + 1 == A::S ? 0 : nxt + 1;
+      wait_vmcnt<(A::S - 1) * A::LOADS>();
+    } else if (A::S == 3 && j + 1 < turns) {
+      wait_vmcnt<A::LOADS>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    compute(i, ring + cur * A::BYTES);
+    cur = cur + 1 == A::S ? 0 : cur + 1;
   }
+  __syncthreads();  // the rings become the place of the sum
 
-  // join the waves: largest maximum, then the sums in the order of the waves
+  // Join the waves: each output in LDS [wave][head][D], then its share of the sum,
+  // 2^(ref - largest ref), and the sums in the order of the waves.
   l += __shfl_xor(l, 16, kWave);
   l += __shfl_xor(l, 32, kWave);
-  float* red_o = reinterpret_cast<float*>(smem);               // [waves][heads][D]
-  float* red_m = red_o + kAttWaves * heads * D;                // [waves][16]
+  float* red_o = reinterpret_cast<float*>(smem);
+  float* red_m = red_o + kAttWaves * heads * D;  // [wave][16]
   float* red_l = red_m + kAttWaves * kAttHeads;
+  float* share = red_l + kAttWaves * kAttHeads;  // [wave][16], then the head's sum [16]
   if (b == 0) {
-    red_m[wave * kAttHeads + n] = m;
+    red_m[wave * kAttHeads + n] = top_seen == -INFINITY ? -INFINITY : ref;
     red_l[wave * kAttHeads + n] = l;
   }
   if (n < heads) {
-    const float back = F > 0.f ? 1.f / F : 0.f;
 #pragma unroll
     for (int c = 0; c < TILES; ++c)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         red_o[(wave * heads + n) * D + att_channel<D, BITS>(4 * b + r, c)] =
-            (o[c][r] * (att_times16<BITS>(c) ? kTwo24 / 16.f : kTwo24) - oz[r]) * back;
+            o[c][r] * (att_times16<BITS>(c) ? kTwo24 / 16.f : kTwo24) - oz[r];
   }
   __syncthreads();
   const bool whole = len <= chunk;  // the sequence's only chunk: store the result itself
-  for (int i = threadIdx.x; i < heads * D; i += 64 * kAttWaves) {
-    const int h = i / D, d = i - h * D;
-    float mx = -INFINITY;
+  const int64_t head0 = (int64_t)seq * Hq + hk * ratio + h0;
+  if (threadIdx.x < kAttHeads) {
+    float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAttWaves; ++w) mx = fmaxf(mx, red_m[w * kAttHeads + h]);
-    float sum = 0.f, acc = 0.f;
+    for (int w = 0; w < kAttWaves; ++w) mx = fmaxf(mx, red_m[w * kAttHeads + n]);
 #pragma unroll
     for (int w = 0; w < kAttWaves; ++w) {
-      const float mw = red_m[w * kAttHeads + h];
+      const float mw = red_m[w * kAttHeads + n];
       const float f = mw == -INFINITY ? 0.f : exp2f(mw - mx);
-      sum += f * red_l[w * kAttHeads + h];
-      acc = fmaf(f, red_o[(w * heads + h) * D + d], acc);
+      share[w * kAttHeads + n] = f;
+      sum = fmaf(f, red_l[w * kAttHeads + n], sum);
     }
-    const int64_t head = (int64_t)seq * Hq + hk * ratio + h0 + h;
+    share[kAttWaves * kAttHeads + n] = sum > 0.f ? 1.f / sum : 0.f;
+    if (!whole && n < heads) {
+      const int64_t at = (head0 + n) * chunks + blockIdx.y;
+      part_ml[2 * at] = mx;
+      part_ml[2 * at + 1] = sum;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * D / 4; i += 64 * kAttWaves) {
+    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kAttWaves; ++w) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(red_o + (w * heads + h) * D + d);
+      const float f = share[w * kAttHeads + h];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+    }
     if (whole) {
-      out[head * D + d] = (f16)(sum > 0.f ? acc / sum : 0.f);
+      const float f = share[kAttWaves * kAttHeads + h];
+      *reinterpret_cast<u32x2*>(out + (head0 + h) * D + d) =
+          u32x2{as_u32(f16x2{(f16)(acc[0] * f), (f16)(acc[1] * f)}), as_u32(f16x2{(f16)(acc[2] * f), (f16)(acc[3] * f)})};
     } else {
-      const int64_t at = head * chunks + blockIdx.y;
-      part_o[at * D + d] = acc;
-      if (d == 0) {
-        part_ml[2 * at] = mx;
-        part_ml[2 * at + 1] = sum;
-      }
+      *reinterpret_cast<f32x4*>(part_o + ((head0 + h) * chunks + blockIdx.y) * D + d) = acc;
     }
   }
 }
 
-// Joins the chunks of one query head of one sequence: D threads.
-__global__ void kv_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml,
-                               const int32_t* __restrict__ lengths, int64_t max_len, int width, KvShape sh, int Hq,
-                               int chunk, int chunks, f16* __restrict__ out) {
+// Joins the chunks of one query head of one sequence: D x parts threads, part p
+// taking chunks p, p + parts, ...; the parts are summed in order.
+__global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__ part_o,
+                                                       const float* __restrict__ part_ml,
+                                                       const int32_t* __restrict__ lengths, int64_t max_len, int width,
+                                                       KvShape sh, int Hq, int chunk, int chunks,
+                                                       f16* __restrict__ out) {
+  __shared__ float red[2 * 1024], top[16];
   const int64_t head = blockIdx.x;
-  const int D = (int)blockDim.x, d = (int)threadIdx.x;
+  const int D = (int)blockDim.x, d = (int)threadIdx.x, part = (int)threadIdx.y, parts = (int)blockDim.y;
   const int64_t len = kv_length(sh, lengths[head / Hq], width, max_len);
   if (len <= chunk) return;  // stored by its only block
   const int used = (int)((len + chunk - 1) / chunk);
   const float* ml = part_ml + head * chunks * 2;
   const float* po = part_o + head * chunks * D + d;
+  const int tid = part * D + d, threads = parts * D;
   float mx = -INFINITY;
-  for (int c = 0; c < used; ++c) mx = fmaxf(mx, ml[2 * c]);
+  for (int c = tid; c < used; c += threads) mx = fmaxf(mx, ml[2 * c]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, kWave));
+  if ((tid & 63) == 0) top[tid >> 6] = mx;
+  __syncthreads();
+  for (int w = 0; w < threads / 64; ++w) mx = fmaxf(mx, top[w]);
   float sum = 0.f, acc = 0.f;
-  for (int c = 0; c < used; ++c) {
-    const float f = ml[2 * c] == -INFINITY ? 0.f : exp2f(ml[2 * c] - mx);
+#pragma unroll 4
+  for (int c = part; c < used; c += parts) {
+    const float m = ml[2 * c];
+    const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
     sum = fmaf(f, ml[2 * c + 1], sum);
     acc = fmaf(f, po[(int64_t)c * D], acc);
+  }
+  red[2 * tid] = acc;
+  red[2 * tid + 1] = sum;
+  __syncthreads();
+  if (part > 0) return;
+  for (int p = 1; p < parts; ++p) {
+    acc += red[2 * (p * D + d)];
+    sum += red[2 * (p * D + d) + 1];
   }
   out[head * D + d] = (f16)(sum > 0.f ? acc / sum : 0.f);
 }
@@ -358,7 +455,8 @@ __global__ void kv_join_kernel(const float* __restrict__ part_o, const float* __
 static int att_chunk(int64_t B, int64_t Hkv, int ratio, int64_t max_len) {
   const int64_t rows = B * Hkv * ((ratio + kAttHeads - 1) / kAttHeads);
   int chunk = kAttStep * kAttWaves;
-  while (chunk < 1024 && rows * ((max_len + chunk - 1) / chunk) > 2048) chunk *= 2;
+  const char* ev = getenv("CHT"); const int target = ev ? atoi(ev) : 2048;
+  while (chunk < 1024 * kAttWindows && rows * ((max_len + chunk - 1) / chunk) > target) chunk *= 2;
   return chunk;
 }
 
@@ -375,7 +473,8 @@ static hipError_t attention_launch(const void* q, int64_t q_stride, KvHalf kc, K
   const int chunk = att_chunk(B, sh.heads, ratio, max_len);
   const int chunks = max_len > 0 ? (int)((max_len + chunk - 1) / chunk) : 1;
   const int heads = ratio < kAttHeads ? ratio : kAttHeads;
-  const size_t lds = (size_t)(kAttWaves * (heads * D + 2 * kAttHeads)) * sizeof(float);
+  const size_t sum = (size_t)(kAttWaves * heads * D + (3 * kAttWaves + 1) * kAttHeads) * sizeof(float);
+  const size_t ring = (size_t)kAttWaves * AttStage<D, BITS>::RING, lds = ring > sum ? ring : sum;
   const dim3 grid((unsigned)(sh.heads * ((ratio + kAttHeads - 1) / kAttHeads)), (unsigned)chunks, (unsigned)B);
   float* part_ml = ws == nullptr ? nullptr : ws + B * sh.heads * ratio * chunks * D;
   kv_attention_kernel<D, BITS><<<grid, dim3(64 * kAttWaves), lds, st>>>(
@@ -383,7 +482,9 @@ static hipError_t attention_launch(const void* q, int64_t q_stride, KvHalf kc, K
       scale * 1.4426950408889634f, chunk, chunks, reinterpret_cast<f16*>(out), ws, part_ml);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks == 1) return e;
-  kv_join_kernel<<<dim3((unsigned)(B * sh.heads * ratio)), dim3(D), 0, st>>>(
+  int parts = 1;  // about eight chunks a part
+  while (parts * D < 1024 && 8 * parts < chunks) parts *= 2;
+  kv_join_kernel<<<dim3((unsigned)(B * sh.heads * ratio)), dim3(D, parts), 0, st>>>(
       ws, part_ml, lengths, max_len, (int)width, sh, sh.heads * ratio, chunk, chunks, reinterpret_cast<f16*>(out));
   return hipGetLastError();
 }

@@ -2,102 +2,138 @@
 // the weighted sum that ends an expert layer.
 //
 // Route: the top_k largest logits of a token (first of equal ones) and their
-// softmax weights, one wave per token with the logits in registers.
-// Plan: a stable counting sort of the pairs p = t * top_k + j by expert.  A
-// block counts the pairs of its run of kPlanPairs by expert; one block turns
-// the counts into offsets (in the order expert, then run); each block then
-// places its pairs, a lane's rank among the 64 pairs of its wave coming from
-// ballots on the bits of the expert.  No atomics on memory: the order never
-// depends on timing.
-// All of it is small and bound by launches and latency; the sum is bound by
-// memory.
+// softmax weights, 16 lanes per token (a wave above 256 experts or 16 choices)
+// with the logits in registers.
+// Plan: a stable counting sort of the pairs p = t * top_k + j by expert.  The
+// pairs are cut into runs; each run's pairs are counted by expert, the counts
+// become first rows (in the order expert, then run), and each run places its
+// pairs, a lane's rank among the 64 pairs of its wave coming from ballots on the
+// bits of the expert.  No order depends on timing.
+// All of it is bound by launches and latency: up to kSmallPairs pairs one block
+// does everything in one launch (45 tokens x 6 of 64 experts: one launch of
+// 6 us where four took 10); beyond, three launches.  The sum is bound by memory.
 #include "awq_common.h"
 #include "awq_internal.h"
 
 namespace awq {
 
-constexpr int kPlanThreads = 1024;  // pairs of one run: one per thread
+constexpr int kMoeThreads = 1024, kMoeWaves = kMoeThreads / 64;
+constexpr int kSmallPairs = 1024;  // in one block
+constexpr int kRunPairs = 512;     // of a run, at most (a route's run is whole tokens)
 
 // Order-preserving image of a float: larger floats have larger images, equal
-// ones (+0 and -0, which adding 0 makes +0) the same.
+// ones (+0 and -0, which adding 0 makes +0) the same.  No float's image is 0.
 __device__ inline uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ inline float key_value(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
 
-// V logits per lane (E <= 64 V); lane i holds experts V i .. V i + V - 1, so
-// the first of equal logits is in the first lane that has one.
-template <int V, typename T>
-__global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits, int64_t tokens, int E, int top_k,
-                                                    int renorm, int32_t* __restrict__ experts,
-                                                    float* __restrict__ weights) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= tokens) return;
-  float v[V];
-  uint32_t key[V];  // 0: not to be chosen (no such expert, -inf, NaN, or chosen already)
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    v[i] = e < E ? (float)logits[t * E + e] : -INFINITY;
-    key[i] = v[i] > -INFINITY ? order_key(v[i]) : 0u;
-    if (key[i]) top = fmaxf(top, v[i]);
+// v joined by `op` over each run of L = 16 or 64 lanes, in every lane of it: by
+// rotations within 16 lanes, then across.
+template <int L, typename Op>
+__device__ __forceinline__ uint32_t lanes_join(uint32_t v, Op op) {
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));  // row_ror 8, 4, 2, 1
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, false));
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, false));
+  if (L == 64) {
+    v = op(v, (uint32_t)__shfl_xor((int)v, 16, kWave));
+    v = op(v, (uint32_t)__shfl_xor((int)v, 32, kWave));
   }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  return lanes_join<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+  return lanes_join<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return __uint_as_float(lanes_join<L>(
+      __float_as_uint(v), [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
+}
+__device__ inline int wave_scan(int v) {  // inclusive
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+struct RouteArgs {
+  const void* logits;
+  float* weights;
+  int half, top_k, renorm;
+};
+
+// Tokens t0 .. t0 + count - 1, one for each run of L lanes in turn (V logits per
+// lane, E <= L V); lane j of the run writes the j-th choice and its weight, and
+// the expert to copy [count * top_k] too.  Four tokens a wave (L = 16) share every
+// instruction of the choice; one token a wave was bound by the vector ALU (16384
+// tokens x 8 of 128: 13.8 us against 6).
+template <int V, int L>
+__device__ inline void route_tokens(const RouteArgs& a, int64_t t0, int count, int E, int32_t* __restrict__ experts,
+                                    int* copy) {
+  const int r = threadIdx.x % L;
+  for (int i = threadIdx.x / L; i - (int)(threadIdx.x % 64) / L < count; i += kMoeThreads / L) {  // whole waves
+    const int64_t t = t0 + (i < count ? i : count - 1);  // lanes past the last token repeat it
+    uint32_t key[V];  // 0: not to be chosen (no such expert, -inf, NaN, or chosen already)
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) sum += key[i] ? expf(v[i] - top) : 0.f;
-  sum = wave_sum(sum);
-  int mine = -1;      // lane j keeps choice j
-  float w = 0.f, chosen = 0.f;
-  for (int j = 0; j < top_k; ++j) {
+    for (int u = 0; u < V; ++u) {
+      const int e = u * L + r;
+      float v = -INFINITY;
+      if (e < E)
+        v = a.half ? (float)reinterpret_cast<const f16*>(a.logits)[t * E + e]
+                   : reinterpret_cast<const float*>(a.logits)[t * E + e];
+      key[u] = v > -INFINITY ? order_key(v) : 0u;
+    }
     uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) best = key[i] > best ? key[i] : best;
-    uint32_t all = best;
+    for (int u = 0; u < V; ++u) best = key[u] > best ? key[u] : best;
+    const float top = key_value(lanes_max<L>(best));
+    float sum = 0.f;
+    if (!a.renorm) {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const uint32_t o = (uint32_t)__shfl_xor((int)all, off, kWave);
-      all = o > all ? o : all;
+      for (int u = 0; u < V; ++u) sum += key[u] ? expf(key_value(key[u]) - top) : 0.f;
     }
-    if (all == 0) break;  // nothing left to choose
-    const int owner = __ffsll((unsigned long long)__ballot(best == all)) - 1;
-    int slot = -1;
-    float val = 0.f;
+    int mine = -1;
+    uint32_t chosen = 0;
+    for (int j = 0; j < a.top_k; ++j) {
+      best = 0;
 #pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (key[i] == all) {
-        slot = i;
-        val = v[i];
+      for (int u = 0; u < V; ++u) best = key[u] > best ? key[u] : best;
+      const uint32_t most = lanes_max<L>(best);
+      uint32_t e = ~0u;  // the first expert that has it
+#pragma unroll
+      for (int u = V - 1; u >= 0; --u) e = key[u] == most ? u * L + r : e;
+      e = lanes_min<L>(e);
+#pragma unroll
+      for (int u = 0; u < V; ++u) key[u] = e == (uint32_t)(u * L + r) ? 0u : key[u];
+      if (r == j && most != 0) {  // 0: nothing was left to choose
+        mine = (int)e;
+        chosen = most;
       }
-    if (lane == owner) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == slot) key[i] = 0u;
     }
-    const int e = __shfl(lane * V + slot, owner, kWave);
-    const float p = expf(__shfl(val, owner, kWave) - top);
-    chosen += p;
-    if (lane == j) {
-      mine = e;
-      w = p;
+    const float w = mine >= 0 ? expf(key_value(chosen) - top) : 0.f;
+    sum = lanes_sum<L>(a.renorm ? w : sum);
+    if (r < a.top_k && i < count) {
+      experts[t * a.top_k + r] = mine;
+      a.weights[t * a.top_k + r] = mine >= 0 ? w / sum : 0.f;
+      copy[i * a.top_k + r] = mine;
     }
-  }
-  if (lane < top_k) {
-    experts[t * top_k + lane] = mine;
-    weights[t * top_k + lane] = mine >= 0 ? w / (renorm ? chosen : sum) : 0.f;
   }
 }
 
-// Expert of pair p as a group of the plan: E for a dropped pair (an id outside
-// [0, E)) and E + 1 past the last pair.
-__device__ inline int group_of(const int32_t* experts, int64_t p, int64_t pairs, int E) {
-  if (p >= pairs) return E + 1;
-  const int e = experts[p];
-  return e >= 0 && e < E ? e : E;
-}
+// A pair's group in the plan: its expert, or E for a dropped pair (an id outside [0, E)).
+__device__ inline int group_of(int expert, int E) { return expert >= 0 && expert < E ? expert : E; }
 
 // Lanes of the wave whose group equals this lane's.
 __device__ inline uint64_t same_group(int g, int bits) {
@@ -109,78 +145,150 @@ __device__ inline uint64_t same_group(int g, int bits) {
   return same;
 }
 
-constexpr int kPlanWaves = kPlanThreads / 64;
-
-// counts[run][g] for the E + 1 groups.
-__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(const int32_t* __restrict__ experts, int64_t pairs,
-                                                                  int E, int32_t* __restrict__ counts) {
-  extern __shared__ int32_t hist[];
-  for (int g = threadIdx.x; g <= E; g += kPlanThreads) hist[g] = 0;
-  __syncthreads();
-  const int g = group_of(experts, (int64_t)blockIdx.x * kPlanThreads + threadIdx.x, pairs, E);
-  if (g <= E) atomicAdd(&hist[g], 1);  // whole numbers: the order of the sum does not matter
-  __syncthreads();
-  for (int i = threadIdx.x; i <= E; i += kPlanThreads) counts[(int64_t)blockIdx.x * (E + 1) + i] = hist[i];
-}
-
-// counts[run][g] becomes the first row of run's pairs in group g; offsets too.
-__global__ __launch_bounds__(kPlanThreads) void plan_scan_kernel(int32_t* __restrict__ counts, int64_t runs, int E,
-                                                                 int32_t* __restrict__ offsets) {
-  extern __shared__ int32_t total[];  // [E + 1]
-  for (int g = threadIdx.x; g <= E; g += kPlanThreads) {
-    int32_t s = 0;
-    for (int64_t r = 0; r < runs; ++r) s += counts[r * (E + 1) + g];
-    total[g] = s;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int32_t s = 0;
-    for (int g = 0; g <= E; ++g) {
-      const int32_t c = total[g];
-      total[g] = s;
-      offsets[g] = s;
-      s += c;
-    }
-  }
-  __syncthreads();
-  for (int g = threadIdx.x; g <= E; g += kPlanThreads) {
-    int32_t s = total[g];
-    for (int64_t r = 0; r < runs; ++r) {
-      const int32_t c = counts[r * (E + 1) + g];
-      counts[r * (E + 1) + g] = s;
-      s += c;
-    }
-  }
-}
-
-__global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t* __restrict__ experts, int64_t pairs,
-                                                                  int E, int bits, const int32_t* __restrict__ counts,
-                                                                  int32_t* __restrict__ rows,
-                                                                  int32_t* __restrict__ pos) {
-  extern __shared__ int32_t hist[];  // [waves][E + 1]
+// Exclusive sums of v over the block's threads (of whole waves), by way of `part` [16].
+__device__ inline int block_scan(int v, int* part) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < kPlanWaves * (E + 1); i += kPlanThreads) hist[i] = 0;
+  const int upto = wave_scan(v);
+  if (lane == 63) part[wave] = upto;
   __syncthreads();
-  const int64_t p = (int64_t)blockIdx.x * kPlanThreads + threadIdx.x;
-  const int g = group_of(experts, p, pairs, E);
-  const uint64_t same = same_group(g, bits);
+  int before = 0;
+  for (int w = 0; w < wave; ++w) before += part[w];
+  __syncthreads();
+  return before + upto - v;
+}
+
+// Places the block's pairs, one per thread: hist [16][E + 1] is scratch, start(g)
+// the first row of the block's pairs of group g (called once per group by the
+// thread g % kMoeThreads, the counts of the block's waves being in hist).
+template <typename Start>
+__device__ inline void place(int64_t p, bool valid, int g, int E, int bits, int* hist, Start start,
+                             int32_t* __restrict__ rows, int32_t* __restrict__ pos) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t same = same_group(valid ? g : E + 1, bits);
   const int rank = __popcll(same & ((1ull << lane) - 1));
-  if (rank == 0 && g <= E) hist[wave * (E + 1) + g] = __popcll(same);
+  if (rank == 0 && valid) hist[wave * (E + 1) + g] = __popcll(same);
   __syncthreads();
-  for (int i = threadIdx.x; i <= E; i += kPlanThreads) {
-    int32_t s = counts[(int64_t)blockIdx.x * (E + 1) + i];
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int32_t c = hist[w * (E + 1) + i];
-      hist[w * (E + 1) + i] = s;
-      s += c;
-    }
-  }
+  start();
   __syncthreads();
-  if (p < pairs) {
+  if (valid) {
     const int32_t row = hist[wave * (E + 1) + g] + rank;
     rows[row] = (int32_t)p;
     pos[p] = g < E ? row : -1;
   }
+}
+
+// Turns the waves' counts of a group into the first rows of each wave's pairs.
+__device__ inline void spread(int* hist, int g, int E, int row) {
+  for (int w = 0; w < kMoeWaves; ++w) {
+    const int c = hist[w * (E + 1) + g];
+    hist[w * (E + 1) + g] = row;
+    row += c;
+  }
+}
+
+// Everything in one block: V = 0 plans given experts, otherwise they are chosen first.
+template <int V, int L>
+__global__ __launch_bounds__(kMoeThreads) void plan_small_kernel(RouteArgs a, int64_t tokens, int pairs, int E,
+                                                                 int bits, int32_t* __restrict__ experts,
+                                                                 int32_t* __restrict__ offsets,
+                                                                 int32_t* __restrict__ rows, int32_t* __restrict__ pos) {
+  extern __shared__ int hist[];  // [16][E + 1]
+  __shared__ int part[kMoeWaves], mine[kSmallPairs];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < kMoeWaves * (E + 1); i += kMoeThreads) hist[i] = 0;
+  if constexpr (V > 0) {
+    route_tokens<V, L>(a, 0, (int)tokens, E, experts, mine);
+  } else if (tid < pairs) {
+    mine[tid] = experts[tid];
+  }
+  __syncthreads();
+  const bool valid = tid < pairs;
+  const int g = valid ? group_of(mine[tid], E) : 0;
+  place(tid, valid, g, E, bits, hist,
+        [&] {  // E + 1 <= 1025 groups: thread i takes group i, the dropped pairs (last) start where the others end
+          int count = 0;
+          if (tid < E)
+            for (int w = 0; w < kMoeWaves; ++w) count += hist[w * (E + 1) + tid];
+          const int first = block_scan(count, part);
+          if (tid < E) {
+            offsets[tid] = first;
+            spread(hist, tid, E, first);
+          }
+          if (tid == E - 1) {
+            offsets[E] = first + count;
+            spread(hist, E, E, first + count);
+          }
+        },
+        rows, pos);
+}
+
+// counts[g][run] of each run's pairs (V > 0: after choosing them; a run is `run` pairs, whole tokens).
+template <int V, int L>
+__global__ __launch_bounds__(kMoeThreads) void plan_count_kernel(RouteArgs a, int64_t tokens, int64_t pairs, int run,
+                                                                 int E, int32_t* __restrict__ experts,
+                                                                 int32_t* __restrict__ counts, int64_t runs) {
+  extern __shared__ int hist[];  // [E + 1]
+  __shared__ int mine[kRunPairs];
+  const int tid = threadIdx.x;
+  const int64_t p0 = (int64_t)blockIdx.x * run;
+  const int n = pairs - p0 < run ? (int)(pairs - p0) : run;
+  for (int g = tid; g <= E; g += kMoeThreads) hist[g] = 0;
+  if constexpr (V > 0) {
+    route_tokens<V, L>(a, p0 / a.top_k, n / a.top_k, E, experts, mine);
+  } else if (tid < n) {
+    mine[tid] = experts[p0 + tid];
+  }
+  __syncthreads();
+  if (tid < n) atomicAdd(&hist[group_of(mine[tid], E)], 1);  // whole numbers: the order does not matter
+  __syncthreads();
+  for (int g = tid; g <= E; g += kMoeThreads) counts[(int64_t)g * runs + blockIdx.x] = hist[g];
+}
+
+// counts[g][run]: exclusive sums over the runs of group g = blockIdx.x; total[g].
+__global__ __launch_bounds__(kMoeThreads) void plan_scan_kernel(int32_t* __restrict__ counts, int64_t runs,
+                                                                int32_t* __restrict__ total) {
+  __shared__ int part[kMoeWaves];
+  int32_t* c = counts + (int64_t)blockIdx.x * runs;
+  int before = 0;
+  for (int64_t r0 = 0; r0 < runs; r0 += blockDim.x) {
+    const int64_t r = r0 + threadIdx.x;
+    const int v = r < runs ? c[r] : 0;
+    const int first = block_scan(v, part);
+    if (r < runs) c[r] = before + first;
+    if (threadIdx.x == blockDim.x - 1) part[0] = first + v;
+    __syncthreads();
+    before += part[0];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) total[blockIdx.x] = before;
+}
+
+__global__ __launch_bounds__(kMoeThreads) void plan_place_kernel(const int32_t* __restrict__ experts, int64_t pairs,
+                                                                 int run, int E, int bits,
+                                                                 const int32_t* __restrict__ counts, int64_t runs,
+                                                                 const int32_t* __restrict__ total,
+                                                                 int32_t* __restrict__ offsets,
+                                                                 int32_t* __restrict__ rows, int32_t* __restrict__ pos) {
+  extern __shared__ int hist[];  // [16][E + 1]
+  __shared__ int part[kMoeWaves];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < kMoeWaves * (E + 1); i += kMoeThreads) hist[i] = 0;
+  __syncthreads();
+  const int64_t p = (int64_t)blockIdx.x * run + tid;
+  const bool valid = tid < run && p < pairs;
+  const int g = valid ? group_of(experts[p], E) : 0;
+  place(p, valid, g, E, bits, hist,
+        [&] {
+          const int count = tid < E ? total[tid] : 0;
+          const int first = block_scan(count, part);  // of the group, over all runs
+          if (tid < E) spread(hist, tid, E, first + counts[(int64_t)tid * runs + blockIdx.x]);
+          if (tid == E - 1) spread(hist, E, E, first + count + counts[(int64_t)E * runs + blockIdx.x]);
+          if (blockIdx.x == 0) {
+            if (tid < E) offsets[tid] = first;
+            if (tid == E - 1) offsets[E] = first + count;
+          }
+        },
+        rows, pos);
 }
 
 // out[t][n] = sum_j weights[t][j] y[pos[t * k + j]][n], 8 channels per thread.
@@ -206,42 +314,50 @@ __global__ __launch_bounds__(256) void combine_kernel(const f16* __restrict__ y,
   *reinterpret_cast<f16x8*>(out + t * N + c) = o;
 }
 
-size_t moe_plan_workspace(int64_t pairs, int E) {
-  return (size_t)((pairs + kPlanThreads - 1) / kPlanThreads) * (size_t)(E + 1) * sizeof(int32_t);
+// A run: whole tokens where the experts are chosen along (top_k > 1), at most kRunPairs pairs.
+static int run_pairs(int top_k) { return kRunPairs / top_k * top_k; }
+
+size_t moe_plan_workspace(int64_t pairs, int E, int top_k) {
+  const int run = run_pairs(top_k);
+  return (size_t)((pairs + run - 1) / run + 1) * (size_t)(E + 1) * sizeof(int32_t);
 }
 
-template <int V>
-static hipError_t route_launch(const void* logits, int bytes, int64_t T, int E, int top_k, int renorm,
-                               int32_t* experts, float* weights, hipStream_t st) {
-  const dim3 grid((unsigned)((T + 3) / 4)), block(256);
-  if (bytes == 2)
-    route_kernel<V, f16><<<grid, block, 0, st>>>(reinterpret_cast<const f16*>(logits), T, E, top_k, renorm, experts,
-                                                 weights);
-  else
-    route_kernel<V, float><<<grid, block, 0, st>>>(reinterpret_cast<const float*>(logits), T, E, top_k, renorm,
-                                                   experts, weights);
+template <int V, int L>
+static hipError_t plan_launch(const RouteArgs& a, int64_t T, int E, int32_t* experts, int32_t* offsets, int32_t* rows,
+                              int32_t* pos, int32_t* ws, hipStream_t st) {
+  const int64_t pairs = T * a.top_k;
+  int bits = 0;
+  while ((1 << bits) < E + 2) ++bits;
+  const size_t hist = (size_t)(E + 1) * sizeof(int);
+  if (pairs <= kSmallPairs) {
+    plan_small_kernel<V, L><<<dim3(1), dim3(kMoeThreads), hist * kMoeWaves, st>>>(a, T, (int)pairs, E, bits, experts,
+                                                                               offsets, rows, pos);
+    return hipGetLastError();
+  }
+  const int run = run_pairs(a.top_k);
+  const int64_t runs = (pairs + run - 1) / run;
+  int32_t* total = ws + runs * (E + 1);
+  plan_count_kernel<V, L><<<dim3((unsigned)runs), dim3(kMoeThreads), hist, st>>>(a, T, pairs, run, E, experts, ws, runs);
+  plan_scan_kernel<<<dim3((unsigned)(E + 1)), dim3(runs > 256 ? kMoeThreads : 256), 0, st>>>(ws, runs, total);
+  plan_place_kernel<<<dim3((unsigned)runs), dim3(kMoeThreads), hist * kMoeWaves, st>>>(experts, pairs, run, E, bits, ws,
+                                                                                      runs, total, offsets, rows, pos);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_route(const void* logits, int bytes, int64_t T, int E, int top_k, int renorm, int32_t* experts,
-                            float* weights, hipStream_t st) {
-  if (E <= 64) return route_launch<1>(logits, bytes, T, E, top_k, renorm, experts, weights, st);
-  if (E <= 128) return route_launch<2>(logits, bytes, T, E, top_k, renorm, experts, weights, st);
-  if (E <= 256) return route_launch<4>(logits, bytes, T, E, top_k, renorm, experts, weights, st);
-  return route_launch<16>(logits, bytes, T, E, top_k, renorm, experts, weights, st);
+                            float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, int32_t* ws,
+                            hipStream_t st) {
+  const RouteArgs a{logits, weights, bytes == 2, top_k, renorm};
+  if (top_k <= 16 && E <= 64) return plan_launch<4, 16>(a, T, E, experts, offsets, rows, pos, ws, st);
+  if (top_k <= 16 && E <= 128) return plan_launch<8, 16>(a, T, E, experts, offsets, rows, pos, ws, st);
+  if (top_k <= 16 && E <= 256) return plan_launch<16, 16>(a, T, E, experts, offsets, rows, pos, ws, st);
+  return plan_launch<16, 64>(a, T, E, experts, offsets, rows, pos, ws, st);  // a choice for each lane, 1024 experts
 }
 
-hipError_t launch_moe_plan(const int32_t* experts, int64_t pairs, int E, int32_t* offsets, int32_t* rows, int32_t* pos,
-                           int32_t* counts, hipStream_t st) {
-  const int64_t runs = (pairs + kPlanThreads - 1) / kPlanThreads;
-  int bits = 0;
-  while ((1 << bits) < E + 2) ++bits;
-  const size_t hist = (size_t)(E + 1) * sizeof(int32_t);
-  plan_count_kernel<<<dim3((unsigned)runs), dim3(kPlanThreads), hist, st>>>(experts, pairs, E, counts);
-  plan_scan_kernel<<<dim3(1), dim3(kPlanThreads), hist, st>>>(counts, runs, E, offsets);
-  plan_place_kernel<<<dim3((unsigned)runs), dim3(kPlanThreads), hist * kPlanWaves, st>>>(experts, pairs, E, bits,
-                                                                                         counts, rows, pos);
-  return hipGetLastError();
+hipError_t launch_moe_plan(const int32_t* experts, int64_t T, int E, int top_k, int32_t* offsets, int32_t* rows,
+                           int32_t* pos, int32_t* ws, hipStream_t st) {
+  return plan_launch<0, 16>(RouteArgs{nullptr, nullptr, 0, top_k, 0}, T, E, const_cast<int32_t*>(experts), offsets, rows,
+                        pos, ws, st);
 }
 
 hipError_t launch_moe_combine(const void* y, int64_t R, const int32_t* pos, const float* weights, int64_t T, int top_k,
