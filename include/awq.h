@@ -516,7 +516,8 @@ size_t awq_kv_params_bytes(int64_t pages, int32_t H, int32_t page);
  *             (padding: -1) is not written.  Slots of one call are distinct; of
  *             tokens that share a slot, which one's values end there (row by
  *             row, or a mix of them) is unspecified
- * Other slots are left as they were.
+ * Other slots are left as they were.  Requires 1 <= T <= AWQ_MAX_KV_TOKENS and
+ * (T + 31) * H * D < 2^35; so does awq_kv_read.
  */
 int awq_kv_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slots, void* k_codes,
                  void* k_params, void* v_codes, void* v_params, int64_t T, int32_t H, int32_t D, int64_t pages,
@@ -541,7 +542,7 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
  *               (elements, a multiple of 8, >= Hq * D)
  *   page_table  device int32 [B][table_width]: page of the sequence's tokens
  *               page * i .. page * i + page - 1.  Entries past the length are
- *               not read; the tokens of an entry outside [0, pages) count as
+ *               not used; the tokens of an entry outside [0, pages) count as
  *               absent
  *   lengths     device int32 [B]; at most table_width * page and max_len are
  *               used.  A sequence with no tokens gets out = 0

@@ -63,7 +63,7 @@ BAD = {
                          dict(N=0), dict(K=100), dict(group=64), dict(bits=8), dict(R=(1 << 24) + 1), dict(K=1 << 21), dict(K=(1 << 17) + 128),
                          dict(R=1 << 24, N=1 << 20, s=None)],
     "awq_moe_combine": [dict(T=0), dict(R=0), dict(top_k=0), dict(N=12), dict(N=0), dict(T=1 << 24, N=1 << 20)],
-    "awq_kv_write": [dict(T=0), dict(T=(1 << 22) + 1), dict(H=0), dict(H=1025), dict(D=96), dict(page=24), dict(page=8),
+    "awq_kv_write": [dict(T=0), dict(T=(1 << 22) + 1), dict(T=1 << 22, H=64, k_stride=8192, v_stride=8192), dict(H=0), dict(H=1025), dict(D=96), dict(page=24), dict(page=8),
                      dict(page=2048), dict(pages=0), dict(pages=1 << 27), dict(bits=3), dict(k_stride=128),
                      dict(v_stride=260)],
     "awq_kv_read": [dict(T=0), dict(D=32), dict(page=0), dict(pages=-1), dict(bits=16)],

@@ -170,7 +170,8 @@ int awq_kv_write(const void* k, const void* v, int64_t k_stride, int64_t v_strid
               "k, v, slots and the cache's four arrays must not be NULL");
   awq::KvShape sh;
   if (int st = check_cache(pages, H, page, D, bits, &sh)) return st;
-  AWQ_REQUIRE(T >= 1 && T <= AWQ_MAX_KV_TOKENS, AWQ_ERROR_INVALID_VALUE, "T=%lld outside [1, 2^22]", (long long)T);
+  AWQ_REQUIRE(T >= 1 && T <= AWQ_MAX_KV_TOKENS && (T + 31) * H * (D / 8) < (int64_t(1) << 32), AWQ_ERROR_INVALID_VALUE,
+              "T=%lld: between 1 and 2^22 tokens, (T + 31) * H * D below 2^35, are moved by one call", (long long)T);
   for (int64_t s : {k_stride, v_stride})
     AWQ_REQUIRE(s >= (int64_t)H * D && s % 8 == 0 && s < (int64_t(1) << 31), AWQ_ERROR_INVALID_VALUE,
                 "a token stride of %lld elements: a multiple of 8, at least H * D and below 2^31, is needed",
@@ -192,7 +193,8 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
               "k, v, slots and the cache's four arrays must not be NULL");
   awq::KvShape sh;
   if (int st = check_cache(pages, H, page, D, bits, &sh)) return st;
-  AWQ_REQUIRE(T >= 1 && T <= AWQ_MAX_KV_TOKENS, AWQ_ERROR_INVALID_VALUE, "T=%lld outside [1, 2^22]", (long long)T);
+  AWQ_REQUIRE(T >= 1 && T <= AWQ_MAX_KV_TOKENS && (T + 31) * H * (D / 8) < (int64_t(1) << 32), AWQ_ERROR_INVALID_VALUE,
+              "T=%lld: between 1 and 2^22 tokens, (T + 31) * H * D below 2^35, are moved by one call", (long long)T);
   if (int st = check_aligned({{k_codes, "k_codes"}, {k_params, "k_params"}, {v_codes, "v_codes"},
                               {v_params, "v_params"}, {slots, "slots"}, {k, "k"}, {v, "v"}}))
     return st;

@@ -4,6 +4,10 @@ As in api.py: each wrapper checks dtypes, devices and shapes, allocates outputs 
 workspaces with torch on the inputs' device, and calls libawq on torch's current stream of
 that device; all arithmetic happens in the library's HIP kernels.  Inputs on another device
 than the first argument's are refused.
+
+A decoding step makes many of these calls on little data, so the wrappers are kept short:
+the device is switched only when it is not the current one, and a plan's arrays share one
+allocation.
 """
 from __future__ import annotations
 
@@ -12,17 +16,39 @@ from typing import Optional
 import torch
 
 from ._lib import check, load
-from .api import BITS, GROUP, _need, _ptr, _stream, packed_words
+from .api import BITS, GROUP, _need, _ptr, packed_words
 
 KV_BITS = (4, 8)               # code widths of a cache
 KV_HEAD_DIMS = (64, 128, 256)  # channels of a head
-CACHE_KEYS = ("k_codes", "k_params", "v_codes", "v_params")
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
 
 
-def _on(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _like(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, index: int) -> None:
+    """_need, on the given device."""
+    if isinstance(t, torch.Tensor) and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    _need(t, name, dtype, ndim)
+
+
+def _run(index: int, fn, *args) -> None:
+    """fn(*args, stream) with the device current and its current stream; raises on a status."""
+    if index == torch.cuda.current_device():
+        check(fn(*args, _raw_stream(index)))
+    else:
+        with torch.cuda.device(index):
+            check(fn(*args, _raw_stream(index)))
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
+    """(pointer, bytes) of the caller's workspace or a new one; the tensor too, to keep it."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 # --------------------------------------------------------------------- experts
@@ -30,13 +56,28 @@ def awq_moe_workspace_bytes(T: int, E: int, top_k: int) -> int:
     return int(load().awq_moe_workspace_bytes(T, E, top_k))
 
 
-def _plan_buffers(T: int, E: int, top_k: int, dev: torch.device):
-    need = awq_moe_workspace_bytes(T, E, top_k)
+def _int_arrays(dev: torch.device, *sizes: int):
+    """int32 arrays of these sizes in one allocation, each 16-byte aligned."""
+    pieces = []
+    for n in sizes:
+        pieces.append(n)
+        if n % 4:
+            pieces.append(4 - n % 4)  # padding
+    parts = torch.empty(sum(pieces), dtype=torch.int32, device=dev).split_with_sizes(pieces)
+    if len(parts) == len(sizes):
+        return parts
+    out, i = [], 0
+    for n in sizes:
+        out.append(parts[i])
+        i += 2 if n % 4 else 1
+    return out
+
+
+def _plan_workspace(T: int, E: int, top_k: int) -> int:
+    need = load().awq_moe_workspace_bytes(T, E, top_k)
     if need == 0:
         raise ValueError(f"unsupported sizes for a plan: T={T}, E={E}, top_k={top_k}")
-    ints = dict(dtype=torch.int32, device=dev)
-    return (dict(offsets=torch.empty(E + 1, **ints), rows=torch.empty(T * top_k, **ints),
-                 pos=torch.empty(T * top_k, **ints)), torch.empty(need, dtype=torch.uint8, device=dev), need)
+    return need
 
 
 def awq_moe_plan(experts: torch.Tensor, num_experts: int) -> dict:
@@ -44,12 +85,12 @@ def awq_moe_plan(experts: torch.Tensor, num_experts: int) -> dict:
     pair): offsets [E+1], rows and pos [T*top_k] as awq_gemm_grouped and awq_moe_combine take."""
     _need(experts, "experts", torch.int32, 2)
     T, top_k = experts.shape
-    plan, ws, need = _plan_buffers(T, num_experts, top_k, experts.device)
-    with torch.cuda.device(experts.device):
-        check(load().awq_moe_plan(experts.data_ptr(), T, num_experts, top_k, plan["offsets"].data_ptr(),
-                                  plan["rows"].data_ptr(), plan["pos"].data_ptr(), ws.data_ptr(), need,
-                                  _stream(experts.device)))
-    return plan
+    need = _plan_workspace(T, num_experts, top_k)
+    R = T * top_k
+    rows, pos, offsets, ws = _int_arrays(experts.device, R, R, num_experts + 1, need // 4)
+    _run(experts.get_device(), load().awq_moe_plan, experts.data_ptr(), T, num_experts, top_k, offsets.data_ptr(),
+         rows.data_ptr(), pos.data_ptr(), ws.data_ptr(), need)
+    return dict(offsets=offsets, rows=rows, pos=pos)
 
 
 def awq_moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True) -> dict:
@@ -60,17 +101,16 @@ def awq_moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True) ->
     half = isinstance(logits, torch.Tensor) and logits.dtype == torch.float16
     _need(logits, "logits", torch.float16 if half else torch.float32, 2)
     T, E = logits.shape
-    dev = logits.device
     if not 1 <= top_k <= E:
         raise ValueError(f"top_k={top_k} outside [1, {E}]")
-    plan, ws, need = _plan_buffers(T, E, top_k, dev)
-    experts = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        check(load().awq_moe_route(logits.data_ptr(), 2 if half else 4, T, E, top_k, int(bool(renormalize)),
-                                   experts.data_ptr(), weights.data_ptr(), plan["offsets"].data_ptr(),
-                                   plan["rows"].data_ptr(), plan["pos"].data_ptr(), ws.data_ptr(), need, _stream(dev)))
-    return dict(experts=experts, weights=weights, **plan)
+    need = _plan_workspace(T, E, top_k)
+    R = T * top_k
+    experts, weights, rows, pos, offsets, ws = _int_arrays(logits.device, R, R, R, R, E + 1, need // 4)
+    _run(logits.get_device(), load().awq_moe_route, logits.data_ptr(), 2 if half else 4, T, E, top_k,
+         int(bool(renormalize)), experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+         pos.data_ptr(), ws.data_ptr(), need)
+    return dict(experts=experts.view(T, top_k), weights=weights.view(torch.float32).view(T, top_k), offsets=offsets,
+                rows=rows, pos=pos)
 
 
 def awq_gemm_grouped_workspace_bytes(R: int, K: int, scaled: bool) -> int:
@@ -87,11 +127,11 @@ def awq_gemm_grouped(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
     (fp32 [E][K]) it is divided by s[e] first, as awq_scale_input does.  Rows from offsets[E] on
     are left as they were (in a new `out`: unset)."""
     _need(x, "x", torch.float16, 2)
-    _need(packed, "packed", torch.int32, 3)
-    _need(scales, "scales", torch.float16, 3)
-    _need(zeros, "zeros", torch.uint8, 3)
-    _need(offsets, "offsets", torch.int32, 1)
-    dev = x.device
+    index = x.get_device()
+    _like(packed, "packed", torch.int32, 3, index)
+    _like(scales, "scales", torch.float16, 3, index)
+    _like(zeros, "zeros", torch.uint8, 3, index)
+    _like(offsets, "offsets", torch.int32, 1, index)
     x_rows, K = x.shape
     E, N, words = packed.shape
     G = K // group
@@ -99,34 +139,29 @@ def awq_gemm_grouped(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
         bits = next((b for b in BITS if words == packed_words(K, b)), None)
         if bits is None:
             raise ValueError(f"packed {tuple(packed.shape)} matches no format for K={K}")
-    if words != packed_words(K, bits) or tuple(scales.shape) != (E, N, G) or tuple(zeros.shape) != (E, N, (G + 1) // 2):
+    if words != packed_words(K, bits) or scales.shape != (E, N, G) or zeros.shape != (E, N, (G + 1) // 2):
         raise ValueError("packed/scales/zeros do not match x's K")
     if offsets.shape[0] != E + 1:
         raise ValueError(f"offsets must have E + 1 = {E + 1} entries")
+    R, need = x_rows, 0
     if rows is not None:
-        _need(rows, "rows", torch.int32, 1)
-    R = x_rows if rows is None else rows.shape[0]
-    if s is not None:
-        _need(s, "s", torch.float32, 2)
-        if tuple(s.shape) != (E, K):
-            raise ValueError("s must be float32 [E][K]")
-    if out is None:
-        out = torch.empty((R, N), dtype=torch.float16, device=dev)
-    else:
-        _need(out, "out", torch.float16, 2)
-        if tuple(out.shape) != (R, N):
-            raise ValueError("out must be fp16 [R][N]")
+        _like(rows, "rows", torch.int32, 1, index)
+        R = rows.shape[0]
     lib = load()
-    need = lib.awq_gemm_grouped_workspace_bytes(R, K, 1) if s is not None else 0
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _on(dev, packed=packed, scales=scales, zeros=zeros, offsets=offsets, rows=rows, s=s, out=out, workspace=workspace)
-    with torch.cuda.device(dev):
-        check(lib.awq_gemm_grouped(x.data_ptr(), x_rows, _ptr(rows), top_k, offsets.data_ptr(), _ptr(s),
-                                   packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), out.data_ptr(), R, E, N, K,
-                                   group, bits, _ptr(workspace),
-                                   0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                   _stream(dev)))
+    if s is not None:
+        _like(s, "s", torch.float32, 2, index)
+        if s.shape != (E, K):
+            raise ValueError("s must be float32 [E][K]")
+        need = lib.awq_gemm_grouped_workspace_bytes(R, K, 1)
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.float16, device=x.device)
+    else:
+        _like(out, "out", torch.float16, 2, index)
+        if out.shape != (R, N):
+            raise ValueError("out must be fp16 [R][N]")
+    ws, ws_bytes, _keep = _scratch(workspace, need, x.device)
+    _run(index, lib.awq_gemm_grouped, x.data_ptr(), x_rows, _ptr(rows), top_k, offsets.data_ptr(), _ptr(s),
+         packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), out.data_ptr(), R, E, N, K, group, bits, ws, ws_bytes)
     return out
 
 
@@ -135,8 +170,9 @@ def awq_moe_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
     """out[t] = sum_j weights[t][j] y[pos[t * top_k + j]] (fp32 sums, fp16 [T][N]); pairs with
     pos outside y add nothing.  weights fp32 [T][top_k], pos int32 [T*top_k]."""
     _need(y, "y", torch.float16, 2)
-    _need(pos, "pos", torch.int32, 1)
-    _need(weights, "weights", torch.float32, 2)
+    index = y.get_device()
+    _like(pos, "pos", torch.int32, 1, index)
+    _like(weights, "weights", torch.float32, 2, index)
     R, N = y.shape
     T, top_k = weights.shape
     if pos.shape[0] != T * top_k:
@@ -144,13 +180,11 @@ def awq_moe_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
     if out is None:
         out = torch.empty((T, N), dtype=torch.float16, device=y.device)
     else:
-        _need(out, "out", torch.float16, 2)
-        if tuple(out.shape) != (T, N):
+        _like(out, "out", torch.float16, 2, index)
+        if out.shape != (T, N):
             raise ValueError("out must be fp16 [T][N]")
-    _on(y.device, pos=pos, weights=weights, out=out)
-    with torch.cuda.device(y.device):
-        check(load().awq_moe_combine(y.data_ptr(), R, pos.data_ptr(), weights.data_ptr(), T, top_k, N, out.data_ptr(),
-                                     _stream(y.device)))
+    _run(index, load().awq_moe_combine, y.data_ptr(), R, pos.data_ptr(), weights.data_ptr(), T, top_k, N,
+         out.data_ptr())
     return out
 
 
@@ -169,21 +203,21 @@ def empty_kv_cache(pages: int, heads: int, head_dim: int, page: int = 16, bits: 
     return dict(k_codes=codes(), k_params=params(), v_codes=codes(), v_params=params(), bits=bits)
 
 
-def _cache_shape(cache: dict, head_dim: int, dev: torch.device):
-    """(pages, heads, page, bits) of a cache whose heads have head_dim channels."""
-    bits = cache["bits"]
+def _cache_args(cache: dict, head_dim: int, index: int):
+    """The four arrays' pointers and (pages, heads, page, bits) of a cache of heads of head_dim channels."""
+    kc, kp, vc, vp, bits = cache["k_codes"], cache["k_params"], cache["v_codes"], cache["v_params"], cache["bits"]
     if bits not in KV_BITS:
         raise ValueError(f"bits must be one of {KV_BITS}, got {bits}")
-    shape = cache["k_codes"].shape
-    for name in CACHE_KEYS:
-        t = cache[name]
-        _need(t, name, torch.int32 if name.endswith("codes") else torch.float16, 4)
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-        if t.shape[:3] != shape[:3] or t.shape[3] != (head_dim * bits // 32 if name.endswith("codes") else 2):
-            raise ValueError(f"{name} {tuple(t.shape)} does not match the cache's other arrays, or {bits}-bit heads "
-                             f"of {head_dim}")
-    return shape[0], shape[1], shape[2], bits
+    _like(kc, "k_codes", torch.int32, 4, index)
+    _like(kp, "k_params", torch.float16, 4, index)
+    _like(vc, "v_codes", torch.int32, 4, index)
+    _like(vp, "v_params", torch.float16, 4, index)
+    pages, heads, page, words = shape = kc.shape
+    if vc.shape != shape or kp.shape != (pages, heads, page, 2) or vp.shape != kp.shape:
+        raise ValueError("k_codes, k_params, v_codes and v_params are not of one cache")
+    if words * 32 != head_dim * bits:
+        raise ValueError(f"the cache's rows of {words} words do not hold {bits}-bit heads of {head_dim}")
+    return (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), pages, heads, page, bits
 
 
 def _need_rows(t: torch.Tensor, name: str) -> None:
@@ -211,20 +245,16 @@ def awq_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: d
     the cache, such as -1 for padding, is not written).  Returns the cache."""
     _need_rows(k, "k")
     _need_rows(v, "v")
-    _need(slots, "slots", torch.int32, 1)
+    index = k.get_device()
+    _like(slots, "slots", torch.int32, 1, index)
     T, H, D = k.shape
-    if v.shape != k.shape or slots.shape[0] != T:
-        raise ValueError("k and v must be fp16 [T][heads][head_dim] and slots int32 [T]")
-    dev = k.device
-    pages, heads, page, bits = _cache_shape(cache, D, dev)
+    if v.shape != k.shape or v.get_device() != index or slots.shape[0] != T:
+        raise ValueError("k and v must be fp16 [T][heads][head_dim] on one device, and slots int32 [T]")
+    arrays, pages, heads, page, bits = _cache_args(cache, D, index)
     if heads != H:
         raise ValueError(f"k has {H} heads, the cache {heads}")
-    _on(dev, v=v, slots=slots)
-    with torch.cuda.device(dev):
-        check(load().awq_kv_write(k.data_ptr(), v.data_ptr(), _token_stride(k), _token_stride(v), slots.data_ptr(),
-                                  cache["k_codes"].data_ptr(), cache["k_params"].data_ptr(),
-                                  cache["v_codes"].data_ptr(), cache["v_params"].data_ptr(), T, H, D, pages, page,
-                                  bits, _stream(dev)))
+    _run(index, load().awq_kv_write, k.data_ptr(), v.data_ptr(), _token_stride(k), _token_stride(v), slots.data_ptr(),
+         *arrays, T, H, D, pages, page, bits)
     return cache
 
 
@@ -232,15 +262,13 @@ def awq_kv_read(cache: dict, slots: torch.Tensor, head_dim: int):
     """The keys and values of T slots (int32 [T]), dequantised: two fp16 [T][heads][head_dim]; 0
     for a slot outside the cache."""
     _need(slots, "slots", torch.int32, 1)
-    dev = slots.device
-    pages, H, page, bits = _cache_shape(cache, head_dim, dev)
+    index = slots.get_device()
+    arrays, pages, H, page, bits = _cache_args(cache, head_dim, index)
     T = slots.shape[0]
-    k = torch.empty((T, H, head_dim), dtype=torch.float16, device=dev)
+    k = torch.empty((T, H, head_dim), dtype=torch.float16, device=slots.device)
     v = torch.empty_like(k)
-    with torch.cuda.device(dev):
-        check(load().awq_kv_read(cache["k_codes"].data_ptr(), cache["k_params"].data_ptr(),
-                                 cache["v_codes"].data_ptr(), cache["v_params"].data_ptr(), slots.data_ptr(),
-                                 k.data_ptr(), v.data_ptr(), T, H, head_dim, pages, page, bits, _stream(dev)))
+    _run(index, load().awq_kv_read, *arrays, slots.data_ptr(), k.data_ptr(), v.data_ptr(), T, H, head_dim, pages, page,
+         bits)
     return k, v
 
 
@@ -258,11 +286,11 @@ def awq_kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, len
     bound on the lengths (0: the table's width), workspace uint8 of
     awq_kv_attention_workspace_bytes bytes (allocated unless given)."""
     _need_rows(q, "q")
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(lengths, "lengths", torch.int32, 1)
+    index = q.get_device()
+    _like(page_table, "page_table", torch.int32, 2, index)
+    _like(lengths, "lengths", torch.int32, 1, index)
     B, Hq, D = q.shape
-    dev = q.device
-    pages, Hkv, page, bits = _cache_shape(cache, D, dev)
+    arrays, pages, Hkv, page, bits = _cache_args(cache, D, index)
     if page_table.shape[0] != B or lengths.shape[0] != B:
         raise ValueError("page_table must be int32 [B][width] and lengths int32 [B]")
     if Hq % Hkv:
@@ -270,26 +298,18 @@ def awq_kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, len
     if max_len < 0:
         raise ValueError(f"max_len must be >= 0, got {max_len}")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float16, device=dev)
+        out = torch.empty((B, Hq, D), dtype=torch.float16, device=q.device)
     else:
-        _need(out, "out", torch.float16, 3)
+        _like(out, "out", torch.float16, 3, index)
         if out.shape != q.shape:
             raise ValueError("out must be fp16 [B][Hq][head_dim]")
     width = page_table.shape[1]
     bound = min(max_len, width * page) if max_len else width * page
     lib = load()
-    need = lib.awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bound)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _on(dev, page_table=page_table, lengths=lengths, out=out, workspace=workspace)
-    with torch.cuda.device(dev):
-        check(lib.awq_kv_attention(q.data_ptr(), _token_stride(q), cache["k_codes"].data_ptr(),
-                                   cache["k_params"].data_ptr(), cache["v_codes"].data_ptr(),
-                                   cache["v_params"].data_ptr(), page_table.data_ptr(), width, lengths.data_ptr(),
-                                   out.data_ptr(), B, Hq, Hkv, D, pages, page, bits,
-                                   D ** -0.5 if scale is None else scale, max_len, _ptr(workspace),
-                                   0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                   _stream(dev)))
+    ws, ws_bytes, _keep = _scratch(workspace, lib.awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bound), q.device)
+    _run(index, lib.awq_kv_attention, q.data_ptr(), _token_stride(q), *arrays, page_table.data_ptr(), width,
+         lengths.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, pages, page, bits, D ** -0.5 if scale is None else scale,
+         max_len, ws, ws_bytes)
     return out
 
 
