@@ -549,14 +549,14 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
  *   out         device fp16 [B][Hq][D]
  *   max_len     host bound on the lengths (0: table_width * page): the split
  *               over the length is made for it.  At most AWQ_MAX_KV_LENGTH
- *   workspace   device, >= awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, the
- *               bound) bytes; it needs no clearing and keeps nothing
+ *   workspace   device, >= awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bits,
+ *               the bound) bytes; it needs no clearing and keeps nothing
  * Scores, softmax statistics and sums are fp32; a weight p_t enters the
  * products with 22 bits.  Chunks of a long sequence are joined in order, so the
  * result does not depend on timing.
  * Requires D 64, 128 or 256, Hq a multiple of Hkv, 1 <= B <= 65535, finite scale.
  */
-size_t awq_kv_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t max_len);
+size_t awq_kv_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t bits, int64_t max_len);
 int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const void* k_params, const void* v_codes,
                      const void* v_params, const int32_t* page_table, int64_t table_width, const int32_t* lengths,
                      void* out, int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t pages, int32_t page,

@@ -85,16 +85,17 @@ def test_workspaces():
     for entry, need in (("awq_moe_plan", awq.awq_moe_workspace_bytes(5, 8, 2)),
                         ("awq_moe_route", awq.awq_moe_workspace_bytes(5, 8, 2)),
                         ("awq_gemm_grouped", awq.awq_gemm_grouped_workspace_bytes(10, 256, True)),
-                        ("awq_kv_attention", awq.awq_kv_attention_workspace_bytes(3, 8, 2, 128, 1024))):
+                        ("awq_kv_attention", awq.awq_kv_attention_workspace_bytes(3, 8, 2, 128, 4, 1024))):
         assert need > 0 and need % 256 == 0
         assert call(entry, workspace_bytes=need - 1) == WS_SMALL
     assert awq.awq_gemm_grouped_workspace_bytes(10, 256, True) == 10 * 256 * 2
     assert awq.awq_gemm_grouped_workspace_bytes(10, 256, False) == 0
     assert awq.awq_gemm_grouped_workspace_bytes(10, 100, True) == 0
     assert awq.awq_moe_workspace_bytes(0, 8, 2) == 0 and awq.awq_moe_workspace_bytes(5, 8, 65) == 0
-    assert awq.awq_kv_attention_workspace_bytes(1, 8, 8, 128, 16) == 0  # one chunk: nothing to join
-    assert awq.awq_kv_attention_workspace_bytes(1, 8, 3, 128, 1000) == 0
-    assert awq.awq_kv_attention_workspace_bytes(1, 8, 8, 96, 1000) == 0
+    assert awq.awq_kv_attention_workspace_bytes(1, 8, 8, 128, 4, 16) == 0  # one chunk: nothing to join
+    assert awq.awq_kv_attention_workspace_bytes(1, 8, 3, 128, 4, 1000) == 0
+    assert awq.awq_kv_attention_workspace_bytes(1, 8, 8, 128, 3, 1000) == 0
+    assert awq.awq_kv_attention_workspace_bytes(1, 8, 8, 96, 4, 1000) == 0
     assert lib.awq_kv_codes_bytes(4, 2, 16, 128, 4) == 4 * 2 * 16 * 64
     assert lib.awq_kv_codes_bytes(4, 2, 16, 128, 8) == 4 * 2 * 16 * 128
     assert lib.awq_kv_params_bytes(4, 2, 16) == 4 * 2 * 16 * 4

@@ -60,7 +60,7 @@ SIGNATURES = {
                                     c_i32, c_i32, c_vp]),
     "awq_kv_read": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_i64, c_i32, c_i32,
                                    c_vp]),
-    "awq_kv_attention_workspace_bytes": (c_size, [c_i64, c_i32, c_i32, c_i32, c_i64]),
+    "awq_kv_attention_workspace_bytes": (c_size, [c_i64, c_i32, c_i32, c_i32, c_i32, c_i64]),
     "awq_kv_attention": (ctypes.c_int, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i32,
                                         c_i32, c_i32, c_i64, c_i32, c_i32, ctypes.c_float, c_i64, c_vp, c_size, c_vp]),
     "awq_status_string": (ctypes.c_char_p, [ctypes.c_int]),

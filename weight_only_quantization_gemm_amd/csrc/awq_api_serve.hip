@@ -204,11 +204,11 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
   AWQ_GUARD_END
 }
 
-size_t awq_kv_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t max_len) {
+size_t awq_kv_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t bits, int64_t max_len) {
   if (B < 1 || B > 65535 || Hkv < 1 || Hkv > 1024 || Hq < Hkv || Hq % Hkv != 0 || Hq > 65536 ||
-      (D != 64 && D != 128 && D != 256) || max_len < 1 || max_len > AWQ_MAX_KV_LENGTH)
+      (D != 64 && D != 128 && D != 256) || (bits != 4 && bits != 8) || max_len < 1 || max_len > AWQ_MAX_KV_LENGTH)
     return 0;
-  return (awq::kv_attention_workspace(B, Hkv, Hq / Hkv, D, max_len) + 255) / 256 * 256;
+  return (awq::kv_attention_workspace(B, Hkv, Hq / Hkv, D, bits, max_len) + 255) / 256 * 256;
 }
 
 int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const void* k_params, const void* v_codes,
@@ -235,7 +235,7 @@ int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const
   AWQ_REQUIRE(max_len >= 0 && most <= AWQ_MAX_KV_LENGTH, AWQ_ERROR_INVALID_VALUE,
               "a longest length of %lld tokens: at most 2^25 are served (give max_len)", (long long)most);
   AWQ_REQUIRE(std::isfinite(scale), AWQ_ERROR_INVALID_VALUE, "scale must be finite");
-  const size_t need = awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, most);
+  const size_t need = awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bits, most);
   AWQ_REQUIRE(workspace || need == 0, AWQ_ERROR_INVALID_VALUE, "workspace must not be NULL (%zu bytes needed)", need);
   if (int st = check_aligned({{q, "q"}, {k_codes, "k_codes"}, {k_params, "k_params"}, {v_codes, "v_codes"},
                               {v_params, "v_params"}, {page_table, "page_table"}, {lengths, "lengths"}, {out, "out"},

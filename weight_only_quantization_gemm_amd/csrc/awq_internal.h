@@ -121,7 +121,7 @@ hipError_t launch_kv_write(const void* k, const void* v, int64_t k_stride, int64
                            KvHalf kc, KvHalf vc, int64_t T, int D, int bits, KvShape sh, hipStream_t st);
 hipError_t launch_kv_read(KvHalf kc, KvHalf vc, const int32_t* slots, void* k, void* v, int64_t T, int D, int bits,
                           KvShape sh, hipStream_t st);
-size_t kv_attention_workspace(int64_t B, int64_t Hkv, int ratio, int D, int64_t max_len);
+size_t kv_attention_workspace(int64_t B, int64_t Hkv, int ratio, int D, int bits, int64_t max_len);
 hipError_t launch_kv_attention(const void* q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* table,
                                int64_t width, const int32_t* lengths, int64_t B, int ratio, int D, int bits,
                                float scale, int64_t max_len, KvShape sh, void* out, void* ws, hipStream_t st);

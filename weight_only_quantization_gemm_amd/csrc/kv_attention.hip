@@ -31,7 +31,6 @@
 #include "kv_common.h"
 #include "mfma_pipe.h"
 
-#include <cstdlib>
 namespace awq {
 
 constexpr int kAttWaves = 4;
@@ -70,8 +69,7 @@ struct AttStage {
   static constexpr int HALF = kAttStep * RB, NI = HALF / 1024;  // bytes, 1 KB loads of keys (and of values)
   static constexpr int BYTES = 2 * HALF + 256, LOADS = 2 * NI + 1;
   static constexpr int KW = RB / 16;                     // words of a lane's quarter of a key row
-  static constexpr int S = 2;                            // stages of a ring
-  static constexpr int RING = S * BYTES;
+  static constexpr int RING = 2 * BYTES;                  // (three stages cost a block per compute unit: 75 us against 70)
   static __host__ __device__ constexpr int slot_xor(int r) { return (r / (256 / RB)) & (PIECES - 1); }
 };
 
@@ -138,9 +136,7 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
   };
   const int steps = (count + kAttStep - 1) / kAttStep;
   const int turns = steps > wave ? (steps - wave + kAttWaves - 1) / kAttWaves : 0;
-#pragma unroll
-  for (int s = 0; s < A::S - 1; ++s)
-    if (s < turns) issue(wave + s * kAttWaves, s);
+  if (turns > 0) issue(wave, 0);
 
   // q: columns past the block's heads repeat the last one and are never stored.  A negative
   // factor goes to q's sign, so that larger sums are larger scores; one of 0 is taken as
@@ -325,23 +321,18 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
     }
   };
 
-  int cur = 0, nxt = A::S - 1;
   for (int j = 0; j < turns; ++j) {
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads of the slot refilled now are done
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads of the stage refilled now are done
     __builtin_amdgcn_sched_barrier(0);
     const int i = wave + j * kAttWaves;
-    if (j + A::S - 1 < turns) {
-      issue(i + (A::S - 1) * kAttWaves, nxt);
-      nxt = nxt + 1 == A::S ? 0 : nxt + 1;
-      wait_vmcnt<(A::S - 1) * A::LOADS>();
-    } else if (A::S == 3 && j + 1 < turns) {
+    if (j + 1 < turns) {
+      issue(i + kAttWaves, (j + 1) & 1);
       wait_vmcnt<A::LOADS>();
     } else {
       wait_vmcnt<0>();
     }
     __builtin_amdgcn_sched_barrier(0);
-    compute(i, ring + cur * A::BYTES);
-    cur = cur + 1 == A::S ? 0 : cur + 1;
+    compute(i, ring + (j & 1) * A::BYTES);
   }
   __syncthreads();  // the rings become the place of the sum
 
@@ -449,19 +440,29 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
   out[head * D + d] = (f16)(sum > 0.f ? acc / sum : 0.f);
 }
 
-// Tokens of a chunk: as many as leave about eight blocks for each of the 256
-// compute units, from one step of every wave (128) to what a wave's lanes
-// hold the pages of (1024).
-static int att_chunk(int64_t B, int64_t Hkv, int ratio, int64_t max_len) {
+// Tokens of a chunk, a power of two of at least one step of every wave (128).  A
+// chunk costs a block's start (three dependent loads) and end (the joins) beside
+// its steps, so chunks grow to 512 tokens while there are more than 512 blocks,
+// and on to 4096 while there are more than about one and a half times what the
+// compute units hold at once (by the rows' bytes, which size the ring).  Measured,
+// us at chunks of 128 / 256 / 512 / 1024 / 2048 / 4096 tokens: one sequence of
+// 30000, 8 heads: 30.4 / 22.4 / 18.9; 16 of up to 2000: 20.9 / 17.6 / 16.4 / 17.9;
+// 4 of up to 5000, 32 heads: -/ 25.8 / 22.3 / 24.6 / 32.1 / 41.7; 64 of up to 6000,
+// 8 heads: - / - / 80.6 / 69.7 / 71 / 89; 8-bit rows of 256 channels, 4 of up to
+// 9000: 58.2 / 43.8 / 35.1 / 28.8.  Up to 512 tokens one block does without a
+// join: 9.4 us where four chunks and a second launch take 9.5.
+static int att_chunk(int64_t B, int64_t Hkv, int ratio, int row_bytes, int64_t max_len) {
   const int64_t rows = B * Hkv * ((ratio + kAttHeads - 1) / kAttHeads);
-  int chunk = kAttStep * kAttWaves;
-  const char* ev = getenv("CHT"); const int target = ev ? atoi(ev) : 2048;
-  while (chunk < 1024 * kAttWindows && rows * ((max_len + chunk - 1) / chunk) > target) chunk *= 2;
+  const int64_t most = row_bytes <= 64 ? 1536 : (row_bytes == 128 ? 1024 : 512);
+  auto blocks = [&](int chunk) { return rows * ((max_len + chunk - 1) / chunk); };
+  int chunk = max_len <= 512 ? 512 : kAttStep * kAttWaves;
+  while (chunk < 512 && blocks(chunk) > 512) chunk *= 2;
+  while (chunk >= 512 && chunk < 1024 * kAttWindows && blocks(chunk) > most) chunk *= 2;
   return chunk;
 }
 
-size_t kv_attention_workspace(int64_t B, int64_t Hkv, int ratio, int D, int64_t max_len) {
-  const int chunk = att_chunk(B, Hkv, ratio, max_len);
+size_t kv_attention_workspace(int64_t B, int64_t Hkv, int ratio, int D, int bits, int64_t max_len) {
+  const int chunk = att_chunk(B, Hkv, ratio, D * bits / 8, max_len);
   const int64_t chunks = (max_len + chunk - 1) / chunk;
   return chunks > 1 ? (size_t)(B * Hkv * ratio * chunks * (D + 2)) * sizeof(float) : 0;
 }
@@ -470,7 +471,7 @@ template <int D, int BITS>
 static hipError_t attention_launch(const void* q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* table,
                                    int64_t width, const int32_t* lengths, int64_t B, int ratio, float scale,
                                    int64_t max_len, KvShape sh, void* out, float* ws, hipStream_t st) {
-  const int chunk = att_chunk(B, sh.heads, ratio, max_len);
+  const int chunk = att_chunk(B, sh.heads, ratio, D * BITS / 8, max_len);
   const int chunks = max_len > 0 ? (int)((max_len + chunk - 1) / chunk) : 1;
   const int heads = ratio < kAttHeads ? ratio : kAttHeads;
   const size_t sum = (size_t)(kAttWaves * heads * D + (3 * kAttWaves + 1) * kAttHeads) * sizeof(float);

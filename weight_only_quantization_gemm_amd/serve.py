@@ -272,8 +272,8 @@ def awq_kv_read(cache: dict, slots: torch.Tensor, head_dim: int):
     return k, v
 
 
-def awq_kv_attention_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, max_len: int) -> int:
-    return int(load().awq_kv_attention_workspace_bytes(B, Hq, Hkv, head_dim, max_len))
+def awq_kv_attention_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, bits: int, max_len: int) -> int:
+    return int(load().awq_kv_attention_workspace_bytes(B, Hq, Hkv, head_dim, bits, max_len))
 
 
 def awq_kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -306,7 +306,7 @@ def awq_kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, len
     width = page_table.shape[1]
     bound = min(max_len, width * page) if max_len else width * page
     lib = load()
-    ws, ws_bytes, _keep = _scratch(workspace, lib.awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bound), q.device)
+    ws, ws_bytes, _keep = _scratch(workspace, lib.awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bits, bound), q.device)
     _run(index, lib.awq_kv_attention, q.data_ptr(), _token_stride(q), *arrays, page_table.data_ptr(), width,
          lengths.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, pages, page, bits, D ** -0.5 if scale is None else scale,
          max_len, ws, ws_bytes)
