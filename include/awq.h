@@ -467,13 +467,21 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
  * the groups stay on the device; the result does not depend on timing.
  * Requires R, x_rows in [1, 2^24] (x_rows >= R without rows), E in
  * [1, AWQ_MAX_EXPERTS], bits 4 or 3, group == AWQ_GROUP, K % group == 0,
- * K <= 2^17.
+ * K <= 2^17, and a batch one launch covers (at 256 rows of an expert or more on
+ * average R * N < 2^39; a scaled batch R < 2^24).  x, y and the workspace do not
+ * overlap.
  */
 size_t awq_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int32_t scaled);
 int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t top_k, const int32_t* offsets,
                      const float* s, const void* packed, const void* scales, const void* zeros, void* y, int64_t R,
                      int32_t E, int64_t N, int64_t K, int32_t group, int32_t bits, void* workspace,
                      size_t workspace_bytes, void* stream);
+
+/* awq_gemm_grouped_kernel -- the kernel awq_gemm_grouped launches for these
+ * sizes, as awq_gemm_kernel says it of the single product: a host-only dry run
+ * (160 bytes always suffice). */
+int awq_gemm_grouped_kernel(int64_t R, int32_t E, int64_t N, int64_t K, int32_t group, int32_t bits, char* out,
+                            size_t out_bytes);
 
 /*
  * awq_moe_combine -- out[t] = sum_j weights[t][j] * y[pos[t * top_k + j]], in
@@ -554,7 +562,8 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
  * Scores, softmax statistics and sums are fp32; a weight p_t enters the
  * products with 22 bits.  Chunks of a long sequence are joined in order, so the
  * result does not depend on timing.
- * Requires D 64, 128 or 256, Hq a multiple of Hkv, 1 <= B <= 65535, finite scale.
+ * Requires D 64, 128 or 256, Hq a multiple of Hkv, 1 <= B <= 65535,
+ * B * Hq * D < 2^32, finite scale.
  */
 size_t awq_kv_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t bits, int64_t max_len);
 int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const void* k_params, const void* v_codes,

@@ -61,7 +61,7 @@ BAD = {
                       dict(renormalize=2)],
     "awq_gemm_grouped": [dict(R=0), dict(x_rows=0), dict(x_rows=9, rows=None), dict(top_k=0), dict(E=0), dict(E=1025),
                          dict(N=0), dict(K=100), dict(group=64), dict(bits=8), dict(R=(1 << 24) + 1), dict(K=1 << 21), dict(K=(1 << 17) + 128),
-                         dict(R=1 << 24, N=1 << 20, s=None)],
+                         dict(R=1 << 24, N=1 << 20, s=None), dict(R=1 << 24, s=FAKE)],
     "awq_moe_combine": [dict(T=0), dict(R=0), dict(top_k=0), dict(N=12), dict(N=0), dict(T=1 << 24, N=1 << 20)],
     "awq_kv_write": [dict(T=0), dict(T=(1 << 22) + 1), dict(T=1 << 22, H=64, k_stride=8192, v_stride=8192), dict(H=0), dict(H=1025), dict(D=96), dict(page=24), dict(page=8),
                      dict(page=2048), dict(pages=0), dict(pages=1 << 27), dict(bits=3), dict(k_stride=128),
@@ -100,6 +100,33 @@ def test_workspaces():
     assert lib.awq_kv_codes_bytes(4, 2, 16, 128, 8) == 4 * 2 * 16 * 128
     assert lib.awq_kv_params_bytes(4, 2, 16) == 4 * 2 * 16 * 4
     assert lib.awq_kv_codes_bytes(4, 2, 15, 128, 4) == 0 and lib.awq_kv_params_bytes(0, 2, 16) == 0
+
+
+@pytest.mark.parametrize("R,E,N,K,bits,kernel", [
+    (2, 8, 11008, 4096, 4, "grouped_ring_kernel<4,2,2> block=256 grid=688"),      # one token, two choices
+    (8, 8, 64, 128, 3, "grouped_ring_kernel<3,2,2> block=64 grid=16"),            # one group: one wave
+    (270, 64, 2048, 1408, 3, "grouped_ring_kernel<3,4,2> block=128 grid=2432"),
+    (640, 64, 2048, 2048, 4, "grouped_ring_kernel<4,4,2> block=64 grid=3200"),    # ten rows an expert
+    (641, 64, 2048, 2048, 4, "grouped_pipe_kernel<4,2,1,3> block=256 grid=640"),
+    (320, 8, 4096, 11008, 4, "grouped_ring_kernel<4,4,2> block=128 grid=1728"),   # too few column tiles for the pipeline
+    (321, 8, 4096, 11008, 4, "grouped_pipe_kernel<4,2,1,3> block=256 grid=256"),
+    (3071, 8, 11008, 4096, 3, "grouped_pipe_kernel<3,2,1,3> block=256 grid=2432"),
+    (12000, 8, 11008, 4096, 4, "grouped_pipe_kernel<4,4,2,3> block=512 grid=2432"),
+    (12000, 8, 1000, 11008, 3, "grouped_pipe_kernel<3,4,2,2> block=512 grid=256"),  # long rows: two stages
+    (12000, 8, 1000, 20480, 4, "grouped_pipe_kernel<4,2,1,3> block=256 grid=896"),  # no 256-row stages left
+    (12000, 8, 1000, 24576, 4, "grouped_pipe_kernel<4,2,1,2> block=256 grid=896"),
+    (12000, 8, 1000, 65536, 4, "grouped_ring_kernel<4,4,2> block=64 grid=12112"),
+    (12000, 8, 1000, 131072, 4, "grouped_ring_kernel<4,2,2> block=64 grid=24224"),
+    (1 << 24, 64, 32768 - 256, 4096, 4, "grouped_pipe_kernel<4,4,2,3> block=512 grid=8331136"),
+])
+def test_grouped_dispatch(R, E, N, K, bits, kernel):
+    assert awq.awq_gemm_grouped_kernel(R, E, N, K, bits=bits) == kernel
+
+
+def test_grouped_dispatch_refuses_what_the_product_refuses():
+    for kw in (dict(R=0), dict(E=0), dict(N=0), dict(K=100), dict(bits=5), dict(R=1 << 24, N=1 << 20), dict(K=1 << 18)):
+        with pytest.raises(awq.AwqError):
+            awq.awq_gemm_grouped_kernel(**{**dict(R=10, E=8, N=64, K=256, bits=4), **kw})
 
 
 def test_cache_buffers_have_the_documented_sizes():

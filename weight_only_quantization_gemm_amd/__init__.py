@@ -36,6 +36,7 @@ from .serve import (  # noqa: F401
     KV_BITS,
     KV_HEAD_DIMS,
     awq_gemm_grouped,
+    awq_gemm_grouped_kernel,
     awq_gemm_grouped_workspace_bytes,
     awq_kv_attention,
     awq_kv_attention_workspace_bytes,

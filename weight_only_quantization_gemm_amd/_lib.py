@@ -53,6 +53,7 @@ SIGNATURES = {
     "awq_gemm_grouped_workspace_bytes": (c_size, [c_i64, c_i64, c_i32]),
     "awq_gemm_grouped": (ctypes.c_int, [c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32,
                                         c_i64, c_i64, c_i32, c_i32, c_vp, c_size, c_vp]),
+    "awq_gemm_grouped_kernel": (ctypes.c_int, [c_i64, c_i32, c_i64, c_i64, c_i32, c_i32, ctypes.c_char_p, c_size]),
     "awq_moe_combine": (ctypes.c_int, [c_vp, c_i64, c_vp, c_vp, c_i64, c_i32, c_i64, c_vp, c_vp]),
     "awq_kv_codes_bytes": (c_size, [c_i64, c_i32, c_i32, c_i32, c_i32]),
     "awq_kv_params_bytes": (c_size, [c_i64, c_i32, c_i32]),

@@ -3,6 +3,7 @@
 // no entry point allocates memory, synchronises the device or lets a C++
 // exception escape.
 #include <cmath>
+#include <cstdio>
 
 #include "awq.h"
 #include "awq_api_util.h"
@@ -119,7 +120,7 @@ int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t
   AWQ_REQUIRE(top_k >= 1, AWQ_ERROR_INVALID_VALUE, "top_k must be >= 1 (got %d)", top_k);
   AWQ_REQUIRE(x_rows >= 1 && x_rows <= AWQ_MAX_PAIRS && (rows || x_rows >= R), AWQ_ERROR_INVALID_VALUE,
               "x_rows=%lld outside [1, 2^24], or fewer than R without rows", (long long)x_rows);
-  AWQ_REQUIRE(awq::gemm_grouped_fits(R, E, N), AWQ_ERROR_INVALID_VALUE, "R=%lld rows of N=%lld exceed one launch",
+  AWQ_REQUIRE(awq::gemm_grouped_fits(R, E, N, K, bits, s != nullptr), AWQ_ERROR_INVALID_VALUE, "R=%lld rows of N=%lld exceed one launch",
               (long long)R, (long long)N);
   const size_t need = awq_gemm_grouped_workspace_bytes(R, K, s != nullptr);
   AWQ_REQUIRE(workspace || need == 0, AWQ_ERROR_INVALID_VALUE, "workspace must not be NULL (%zu bytes needed)", need);
@@ -131,6 +132,28 @@ int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t
   return device_status(awq::launch_gemm_grouped(x, x_rows, rows, top_k, offsets, s, packed, scales, zeros, y, R, E, N, K,
                                                 bits, workspace, as_stream(stream)),
                        "awq_gemm_grouped");
+  AWQ_GUARD_END
+}
+
+int awq_gemm_grouped_kernel(int64_t R, int32_t E, int64_t N, int64_t K, int32_t group, int32_t bits, char* out,
+                            size_t out_bytes) {
+  AWQ_GUARD_BEGIN
+  AWQ_REQUIRE(out && out_bytes > 0, AWQ_ERROR_INVALID_VALUE, "out must not be NULL or empty");
+  out[0] = 0;
+  int st = check_layer(N, K, group);
+  if (st == AWQ_OK) st = check_bits(bits);
+  if (st != AWQ_OK) return st;
+  AWQ_REQUIRE(K <= kMaxGroupedK && R >= 1 && R <= AWQ_MAX_PAIRS && E >= 1 && E <= AWQ_MAX_EXPERTS &&
+                  awq::gemm_grouped_fits(R, E, N, K, bits, false),
+              AWQ_ERROR_INVALID_VALUE, "R=%lld E=%d N=%lld K=%lld: sizes awq_gemm_grouped refuses", (long long)R, E,
+              (long long)N, (long long)K);
+  awq::KernelPlan plan{};
+  awq::install_plan(&plan);
+  const hipError_t e = awq::launch_gemm_grouped(nullptr, R, nullptr, 1, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                                R, E, N, K, bits, nullptr, nullptr);
+  awq::install_plan(nullptr);
+  snprintf(out, out_bytes, "%s", plan.text);
+  return device_status(e, "awq_gemm_grouped_kernel");
   AWQ_GUARD_END
 }
 
@@ -224,6 +247,8 @@ int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const
   AWQ_REQUIRE(B >= 1 && B <= 65535, AWQ_ERROR_INVALID_VALUE, "B=%lld outside [1, 65535]", (long long)B);
   AWQ_REQUIRE(Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536, AWQ_ERROR_INVALID_VALUE,
               "Hq=%d must be a multiple of Hkv=%d, at most 65536", Hq, Hkv);
+  AWQ_REQUIRE(B * Hq * D < (int64_t(1) << 32), AWQ_ERROR_INVALID_VALUE, "B * Hq * D = %lld: below 2^32 is needed",
+              (long long)(B * Hq * D));
   AWQ_REQUIRE(q_stride >= (int64_t)Hq * D && q_stride % 8 == 0 && q_stride < (int64_t(1) << 31),
               AWQ_ERROR_INVALID_VALUE,
               "a q stride of %lld elements: a multiple of 8, at least Hq * D and below 2^31, is needed",

@@ -107,7 +107,7 @@ hipError_t launch_moe_combine(const void* y, int64_t R, const int32_t* pos, cons
                               int64_t N, void* out, hipStream_t st);
 
 // grouped.hip: products grouped by expert (ws: R x K halfs when s is given)
-bool gemm_grouped_fits(int64_t R, int64_t E, int64_t N);
+bool gemm_grouped_fits(int64_t R, int64_t E, int64_t N, int64_t K, int bits, bool scaled);
 hipError_t launch_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
                                const float* s, const void* packed, const void* scales, const void* zeros, void* y,
                                int64_t R, int E, int64_t N, int64_t K, int bits, void* ws, hipStream_t st);

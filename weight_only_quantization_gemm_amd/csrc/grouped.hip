@@ -520,10 +520,6 @@ __global__ __launch_bounds__(256 * WMW) void grouped_pipe_kernel(
 // The most tiles of BM rows that R rows in E groups can make.
 static int64_t row_tiles(int64_t R, int64_t E, int64_t BM) { return (R + (E < R ? E : R) * (BM - 1)) / BM; }
 
-bool gemm_grouped_fits(int64_t R, int64_t E, int64_t N) {
-  return (N + 15) / 16 * row_tiles(R, E, 16) < (int64_t(1) << 23);  // blocks; a grid has at most 2^32 threads
-}
-
 constexpr int64_t kGrpLds = 160 * 1024;
 
 template <int BITS, int AB, int WMW, int STAGES>
@@ -534,6 +530,8 @@ static hipError_t pipe_stages(const f16* x, int64_t x_rows, const int32_t* rows,
   const int64_t nt = (N + kGBN - 1) / kGBN, tiles = nt * row_tiles(R, E, S::BM);
   const size_t lds = (size_t)(STAGES * S::STAGE + grouped_meta_bytes(K / kGroup));
   const dim3 grid((unsigned)((tiles + 127) / 128 * 128)), block(256 * WMW);
+  if (KernelPlan* p = active_plan())
+    return plan_record(p, "grouped_pipe_kernel<%d,%d,%d,%d> block=%u grid=%u", BITS, AB, WMW, STAGES, block.x, grid.x);
   grouped_pipe_kernel<BITS, AB, WMW, STAGES><<<grid, block, lds, st>>>(
       x, x_rows, rows, top_k, offsets, reinterpret_cast<const uint32_t*>(packed), reinterpret_cast<const f16*>(scales),
       reinterpret_cast<const uint8_t*>(zeros), reinterpret_cast<f16*>(y), (int)R, E, N, K, (int)nt, (int)tiles);
@@ -569,6 +567,8 @@ static hipError_t ring_launch(const f16* x, int64_t x_rows, const int32_t* rows,
   // experts of 2048 x 1408: 23.0, 23.5, 30.0, 36.7 us.
   int waves = 1;
   while (waves < 8 && 2 * waves <= G && blocks * waves < 2500) waves *= 2;
+  if (KernelPlan* p = active_plan())
+    return plan_record(p, "grouped_ring_kernel<%d,%d,%d> block=%d grid=%lld", BITS, RW, S, 64 * waves, (long long)blocks);
   grouped_ring_kernel<BITS, RW, S><<<dim3((unsigned)blocks), dim3(64 * waves), RingShape<BITS, RW, S>::bytes(waves, G),
                                      st>>>(
       x, x_rows, rows, top_k, offsets, reinterpret_cast<const uint32_t*>(packed), reinterpret_cast<const f16*>(scales),
@@ -598,11 +598,24 @@ static Kernel grouped_choice(int64_t R, int64_t E, int64_t N, int64_t K, int bit
   return R > E && RingShape<4, 4, 2>::bytes(8, (int)G) <= kGrpLds ? Kernel::ring4 : Kernel::ring2;
 }
 
+// Whether the chosen kernel's grid (2^32 threads at most) covers the batch.
+bool gemm_grouped_fits(int64_t R, int64_t E, int64_t N, int64_t K, int bits, bool scaled) {
+  if (scaled && R >= (int64_t(1) << 24)) return false;  // a block of 256 threads per row
+  const int64_t nt = (N + kGBN - 1) / kGBN;
+  switch (grouped_choice(R, E, N, K, bits)) {
+    case Kernel::ring2: return (N + 31) / 32 * row_tiles(R, E, 16) < (int64_t(1) << 23);
+    case Kernel::ring4: return (N + 63) / 64 * row_tiles(R, E, 16) < (int64_t(1) << 23);
+    case Kernel::rows64: return nt * row_tiles(R, E, 64) + 127 < (int64_t(1) << 24);
+    case Kernel::rows256: return nt * row_tiles(R, E, 256) + 127 < (int64_t(1) << 23);
+  }
+  return false;
+}
+
 hipError_t launch_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
                                const float* s, const void* packed, const void* scales, const void* zeros, void* y,
                                int64_t R, int E, int64_t N, int64_t K, int bits, void* ws, hipStream_t st) {
   const f16* xp = reinterpret_cast<const f16*>(x);
-  if (s != nullptr) {
+  if (s != nullptr && active_plan() == nullptr) {
     scale_rows_kernel<<<dim3((unsigned)R), dim3(256), 0, st>>>(xp, x_rows, rows, top_k, offsets, s, E, (int)R, K,
                                                                reinterpret_cast<f16*>(ws));
     if (hipError_t e = hipGetLastError()) return e;

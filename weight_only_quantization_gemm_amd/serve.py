@@ -11,6 +11,7 @@ allocation.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -154,7 +155,7 @@ def awq_gemm_grouped(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
             raise ValueError("s must be float32 [E][K]")
         need = lib.awq_gemm_grouped_workspace_bytes(R, K, 1)
     if out is None:
-        out = torch.empty((R, N), dtype=torch.float16, device=x.device)
+        out = x.new_empty((R, N))
     else:
         _like(out, "out", torch.float16, 2, index)
         if out.shape != (R, N):
@@ -163,6 +164,14 @@ def awq_gemm_grouped(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
     _run(index, lib.awq_gemm_grouped, x.data_ptr(), x_rows, _ptr(rows), top_k, offsets.data_ptr(), _ptr(s),
          packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), out.data_ptr(), R, E, N, K, group, bits, ws, ws_bytes)
     return out
+
+
+def awq_gemm_grouped_kernel(R: int, E: int, N: int, K: int, bits: int = 4, group: int = GROUP) -> str:
+    """The kernel awq_gemm_grouped launches for R rows over E experts of N x K (a host-only dry run
+    of its dispatch: template arguments, block and grid)."""
+    buf = ctypes.create_string_buffer(160)
+    check(load().awq_gemm_grouped_kernel(R, E, N, K, group, bits, buf, len(buf)))
+    return buf.value.decode()
 
 
 def awq_moe_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
@@ -178,7 +187,7 @@ def awq_moe_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
     if pos.shape[0] != T * top_k:
         raise ValueError("pos must have T * top_k entries")
     if out is None:
-        out = torch.empty((T, N), dtype=torch.float16, device=y.device)
+        out = y.new_empty((T, N))
     else:
         _like(out, "out", torch.float16, 2, index)
         if out.shape != (T, N):
@@ -220,40 +229,32 @@ def _cache_args(cache: dict, head_dim: int, index: int):
     return (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), pages, heads, page, bits
 
 
-def _need_rows(t: torch.Tensor, name: str) -> None:
-    """fp16 [T][H][D] whose rows are contiguous within a token; any stride between tokens."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor (libawq has no CPU path)")
-    if t.dtype != torch.float16:
-        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+def _rows(t: torch.Tensor, name: str):
+    """(T, H, D, elements from one token to the next) of fp16 [T][H][D] whose rows are contiguous
+    within a token; any stride between tokens (a single token has no next)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.float16 and t.dim() == 3):
+        _need(t, name, torch.float16, 3)
+    T, H, D = t.shape
+    token, head, channel = t.stride()
+    if channel != 1 or (H > 1 and head != D):
         raise ValueError(f"{name} must be contiguous within each token (heads, then channels)")
-
-
-def _token_stride(t: torch.Tensor) -> int:
-    """Elements from one token's rows to the next (a single token has no next)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return T, H, D, token if T > 1 else H * D
 
 
 def awq_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: dict) -> dict:
     """Quantises T tokens' keys and values (fp16 [T][heads][head_dim]; slices of a fused q/k/v
     product need no copy) into their slots (int32 [T], page number * page + place; one outside
     the cache, such as -1 for padding, is not written).  Returns the cache."""
-    _need_rows(k, "k")
-    _need_rows(v, "v")
+    T, H, D, k_stride = _rows(k, "k")
+    v_stride = _rows(v, "v")[3]
     index = k.get_device()
     _like(slots, "slots", torch.int32, 1, index)
-    T, H, D = k.shape
     if v.shape != k.shape or v.get_device() != index or slots.shape[0] != T:
         raise ValueError("k and v must be fp16 [T][heads][head_dim] on one device, and slots int32 [T]")
     arrays, pages, heads, page, bits = _cache_args(cache, D, index)
     if heads != H:
         raise ValueError(f"k has {H} heads, the cache {heads}")
-    _run(index, load().awq_kv_write, k.data_ptr(), v.data_ptr(), _token_stride(k), _token_stride(v), slots.data_ptr(),
+    _run(index, load().awq_kv_write, k.data_ptr(), v.data_ptr(), k_stride, v_stride, slots.data_ptr(),
          *arrays, T, H, D, pages, page, bits)
     return cache
 
@@ -265,8 +266,8 @@ def awq_kv_read(cache: dict, slots: torch.Tensor, head_dim: int):
     index = slots.get_device()
     arrays, pages, H, page, bits = _cache_args(cache, head_dim, index)
     T = slots.shape[0]
-    k = torch.empty((T, H, head_dim), dtype=torch.float16, device=slots.device)
-    v = torch.empty_like(k)
+    k = cache["k_params"].new_empty((T, H, head_dim))
+    v = k.new_empty((T, H, head_dim))
     _run(index, load().awq_kv_read, *arrays, slots.data_ptr(), k.data_ptr(), v.data_ptr(), T, H, head_dim, pages, page,
          bits)
     return k, v
@@ -285,11 +286,10 @@ def awq_kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, len
     lengths int32 [B] (0: the output row is 0), scale 1/sqrt(head_dim) unless given, max_len a
     bound on the lengths (0: the table's width), workspace uint8 of
     awq_kv_attention_workspace_bytes bytes (allocated unless given)."""
-    _need_rows(q, "q")
+    B, Hq, D, q_stride = _rows(q, "q")
     index = q.get_device()
     _like(page_table, "page_table", torch.int32, 2, index)
     _like(lengths, "lengths", torch.int32, 1, index)
-    B, Hq, D = q.shape
     arrays, pages, Hkv, page, bits = _cache_args(cache, D, index)
     if page_table.shape[0] != B or lengths.shape[0] != B:
         raise ValueError("page_table must be int32 [B][width] and lengths int32 [B]")
@@ -298,7 +298,7 @@ def awq_kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, len
     if max_len < 0:
         raise ValueError(f"max_len must be >= 0, got {max_len}")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float16, device=q.device)
+        out = q.new_empty((B, Hq, D))
     else:
         _like(out, "out", torch.float16, 3, index)
         if out.shape != q.shape:
@@ -307,7 +307,7 @@ def awq_kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, len
     bound = min(max_len, width * page) if max_len else width * page
     lib = load()
     ws, ws_bytes, _keep = _scratch(workspace, lib.awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bits, bound), q.device)
-    _run(index, lib.awq_kv_attention, q.data_ptr(), _token_stride(q), *arrays, page_table.data_ptr(), width,
+    _run(index, lib.awq_kv_attention, q.data_ptr(), q_stride, *arrays, page_table.data_ptr(), width,
          lengths.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, pages, page, bits, D ** -0.5 if scale is None else scale,
          max_len, ws, ws_bytes)
     return out
