@@ -61,17 +61,50 @@ __device__ inline RowTile find_tile(const int32_t* __restrict__ offsets, int E, 
   return {0, 0, 0};
 }
 
-// Pairs 4 s .. 4 s + 3 of 32 channels' three words, as code - zero.
+// The zero point in the forms the unpacking subtracts: of 4-bit codes those of
+// word_minus_zero; of 3-bit codes 1024 + zero, -(128 + zero) and -(16 + zero).
+template <int BITS>
+struct Zero;
+template <>
+struct Zero<4> {
+  ZeroForms f;
+  __device__ __forceinline__ void set(uint32_t z) { f = zero_forms(z); }
+};
+template <>
+struct Zero<3> {
+  f16x2 zb1, nz128, nz16;
+  __device__ __forceinline__ void set(uint32_t z) {
+    zb1 = zero_biased(z);
+    nz128 = as_f16x2(0xD800D800u | (z << 3) | (z << 19));  // 128 has spacing 1/8
+    nz16 = as_f16x2(0xCC00CC00u | (z << 6) | (z << 22));   // 16 has spacing 1/64
+  }
+};
+
+// Eight channels' code - zero, exact, as a matrix-core operand: 8 s .. 8 s + 7 of
+// the 32 channels in `w` (four words, or three).
 template <typename Words>
-__device__ __forceinline__ f16x8 three_bit_pairs(const Words& w, int s, uint32_t bias, ZeroForms zf) {
+__device__ __forceinline__ f16x8 unpack8(const Words& w, int s, uint32_t bias, const Zero<4>& z) {
+  return word_minus_zero(w[s], bias, z.f);
+}
+// 3 bits: fields 0, 1, 2 of a word, or of the word shifted by nine (fields 3, 4),
+// masked where they stand are 1024 + code, 1024 + 8 code and 1024 + 64 code once
+// the bias is or-ed in; a packed subtraction or fma leaves code - zero, exactly.
+template <typename Words>
+__device__ __forceinline__ f16x8 unpack8(const Words& w, int s, uint32_t bias, const Zero<3>& z) {
+  const f16x2 eighth = {(f16)0.125f, (f16)0.125f}, sixty_fourth = {(f16)0.015625f, (f16)0.015625f};
   f16x2 q[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int p = 4 * s + u;
-    const uint32_t bits = p < 15 ? ((w[p / 5] >> (3 * (p % 5))) & 0x00070007u)
-                                 : (((w[0] >> 15) & 0x00010001u) | ((w[1] >> 14) & 0x00020002u) |
-                                    ((w[2] >> 13) & 0x00040004u));
-    q[u] = as_f16x2(bits | bias) - zf.zb1;
+    const int p = 4 * s + u, j = p % 5;
+    if (p == 15) {
+      const uint32_t bits = ((w[0] >> 15) & 0x00010001u) | ((w[1] >> 14) & 0x00020002u) | ((w[2] >> 13) & 0x00040004u);
+      q[u] = as_f16x2(bits | bias) - z.zb1;
+    } else {
+      const uint32_t v = j < 3 ? w[p / 5] : w[p / 5] >> 9;
+      if (j % 3 == 0) q[u] = as_f16x2((v & 0x00070007u) | bias) - z.zb1;
+      else if (j % 3 == 1) q[u] = __builtin_elementwise_fma(as_f16x2((v & 0x00380038u) | bias), eighth, z.nz128);
+      else q[u] = __builtin_elementwise_fma(as_f16x2((v & 0x01C001C0u) | bias), sixty_fourth, z.nz16);
+    }
   }
   return f16x8{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
 }
@@ -255,14 +288,12 @@ __global__ __launch_bounds__(512) void grouped_ring_kernel(
       }
 #pragma unroll
       for (int t = 0; t < RW; ++t) {
-        const ZeroForms zf = zero_forms(z[t]);
+        Zero<BITS> zf;
+        zf.set(z[t]);
         f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          f16x8 b;
-          if constexpr (BITS == 4) b = word_minus_zero(w[t][s], bias, zf);
-          else b = three_bit_pairs(w[t], s, bias, zf);
-          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[u].a[s], b, d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[u].a[s], unpack8(w[t], s, bias, zf), d, 0, 0, 0);
         }
         const float scale = g < G ? sc[t] : 0.f;
 #pragma unroll
@@ -412,7 +443,7 @@ __global__ __launch_bounds__(256 * WMW) void grouped_pipe_kernel(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[a][j][r] = 0.f;
   const uint32_t magic = bias_in_vgpr();
-  ZeroForms zf[S::JB];
+  Zero<BITS> zf[S::JB];
   uint32_t zz[S::JB];
   bool empty[S::JB];
   float sc[S::JB] = {1.f, 1.f};  // scale of the group the accumulators are in units of
@@ -449,7 +480,7 @@ __global__ __launch_bounds__(256 * WMW) void grouped_pipe_kernel(
 #pragma unroll
       for (int j = 0; j < S::JB; ++j) {
         zz[j] = (mz[mrow[j] * P2 + (gr >> 1)] >> (4 * (gr & 1))) & 0xFu;
-        zf[j] = zero_forms(zz[j]);
+        zf[j].set(zz[j]);
         const float was = sc[j], now = (float)reinterpret_cast<const f16*>(msc)[mrow[j] * G + (gr ^ msx[j])];
         sc[j] = now != 0.f ? now : was;
         empty[j] = now == 0.f;
@@ -470,8 +501,7 @@ __global__ __launch_bounds__(256 * WMW) void grouped_pipe_kernel(
     auto unpack = [&](int s, f16x8(&bq)[S::JB]) {
 #pragma unroll
       for (int j = 0; j < S::JB; ++j) {
-        if constexpr (BITS == 4) bq[j] = word_minus_zero(wv[j][s], magic, zf[j]);
-        else bq[j] = three_bit_pairs(wv[j], s, magic, zf[j]);
+        bq[j] = unpack8(wv[j], s, magic, zf[j]);
       }
     };
     f16x8 av[2][NA > 0 ? NA : 1], bq[2][S::JB];

@@ -56,6 +56,9 @@ __host__ __device__ constexpr bool att_times16(int c) {
   return BITS == 4 && (c & 1);
 }
 
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+__device__ inline u16x2 as_u16x2(uint32_t v) { return __builtin_bit_cast(u16x2, v); }
+
 __device__ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); }
 
 // A stage of a wave's ring: 32 tokens' keys, values and parameters, moved
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const f16x2 p = as_f16x2(kp[r]);
-        s[4 * u + r] = fmaf((float)p.y, qz, acc[r]) * (float)p.x;
+        s[4 * u + r] = fmaf(fmaf((float)p.y, qz, acc[r]), (float)p.x, 0.f);  // (fma takes the fp16 operand as it is)
         vp[4 * u + r] = vq[r];
       }
     }
@@ -223,13 +226,15 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
         vp[j] = live ? vp[j] : 0u;
       }
     }
-    float vscale[8], top = s[0], wide = 0.f;
+    // the largest score and the largest value scale (positive: ordered as its bits are)
+    float top = s[0];
+    u16x2 widest = as_u16x2(vp[0]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      vscale[j] = (float)as_f16x2(vp[j]).x;
+    for (int j = 1; j < 8; ++j) {
       top = fmaxf(top, s[j]);
-      wide = fmaxf(wide, vscale[j]);
+      widest = __builtin_elementwise_max(widest, as_u16x2(vp[j]));
     }
+    float wide = (float)__builtin_bit_cast(f16, widest.x);
     // rarely: a new maximum or a larger value scale; every lane then rescales what it holds
     if (__ballot(top > limit || wide > wide_limit)) {
       top = fmaxf(top, __shfl_xor(top, 16, kWave));
@@ -261,9 +266,9 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
     for (int j = 0; j < 8; ++j) {
       const float p = __builtin_amdgcn_exp2f(fmaf(s[j], factor, -ref));
       l += p;
-      const float w = p * vscale[j];
+      const float w = fmaf(p, (float)as_f16x2(vp[j]).x, 0.f);
       whi[j] = (f16)w;
-      wlo[j] = (f16)(w - (float)whi[j]);
+      wlo[j] = (f16)fmaf((float)whi[j], -1.f, w);
     }
     auto mac = [&](u32x4 a, f32x4& acc) {
       const f16x8 af = __builtin_bit_cast(f16x8, a);

@@ -296,17 +296,27 @@ __global__ __launch_bounds__(256) void combine_kernel(const f16* __restrict__ y,
                                                       const int32_t* __restrict__ pos,
                                                       const float* __restrict__ weights, int64_t T, int top_k,
                                                       int64_t N, f16* __restrict__ out) {
-  const int64_t per = N / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= T * per) return;
-  const int64_t t = i / per, c = (i - t * per) * 8;
+  const uint32_t per = (uint32_t)(N / 8), i = blockIdx.x * 256u + threadIdx.x;  // T N / 8 < 2^32 - 256
+  if (i >= (uint64_t)T * per) return;
+  const int64_t t = i / per, c = (int64_t)(i % per) * 8;
   float acc[8] = {};
-  for (int j = 0; j < top_k; ++j) {
-    const int32_t row = pos[t * top_k + j];
-    if (row < 0 || row >= R) continue;
-    const float w = weights[t * top_k + j];
-    const f16x8 v = *reinterpret_cast<const f16x8*>(y + row * N + c);
+  // four rows' loads under way before the first is used
+  for (int j0 = 0; j0 < top_k; j0 += 4) {
+    f16x8 v[4];
+    float w[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) acc[u] = fmaf(w, (float)v[u], acc[u]);
+    for (int k = 0; k < 4; ++k) {
+      const int64_t p = t * top_k + (j0 + k < top_k ? j0 + k : top_k - 1);
+      const int32_t row = pos[p];
+      const bool live = j0 + k < top_k && row >= 0 && row < R;
+      w[k] = live ? weights[p] : 0.f;
+      v[k] = f16x8{};
+      if (live) v[k] = __builtin_nontemporal_load(reinterpret_cast<const f16x8*>(y + row * N + c));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) acc[u] = fmaf(w[k], (float)v[k][u], acc[u]);
   }
   f16x8 o;
 #pragma unroll
