@@ -259,6 +259,23 @@ def test_grouped_scales_of_zero(bits, rows):
     assert np.all(y[:rows, 0] == 0)
 
 
+@pytest.mark.parametrize("bits", [4, 3])
+@pytest.mark.parametrize("rows", [1, 5, 80])
+def test_grouped_infinite_input(bits, rows):
+    """An infinity in x gives what the formula gives, infinities of the weight's sign and NaN where
+    the weight is 0, in its own row; in the last of an odd number of groups, too."""
+    N, K, at = 50, 640, 600
+    w, p, sc, z = layer(2, N, K, bits, 31)
+    x = inputs(2 * rows, K, 32)
+    x[rows - 1, at] = np.inf
+    y = host(awq.awq_gemm_grouped(dev(x), p, sc, z, dev(np.array([0, rows, 2 * rows], np.int32))))
+    with np.errstate(invalid="ignore"):
+        assert np.array_equal(y[rows - 1].astype(np.float64), np.inf * w[0, :, at], equal_nan=True)
+    for e, lo, hi in ((0, 0, rows - 1), (1, rows, 2 * rows)):
+        if lo < hi:
+            assert_rows(y[lo:hi], x[lo:hi], w[e], f"expert {e}")
+
+
 def test_grouped_matches_single_products_and_is_deterministic():
     """Each expert's rows are awq_gemm's product with its matrix, to rounding; two calls agree bit for bit."""
     sizes, N, K = [3, 0, 20, 1, 150], 256, 1024

@@ -257,7 +257,7 @@ __global__ __launch_bounds__(512) void grouped_ring_kernel(
   for (int t = 0; t < RW; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   wait_vmcnt<(S - 2) * Q::LOADS>();  // the scales and zeros (issued first), and the first stage
   lds_barrier();
-  const int turns = (G + waves - 1) / waves;  // stages of this wave; the last may lie past the end
+  const int turns = (G - wave + waves - 1) / waves;  // stages of this wave
   for (int j0 = 0; j0 < turns; j0 += S)
 #pragma unroll
     for (int u = 0; u < S; ++u) {  // slot u
@@ -269,7 +269,6 @@ __global__ __launch_bounds__(512) void grouped_ring_kernel(
       wait_vmcnt<(S - 1) * Q::LOADS>();
       __builtin_amdgcn_sched_barrier(0);
       const unsigned char* st = ring + u * Q::STAGE;
-      const int gc = g < G ? g : G - 1;
       uint32_t w[RW][BITS], z[RW];
       float sc[RW];
 #pragma unroll
@@ -283,8 +282,8 @@ __global__ __launch_bounds__(512) void grouped_ring_kernel(
 #pragma unroll
           for (int i = 0; i < 3; ++i) w[t][i] = v[i];
         }
-        z[t] = (zl[row[t] * P2 + (gc >> 1)] >> (4 * (gc & 1))) & 0xFu;
-        sc[t] = (float)reinterpret_cast<const f16*>(sl)[row[t] * G + (gc ^ sx[t])];
+        z[t] = (zl[row[t] * P2 + (g >> 1)] >> (4 * (g & 1))) & 0xFu;
+        sc[t] = (float)reinterpret_cast<const f16*>(sl)[row[t] * G + (g ^ sx[t])];
       }
 #pragma unroll
       for (int t = 0; t < RW; ++t) {
@@ -295,9 +294,8 @@ __global__ __launch_bounds__(512) void grouped_ring_kernel(
         for (int s = 0; s < 4; ++s) {
           d = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[u].a[s], unpack8(w[t], s, bias, zf), d, 0, 0, 0);
         }
-        const float scale = g < G ? sc[t] : 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(scale, d[r], acc[t][r]);
+        for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(sc[t], d[r], acc[t][r]);
       }
     }
   // the rings become the place of the sum: lane holds rows 4 kq + r of column 16 t + nl
