@@ -255,6 +255,20 @@ def test_attention_peaked_rising_and_zero_scores():
     assert np.all(np.abs(y - ref) <= tol)
 
 
+@pytest.mark.parametrize("n", [40, 5000])
+def test_attention_of_nan(n):
+    """A NaN in one query head makes that head's output NaN, in one chunk and in many, and no other."""
+    c = random_cache(320, 1, 64, 16, 4, 11)
+    q = np.random.default_rng(12).standard_normal((1, 3, 64)).astype(np.float16)
+    q[0, 1, 7] = np.nan
+    table, lengths = np.arange(320, dtype=np.int32)[None], np.array([n], np.int32)
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(lengths)))
+    assert np.isnan(y[0, 1]).all()
+    q[0, 1, 7] = 0
+    ref, tol = attend_ref(q, host_cache(c), table, lengths, 64 ** -0.5, 4, 40)
+    assert np.all(np.abs(y - ref)[:, [0, 2]] <= tol[:, [0, 2]])
+
+
 def test_attention_past_32_bit_offsets():
     """A cache whose halves pass 2^32 bytes and 2^31 words: first and last pages."""
     free, _ = torch.cuda.mem_get_info()

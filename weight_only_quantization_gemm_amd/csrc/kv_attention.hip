@@ -375,7 +375,7 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
       share[w * kAttHeads + n] = f;
       sum = fmaf(f, red_l[w * kAttHeads + n], sum);
     }
-    share[kAttWaves * kAttHeads + n] = sum > 0.f ? 1.f / sum : 0.f;
+    share[kAttWaves * kAttHeads + n] = sum == 0.f ? 0.f : 1.f / sum;
     if (!whole && n < heads) {
       const int64_t at = (head0 + n) * chunks + blockIdx.y;
       part_ml[2 * at] = mx;
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
     acc += red[2 * (p * D + d)];
     sum += red[2 * (p * D + d) + 1];
   }
-  out[head * D + d] = (f16)(sum > 0.f ? acc / sum : 0.f);
+  out[head * D + d] = (f16)(sum == 0.f ? 0.f : acc / sum);  // no token: 0 (a NaN stays one)
 }
 
 // Tokens of a chunk, a power of two of at least one step of every wave (128).  A
