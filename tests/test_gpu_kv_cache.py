@@ -209,6 +209,13 @@ def test_attention_many_sequences_take_larger_chunks():
     check_attention(150, np.random.default_rng(3).integers(0, 2100, size=150), 8, 1, 64, 16, 4, seed=8)
 
 
+def test_attention_many_long_sequences_take_the_largest_chunks():
+    """Chunks of 4096 tokens, their pages read in four runs, and a second chunk behind them."""
+    n = np.random.default_rng(16).integers(2500, 4400, size=120)
+    n[:4] = [4096, 4097, 4111, 0]
+    check_attention(120, n, 8, 1, 64, 16, 4, seed=17)
+
+
 def test_attention_of_bad_pages():
     """Entries outside the cache count as absent; a sequence of nothing else gives 0."""
     g = np.random.default_rng(1)
@@ -252,6 +259,23 @@ def test_attention_peaked_rising_and_zero_scores():
     table, lengths = np.arange(40, dtype=np.int32)[None], np.array([n], np.int32)
     y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(lengths), scale=1.0))
     ref, tol = attend_ref(q, host_cache(c), table, lengths, 1.0, 8, 8)
+    assert np.all(np.abs(y - ref) <= tol)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("gain", [-22, -14, -8, 9])
+def test_attention_query_magnitudes(gain, bits):
+    """Queries from fp16's smallest numbers to its largest, with a scale that brings the scores back,
+    and heads of mixed magnitudes: q enters as it is given."""
+    check_attention(2, [700, 40], 2, 4, 128, 16, bits, seed=13, q_gain=2.0 ** gain, scale=2.0 ** (-gain - 3))
+    g = np.random.default_rng(14)
+    c = random_cache(20, 1, 64, 16, bits, 15)
+    q = (g.standard_normal((1, 5, 64)) * np.exp2(np.array([-24, -10, 0, 4, 13])[None, :, None])).astype(np.float16)
+    q[0, 1, 9] = 3.0
+    q[0, 0] = 0
+    table, lengths = np.arange(20, dtype=np.int32)[None], np.array([300], np.int32)
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(lengths), scale=2.0 ** -10))
+    ref, tol = attend_ref(q, host_cache(c), table, lengths, 2.0 ** -10, bits, 4)
     assert np.all(np.abs(y - ref) <= tol)
 
 
@@ -341,6 +365,43 @@ def test_decoding_step_together(bits):
         n = advance(i)
         graph.replay()
         check(*captured, n)
+
+
+def test_calls_on_two_streams_at_once_and_given_workspaces():
+    """Long attention and routing on two streams side by side, each call with a workspace of its
+    own (allocated, or given and full of NaN): the results of the calls one after the other."""
+    g = np.random.default_rng(18)
+    c = random_cache(900, 2, 128, 16, 4, 19)
+    cases = []
+    for i in range(2):
+        q = dev(g.standard_normal((2, 16, 128)).astype(np.float16))
+        table = dev(g.permutation(900)[:800].reshape(2, 400).astype(np.int32))
+        lengths = dev(g.integers(5000, 6400, size=2).astype(np.int32))
+        logits = dev(g.standard_normal((700, 33)).astype(np.float32))
+        cases.append((q, table, lengths, logits))
+
+    def run(case, ws=None):
+        q, table, lengths, logits = case
+        y = awq.awq_kv_attention(q, c, table, lengths, workspace=ws)
+        r = awq.awq_moe_route(logits, 5)
+        return [y.view(torch.int16), r["experts"], r["weights"].view(torch.int32), r["offsets"], r["rows"], r["pos"]]
+
+    alone = [[host(t) for t in run(case)] for case in cases]
+    need = awq.awq_kv_attention_workspace_bytes(2, 16, 2, 128, 4, 6400)
+    assert need > 0
+    streams, got = [torch.cuda.Stream() for _ in cases], [[], []]
+    given = [torch.full((need // 4,), float("nan"), device=DEV) for _ in cases]
+    torch.cuda.synchronize()
+    for turn in range(6):
+        for i, (s, case) in enumerate(zip(streams, cases)):
+            with torch.cuda.stream(s):
+                got[i].append(run(case, given[i] if turn % 2 else None))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for result in got[i]:
+            assert all(np.array_equal(host(t), a) for t, a in zip(result, alone[i]))
+    with pytest.raises(awq.AwqError):
+        run(cases[0], given[0][:need // 4 - 64])
 
 
 def test_refusals_of_the_binding():
