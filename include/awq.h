@@ -563,7 +563,7 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
  * products with 22 bits.  Chunks of a long sequence are joined in order, so the
  * result does not depend on timing.
  * Requires D 64, 128 or 256, Hq a multiple of Hkv, 1 <= B <= 65535,
- * B * Hq * D < 2^32, finite scale.
+ * B * Hq * D < 2^32, |scale| <= 2^64.
  */
 size_t awq_kv_attention_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t bits, int64_t max_len);
 int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const void* k_params, const void* v_codes,

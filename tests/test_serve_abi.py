@@ -70,7 +70,7 @@ BAD = {
     "awq_kv_attention": [dict(B=0), dict(B=65536), dict(Hq=7), dict(Hq=1), dict(Hkv=0), dict(D=80), dict(page=17),
                          dict(bits=2), dict(q_stride=1023), dict(q_stride=512), dict(table_width=0), dict(max_len=-1),
                          dict(table_width=1 << 26), dict(table_width=1 << 27), dict(scale=float("nan")),
-                         dict(scale=float("inf"))],
+                         dict(scale=float("inf")), dict(scale=2e19), dict(scale=-2e19)],
 }
 
 

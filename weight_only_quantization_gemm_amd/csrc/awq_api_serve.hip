@@ -259,7 +259,8 @@ int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const
   const int64_t most = max_len == 0 || max_len > room ? room : max_len;
   AWQ_REQUIRE(max_len >= 0 && most <= AWQ_MAX_KV_LENGTH, AWQ_ERROR_INVALID_VALUE,
               "a longest length of %lld tokens: at most 2^25 are served (give max_len)", (long long)most);
-  AWQ_REQUIRE(std::isfinite(scale), AWQ_ERROR_INVALID_VALUE, "scale must be finite");
+  AWQ_REQUIRE(std::isfinite(scale) && std::fabs(scale) <= 0x1p64f, AWQ_ERROR_INVALID_VALUE,
+              "scale must be finite and at most 2^64 in magnitude");
   const size_t need = awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bits, most);
   AWQ_REQUIRE(workspace || need == 0, AWQ_ERROR_INVALID_VALUE, "workspace must not be NULL (%zu bytes needed)", need);
   if (int st = check_aligned({{q, "q"}, {k_codes, "k_codes"}, {k_params, "k_params"}, {v_codes, "v_codes"},
