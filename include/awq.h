@@ -555,13 +555,14 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
  *   lengths     device int32 [B]; at most table_width * page and max_len are
  *               used.  A sequence with no tokens gets out = 0
  *   out         device fp16 [B][Hq][D]
- *   max_len     host bound on the lengths (0: table_width * page): the split
- *               over the length is made for it.  At most AWQ_MAX_KV_LENGTH
+ *   max_len     host bound on the lengths (0: table_width * page), at most
+ *               AWQ_MAX_KV_LENGTH.  Up to 256 sequences the work is split by
+ *               the lengths themselves, beyond by the bound
  *   workspace   device, >= awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bits,
  *               the bound) bytes; it needs no clearing and keeps nothing
  * Scores, softmax statistics and sums are fp32; a weight p_t enters the
- * products with 22 bits.  Chunks of a long sequence are joined in order, so the
- * result does not depend on timing.
+ * products with 22 bits.  The pieces of a long sequence are joined in order, so
+ * the result does not depend on timing.
  * Requires D 64, 128 or 256, Hq a multiple of Hkv, 1 <= B <= 65535,
  * B * Hq * D < 2^32, |scale| <= 2^64.
  */

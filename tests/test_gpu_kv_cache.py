@@ -210,10 +210,65 @@ def test_attention_many_sequences_take_larger_chunks():
 
 
 def test_attention_many_long_sequences_take_the_largest_chunks():
-    """Chunks of 4096 tokens, their pages read in four runs, and a second chunk behind them."""
+    """Pieces whose pages are read in several runs of 1024 tokens; for more than 256 sequences
+    chunks of 4096 tokens and a second one behind them."""
     n = np.random.default_rng(16).integers(2500, 4400, size=120)
     n[:4] = [4096, 4097, 4111, 0]
     check_attention(120, n, 8, 1, 64, 16, 4, seed=17)
+    n = np.random.default_rng(27).integers(0, 300, size=260)
+    n[[5, 100, 101, 259]] = [4400, 4096, 4097, 1025]
+    check_attention(260, n, 8, 1, 64, 16, 4, seed=28)
+
+
+@pytest.mark.parametrize("B", [1, 3, 64, 65, 255, 256, 257])
+def test_attention_bound_far_above_the_lengths(B):
+    """A page table made for 70000 tokens and sequences of a few hundred, some empty: the tokens
+    are shared out by the lengths, up to 256 sequences."""
+    n = np.random.default_rng(B).integers(-100, 700, size=B)
+    n[0] = 900
+    check_attention(B, n, 2, 4, 64, 16, 4, seed=20 + B, width=4400 if B < 10 else 60)
+
+
+def test_attention_runs_past_the_blocks():
+    """More tokens than the blocks of a head take in one run each: they go on to further runs of
+    4096 tokens (three of the 64 heads are checked)."""
+    H, B, D, page, heads = 64, 40, 64, 16, [0, 31, 63]
+    g = np.random.default_rng(23)
+    lengths = g.integers(2000, 3000, size=B).astype(np.int32)
+    lengths[[3, 17]] = [0, 1]
+    table = g.integers(0, 1500, size=(B, 188)).astype(np.int32)  # pages shared between sequences
+    c = random_cache(1500, H, D, page, 8, 24)
+    q = g.standard_normal((B, H, D)).astype(np.float16)
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(lengths)))
+    sub = {k: v[:, heads] for k, v in host_cache(c).items()}
+    ref, tol = attend_ref(q[:, heads], sub, table, lengths, D ** -0.5, 8, 24)
+    assert np.all(np.abs(y[:, heads] - ref) <= tol)
+    assert np.all(y[3] == 0)
+
+
+def test_attention_captured_while_lengths_move_on():
+    """One captured call over a table for 20000 tokens, replayed for lengths that change how the
+    work is shared out, with eager calls between: each replay is the eager result."""
+    B, H, r, D = 5, 2, 4, 128
+    g = np.random.default_rng(25)
+    c = random_cache(1300, H, D, 16, 4, 26)
+    tab = dev(g.integers(0, 1300, size=(B, 1250)).astype(np.int32))
+    q = dev(g.standard_normal((B, H * r, D)).astype(np.float16))
+    lengths = torch.ones(B, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        awq.awq_kv_attention(q, c, tab, lengths)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = awq.awq_kv_attention(q, c, tab, lengths)
+    for n in ([1, 1, 1, 1, 1], [20000, 0, 1, 128, 129], [0, 0, 0, 0, 0], [300, 4096, 4097, 12, 700], [19000, 20000, 18000, 17, 3]):
+        lengths.copy_(dev(np.array(n, np.int32)))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(host(out).view(np.uint16), host(awq.awq_kv_attention(q, c, tab, lengths)).view(np.uint16))
+        ref, tol = attend_ref(host(q), host_cache(c), host(tab), n, D ** -0.5, 4, 160)
+        assert np.all(np.abs(host(out) - ref) <= tol)
 
 
 def test_attention_of_bad_pages():

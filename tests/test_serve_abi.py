@@ -166,3 +166,14 @@ def test_cache_addresses_stay_inside(tmp_path):
                     "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
+def test_attention_split_covers_every_token_once(tmp_path):
+    """The pieces attention's work is cut into by the lengths: the kernels' own arithmetic,
+    compiled for the host."""
+    exe = tmp_path / "kv_split_check"
+    csrc = os.path.join(ROOT, "weight_only_quantization_gemm_amd", "csrc")
+    subprocess.run(["g++", "-O1", "-Wall", "-Werror", "-I", csrc, os.path.join(ROOT, "tests", "kv_split_check.cpp"),
+                    "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout

@@ -13,11 +13,17 @@
 // fp32; w_t enters the products as the sum of two fp16 numbers, which leaves
 // 2^-22 of it (one would add an error of the size of the output's own rounding).
 //
-// A block takes one chunk of the sequence's tokens for one key-value head and
-// up to 16 of its query heads; its waves take 32-token steps in turn, each
-// wave with its own running maximum, sum and output, and are joined through
-// LDS.  Chunks of one sequence are joined by kv_join_kernel in the order of
-// the chunks, so results do not depend on timing.
+// A block takes one piece of a sequence's tokens for one key-value head and up to
+// 16 of its query heads; its waves take 32-token steps in turn, each wave with its
+// own running maximum, sum and output, and are joined through LDS.  The pieces of
+// one sequence are joined by kv_join_kernel in their order, so results do not
+// depend on timing.
+//
+// Bound by reading the cache: 64 sequences of 4096 tokens x 8 heads of 128 at 4
+// bits, 287 MB in 61 us (4.7 TB/s); 32 of 2000 to 6000 at 8 bits, 269 MB in 62 us;
+// 64 ragged ones of 2000 to 6000 tokens at 4 bits 279 MB in 67 us, the last blocks
+// leaving units idle; one of 2000 tokens 10 us, launches and latency.  The vector
+// ALU is busy 44 % of the time.
 //
 // Lanes.  With l = 16 b + n, the products are 16 x 16 x 32:
 //   scores  A = codes of 16 tokens (row n: token; lane's channels D/4 b ..),
@@ -39,7 +45,7 @@ constexpr int kAttHeads = 16;      // query heads of a block: columns of a produ
 constexpr float kSlack = 8.f;      // a score may pass the running maximum by this (log2) before all is rescaled
 constexpr float kTwo24 = 16777216.f;
 constexpr int kNonTemporal = 2;    // cache policy of the code loads: every line is used once (54 against 61 us on long sequences)
-constexpr int kAttWindows = 4;     // 64-tile runs of the pages of a chunk: 4096 tokens at most
+constexpr int kAttWindow = 1024;   // tokens whose pages a wave's lanes hold, 16 each
 
 // Channel of the cache row that product row n of tile c of the output stands for.
 template <int D, int BITS>
@@ -76,52 +82,135 @@ struct AttStage {
   static __host__ __device__ constexpr int slot_xor(int r) { return (r / (256 / RB)) & (PIECES - 1); }
 };
 
+// How a call's tokens are cut into pieces, one (sequence, run of tokens) each.
+// By the bound on the lengths (chunk > 0): `chunk` tokens of sequence blockIdx.z.
+// By the lengths themselves (chunk = 0): piece blockIdx.y of those of all sequences,
+// which PieceSplit counts from the lengths on the device.
+struct AttSplit {
+  const int32_t* lengths;
+  int64_t max_len;
+  int width;   // entries of a page table's row
+  int batch;
+  int chunk, chunks;
+  int heads;   // blocks' heads: key-value heads x tiles of query heads
+  int most;    // pieces of all heads that keep the chip full
+};
+
+static_assert(kKvUnit == kAttStep * kAttWaves, "a unit is a step of every wave");
+constexpr int kPieceWindows = 4, kPieceBatch = 64 * kPieceWindows;
+
+// The lengths of a batch and the pieces they make; lane i of window k holds sequence
+// 64 k + i.
+struct PieceSplit {
+  int len[kPieceWindows], upto[kPieceWindows];  // pieces up to and with the sequence
+  int total, shift;
+
+  __device__ __forceinline__ void read(const AttSplit& sp, const KvShape& sh, int lane) {
+    int64_t units = 0;
+#pragma unroll
+    for (int k = 0; k < kPieceWindows; ++k)  // (sequences past the batch repeat its last and do not count)
+      len[k] = (int)kv_length(sh, sp.lengths[64 * k + lane < sp.batch ? 64 * k + lane : sp.batch - 1], sp.width, sp.max_len);
+#pragma unroll
+    for (int k = 0; k < kPieceWindows; ++k)
+      if (64 * k < sp.batch)
+        units += __builtin_amdgcn_readlane(wave_scan(64 * k + lane < sp.batch ? kv_units(len[k]) : 0), 63);
+    shift = kv_piece_shift(units, sp.heads, sp.most);
+    total = 0;
+#pragma unroll
+    for (int k = 0; k < kPieceWindows; ++k) {
+      upto[k] = total;
+      if (64 * k < sp.batch) {
+        upto[k] += wave_scan(64 * k + lane < sp.batch ? kv_pieces(kv_units(len[k]), shift) : 0);
+        total = __builtin_amdgcn_readlane(upto[k], 63);
+      }
+    }
+  }
+  __device__ __forceinline__ static int pick(const int (&v)[kPieceWindows], int seq) {
+    int x = __builtin_amdgcn_readlane(v[0], seq & 63);
+#pragma unroll
+    for (int k = 1; k < kPieceWindows; ++k) x = seq >> 6 == k ? __builtin_amdgcn_readlane(v[k], seq & 63) : x;
+    return x;
+  }
+  // The sequence of piece i (< total).
+  __device__ __forceinline__ int sequence(int i) const {
+    int seq = 0;
+#pragma unroll
+    for (int k = kPieceWindows - 1; k >= 0; --k) {
+      const uint64_t past = __ballot(upto[k] > i);
+      if (past) seq = 64 * k + __ffsll((unsigned long long)past) - 1;
+    }
+    return seq;
+  }
+  __device__ __forceinline__ int length(int seq) const { return pick(len, seq); }
+  __device__ __forceinline__ int end(int seq) const { return pick(upto, seq); }
+};
+
 template <int D, int BITS>
-__global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
-    const f16* __restrict__ q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* __restrict__ table, int width,
-    const int32_t* __restrict__ lengths, int64_t max_len, KvShape sh, int ratio, float scale_log2, int chunk,
-    int chunks, f16* __restrict__ out, float* __restrict__ part_o, float* __restrict__ part_ml) {
+__global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_attention_kernel(
+    const f16* __restrict__ q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* __restrict__ table, AttSplit sp,
+    KvShape sh, int ratio, float scale_log2, f16* __restrict__ out, float* __restrict__ part_o,
+    float* __restrict__ part_ml, int32_t* __restrict__ meta) {
   using A = AttStage<D, BITS>;
   constexpr int TILES = D / 16, RB = A::RB;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
 
-  const int lane = threadIdx.x & 63, n = lane & 15, b = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row_tiles = (ratio + kAttHeads - 1) / kAttHeads;
   const int hk = (int)blockIdx.x / row_tiles, h0 = ((int)blockIdx.x - hk * row_tiles) * kAttHeads;
-  const int seq = (int)blockIdx.z;
   const int heads = ratio - h0 < kAttHeads ? ratio - h0 : kAttHeads;  // query heads of this block
   const int Hq = sh.heads * ratio;
 
-  // Pages of the chunk: lane i of window k holds that of the chunk's tile 64 k + i
-  // of 16 tokens, -1 where there is none.  The entries are fetched along with the
-  // length, those past it too (within the table's row), and dropped afterwards.
-  const int64_t t0 = (int64_t)blockIdx.y * chunk;
-  int page_of[kAttWindows];
-#pragma unroll
-  for (int k = 0; k < kAttWindows; ++k) {
-    const int t = 16 * (64 * k + lane);
-    const int64_t entry = (t0 + t) >> sh.ps;
-    page_of[k] = t < chunk && entry < width ? table[(int64_t)seq * width + entry] : -1;
-  }
-  const int64_t len = kv_length(sh, lengths[seq], width, max_len);
-  if (t0 >= len && blockIdx.y > 0) return;  // the first chunk of an empty sequence stores its zeros
-  const int count = (int)(len - t0 < chunk ? (len - t0 > 0 ? len - t0 : 0) : chunk);
-#pragma unroll
-  for (int k = 0; k < kAttWindows; ++k) page_of[k] = 16 * (64 * k + lane) < count ? kv_page(sh, page_of[k]) : -1;
-  auto page = [&](int tile) {
-    int p = __builtin_amdgcn_readlane(page_of[0], tile & 63);
-#pragma unroll
-    for (int k = 1; k < kAttWindows; ++k) p = tile >> 6 == k ? __builtin_amdgcn_readlane(page_of[k], tile & 63) : p;
-    return p;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, n = lane & 15, b = lane >> 4;
+  int seq, slot, count;  // the piece: tokens t0 .. t0 + count - 1 of sequence seq
+  int64_t t0;
+  bool whole;  // all of them
+  // Pages: lane i holds that of tile 64 w + i of 16 tokens, w the window of 1024 tokens
+  // under way, -1 where there is none.  The table's entries are fetched whatever the
+  // count (one load always: the waits below count it), and dropped by it afterwards.
+  auto entry = [&](int w) {
+    const int64_t e = (t0 + kAttWindow * w + 16 * lane) >> sh.ps;
+    return table + (int64_t)seq * sp.width + (e < sp.width ? e : sp.width - 1);
   };
+  auto page_of = [&](int w, int entry) { return kAttWindow * w + 16 * lane < count ? kv_page(sh, entry) : -1; };
+  int pages, next = -1;
+  if (sp.chunk == 0) {
+    PieceSplit split;
+    split.read(sp, sh, lane);
+    slot = (int)blockIdx.y;
+    if (slot >= split.total) return;
+    seq = split.sequence(slot);
+    const int len = split.length(seq), units = kv_units(len), pieces = kv_pieces(units, split.shift);
+    const int span = (units + pieces - 1) / pieces * kKvUnit, first = split.end(seq) - pieces;
+    if (slot == first && blockIdx.x == 0 && tid == 0) {
+      meta[2 * seq] = first;
+      meta[2 * seq + 1] = pieces;
+    }
+    t0 = (int64_t)(slot - first) * span;
+    count = len - (int)t0 < span ? len - (int)t0 : span;
+    whole = pieces == 1;
+    pages = *entry(0);
+  } else {
+    seq = (int)blockIdx.z;
+    t0 = (int64_t)blockIdx.y * sp.chunk;
+    pages = *entry(0);  // along with the length
+    const int64_t len = kv_length(sh, sp.lengths[seq], sp.width, sp.max_len);
+    if (t0 >= len && blockIdx.y > 0) return;  // the first piece of an empty sequence stores its zeros
+    count = (int)(len - t0 < sp.chunk ? (len - t0 > 0 ? len - t0 : 0) : sp.chunk);
+    whole = len <= sp.chunk;
+    slot = seq * sp.chunks + (int)blockIdx.y;
+  }
+  pages = page_of(0, pages);
+  auto page = [&](int tile) { return __builtin_amdgcn_readlane(pages, tile & 63); };
 
   unsigned char* ring = smem + wave * A::RING;
-  auto issue = [&](int i, int slot) {
+  int* ahead = reinterpret_cast<int*>(smem + kAttWaves * A::RING) + wave * 64;  // the next window's entries
+  auto issue = [&](int i, int slot, int pages_of_i) {
     unsigned char* st = ring + slot * A::BYTES;
     int64_t row[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) row[u] = kv_tile_row(sh, page(2 * i + u), t0 + 16 * (2 * i + u), hk);
+    for (int u = 0; u < 2; ++u)
+      row[u] = kv_tile_row(sh, __builtin_amdgcn_readlane(pages_of_i, (2 * i + u) & 63), t0 + 16 * (2 * i + u), hk);
 #pragma unroll
     for (int k = 0; k < A::NI; ++k) {
       const int r = (k * 64 + lane) / A::PIECES, slot_of = lane % A::PIECES;  // row of the step, 16-byte slot
@@ -139,13 +228,14 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
   };
   const int steps = (count + kAttStep - 1) / kAttStep;
   const int turns = steps > wave ? (steps - wave + kAttWaves - 1) / kAttWaves : 0;
-  if (turns > 0) issue(wave, 0);
+  if (turns > 0) issue(wave, 0, pages);
 
   // q: columns past the block's heads repeat the last one and are never stored.  At 4 bits a head
   // is multiplied by the power of two that brings its largest channel to 2^14 .. 2^15 (larger ones
   // stay), so that the sixteenth of a small q, the operand of an upper nibble, keeps its bits; the
-  // factor takes it back (1 us of 70 for 64 sequences of 2000 to 6000 tokens).  A negative factor goes to q's sign, so that larger sums are larger
-  // scores; one of 0 is taken as 2^-100, which leaves a masked score (-infinity) what it is.
+  // factor takes it back (1 us of 70 for 64 sequences of 2000 to 6000 tokens).  A negative factor
+  // goes to q's sign, so that larger sums are larger scores; one of 0 is taken as 2^-100, which
+  // leaves a masked score (-infinity) what it is.
   const int hn = n < heads ? n : heads - 1;
   const f16* qrow = q + seq * q_stride + (int64_t)(hk * ratio + h0 + hn) * D;
   f16x8 qf[D / 32];
@@ -236,7 +326,7 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
         vp[4 * u + r] = vq[r];
       }
     }
-    // tokens past the chunk's end or of a page that is none: no score, value scale and zero point 0
+    // tokens past the piece's end or of a page that is none: no score, value scale and zero point 0
     const bool page0 = page(2 * i) >= 0, page1 = page(2 * i + 1) >= 0;
     if (!page0 || !page1 || kAttStep * (i + 1) > count) {
 #pragma unroll
@@ -346,18 +436,27 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
     }
   };
 
+  constexpr int kTurns = kAttWindow / kKvUnit;
   for (int j = 0; j < turns; ++j) {
     __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads of the stage refilled now are done
     __builtin_amdgcn_sched_barrier(0);
-    const int i = wave + j * kAttWaves;
+    const int i = wave + j * kAttWaves, w = j / kTurns;
+    const bool last = j % kTurns == kTurns - 1;  // the next step lies in the next window
     if (j + 1 < turns) {
-      issue(i + kAttWaves, (j + 1) & 1);
-      wait_vmcnt<A::LOADS>();
+      if (last) next = page_of(w + 1, ahead[lane]);
+      issue(i + kAttWaves, (j + 1) & 1, last ? next : pages);
+      if (j % kTurns == 0) {  // the next window's entries, a window ahead (in a register each turn would wait for them)
+        __builtin_amdgcn_global_load_lds((global_ptr_t)entry(w + 1), (lds_ptr_t)ahead, 4, 0, 0);
+        wait_vmcnt<A::LOADS + 1>();
+      } else {
+        wait_vmcnt<A::LOADS>();
+      }
     } else {
       wait_vmcnt<0>();
     }
     __builtin_amdgcn_sched_barrier(0);
     compute(i, ring + (j & 1) * A::BYTES);
+    if (last) pages = next;
   }
   __syncthreads();  // the rings become the place of the sum
 
@@ -382,9 +481,8 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
             o[c][r] * (att_times16<BITS>(c) ? kTwo24 / 16.f : kTwo24) - oz[r];
   }
   __syncthreads();
-  const bool whole = len <= chunk;  // the sequence's only chunk: store the result itself
   const int64_t head0 = (int64_t)seq * Hq + hk * ratio + h0;
-  if (threadIdx.x < kAttHeads) {
+  if (tid < kAttHeads) {
     float mx = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttWaves; ++w) mx = fmaxf(mx, red_m[w * kAttHeads + n]);
@@ -397,13 +495,13 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
     }
     share[kAttWaves * kAttHeads + n] = sum == 0.f ? 0.f : 1.f / sum;
     if (!whole && n < heads) {
-      const int64_t at = (head0 + n) * chunks + blockIdx.y;
+      const int64_t at = (int64_t)slot * Hq + hk * ratio + h0 + n;
       part_ml[2 * at] = mx;
       part_ml[2 * at + 1] = sum;
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < heads * D / 4; i += 64 * kAttWaves) {
+  for (int i = tid; i < heads * D / 4; i += 64 * kAttWaves) {
     const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -418,29 +516,36 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attention_kernel(
       *reinterpret_cast<u32x2*>(out + (head0 + h) * D + d) =
           u32x2{as_u32(f16x2{(f16)(acc[0] * f), (f16)(acc[1] * f)}), as_u32(f16x2{(f16)(acc[2] * f), (f16)(acc[3] * f)})};
     } else {
-      *reinterpret_cast<f32x4*>(part_o + ((head0 + h) * chunks + blockIdx.y) * D + d) = acc;
+      *reinterpret_cast<f32x4*>(part_o + ((int64_t)slot * Hq + hk * ratio + h0 + h) * D + d) = acc;
     }
   }
 }
 
-// Joins the chunks of one query head of one sequence: D x parts threads, part p
-// taking chunks p, p + parts, ...; the parts are summed in order.
+// Joins the pieces of one query head of one sequence: D x parts threads, part p
+// taking pieces p, p + parts, ...; the parts are summed in order.
 __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__ part_o,
                                                        const float* __restrict__ part_ml,
-                                                       const int32_t* __restrict__ lengths, int64_t max_len, int width,
-                                                       KvShape sh, int Hq, int chunk, int chunks,
-                                                       f16* __restrict__ out) {
+                                                       const int32_t* __restrict__ meta, AttSplit sp, KvShape sh,
+                                                       int Hq, f16* __restrict__ out) {
   __shared__ float red[2 * 1024], top[16];
   const int64_t head = blockIdx.x;
   const int D = (int)blockDim.x, d = (int)threadIdx.x, part = (int)threadIdx.y, parts = (int)blockDim.y;
-  const int64_t len = kv_length(sh, lengths[head / Hq], width, max_len);
-  if (len <= chunk) return;  // stored by its only block
-  const int used = (int)((len + chunk - 1) / chunk);
-  const float* ml = part_ml + head * chunks * 2;
-  const float* po = part_o + head * chunks * D + d;
   const int tid = part * D + d, threads = parts * D;
+  const int seq = (int)blockIdx.x / Hq;
+  int used, slot0;
+  if (sp.chunk == 0) {
+    slot0 = meta[2 * seq];
+    used = meta[2 * seq + 1];
+  } else {
+    used = (int)((kv_length(sh, sp.lengths[seq], sp.width, sp.max_len) + sp.chunk - 1) / sp.chunk);
+    slot0 = seq * sp.chunks;
+  }
+  if (used <= 1) return;  // stored by its only block
+  const int64_t row0 = (int64_t)slot0 * Hq + (head - (int64_t)seq * Hq);
+  const float* ml = part_ml + row0 * 2;
+  const float* po = part_o + row0 * D + d;
   float mx = -INFINITY;
-  for (int c = tid; c < used; c += threads) mx = fmaxf(mx, ml[2 * c]);
+  for (int c = tid; c < used; c += threads) mx = fmaxf(mx, ml[(int64_t)c * Hq * 2]);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, kWave));
   if ((tid & 63) == 0) top[tid >> 6] = mx;
@@ -449,10 +554,10 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
   float sum = 0.f, acc = 0.f;
 #pragma unroll 4
   for (int c = part; c < used; c += parts) {
-    const float m = ml[2 * c];
+    const float m = ml[(int64_t)c * Hq * 2];
     const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
-    sum = fmaf(f, ml[2 * c + 1], sum);
-    acc = fmaf(f, po[(int64_t)c * D], acc);
+    sum = fmaf(f, ml[(int64_t)c * Hq * 2 + 1], sum);
+    acc = fmaf(f, po[(int64_t)c * Hq * D], acc);
   }
   red[2 * tid] = acc;
   red[2 * tid + 1] = sum;
@@ -465,53 +570,78 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
   out[head * D + d] = (f16)(sum == 0.f ? 0.f : acc / sum);  // no token: 0 (a NaN stays one)
 }
 
-// Tokens of a chunk, a power of two of at least one step of every wave (128).  A
-// chunk costs a block's start (three dependent loads) and end (the joins) beside
-// its steps, so chunks grow to 512 tokens while there are more than 512 blocks,
-// and on to 4096 while there are more than about one and a half times what the
-// compute units hold at once (by the rows' bytes, which size the ring).  Measured,
-// us at chunks of 128 / 256 / 512 / 1024 / 2048 / 4096 tokens: one sequence of
-// 30000, 8 heads: 30.4 / 22.4 / 18.9; 16 of up to 2000: 20.9 / 17.6 / 16.4 / 17.9;
-// 4 of up to 5000, 32 heads: -/ 25.8 / 22.3 / 24.6 / 32.1 / 41.7; 64 of up to 6000,
-// 8 heads: - / - / 80.6 / 69.7 / 71 / 89; 8-bit rows of 256 channels, 4 of up to
-// 9000: 58.2 / 43.8 / 35.1 / 28.8.  Up to 512 tokens one block does without a
-// join: 9.4 us where four chunks and a second launch take 9.5.
-static int att_chunk(int64_t B, int64_t Hkv, int ratio, int row_bytes, int64_t max_len) {
-  const int64_t rows = B * Hkv * ((ratio + kAttHeads - 1) / kAttHeads);
-  const int64_t most = row_bytes <= 64 ? 1536 : (row_bytes == 128 ? 1024 : 512);
-  auto blocks = [&](int chunk) { return rows * ((max_len + chunk - 1) / chunk); };
-  int chunk = max_len <= 512 ? 512 : kAttStep * kAttWaves;
-  while (chunk < 512 && blocks(chunk) > 512) chunk *= 2;
-  while (chunk >= 512 && chunk < 1024 * kAttWindows && blocks(chunk) > most) chunk *= 2;
-  return chunk;
+// The split.  By the bound alone, chunks are a power of two of at least 128 tokens: a
+// piece costs a block's start (dependent loads) and end (the joins) beside its steps, so
+// chunks grow to 512 tokens while there are more than 512 blocks, and on to 4096 while
+// there are more than about one and a half times what the compute units hold at once (by
+// the rows' bytes, which size the ring; one at 256 bytes).  Measured, us at chunks of 128 /
+// 256 / 512 / 1024 / 2048 / 4096 tokens: one sequence of 30000, 8 heads: 30.4 / 22.4 /
+// 18.9; 16 of up to 2000: 20.9 / 17.6 / 16.4 / 17.9; 4 of up to 5000, 32 heads: - / 25.8 /
+// 22.3 / 24.6 / 32.1 / 41.7; 64 of up to 6000, 8 heads: - / - / 80.6 / 69.7 / 71 / 89;
+// 8-bit rows of 256 channels, 4 of up to 9000: 58.2 / 43.8 / 35.1 / 28.8.  Up to 512 tokens
+// one block does without a join: 9.4 us where four chunks and a second launch take 9.5.
+// Where the bound leaves a choice (chunks above 128 tokens, several a sequence), batches of
+// up to kPieceBatch make it by the lengths on the device instead, which costs a block's
+// start up to 1 us and serves page tables made for longer sequences (bounds of 131072
+// tokens, by the bound / by the lengths: 8 sequences of 2000 44.5 / 15.8 us, 64 of 2000 to
+// 6000 161 / 67, 256 of 1000 212 / 62) and ragged batches (32 of up to 30000 127 / 110);
+// with tight bounds 64 of 4096 61.6 / 60.8, 16 of up to 2000 17.0 / 17.3, one of 30000
+// 18.9 / 20.1.
+static AttSplit att_split(int64_t B, int64_t Hkv, int ratio, int row_bytes, int64_t max_len) {
+  AttSplit sp{};
+  sp.max_len = max_len;
+  sp.batch = (int)B;
+  sp.heads = (int)(Hkv * ((ratio + kAttHeads - 1) / kAttHeads));
+  sp.most = row_bytes <= 64 ? 1536 : (row_bytes == 128 ? 1024 : 256);
+  auto blocks = [&](int chunk) { return B * sp.heads * ((max_len + chunk - 1) / chunk); };
+  sp.chunk = max_len <= 512 ? 512 : kKvUnit;
+  while (sp.chunk < 512 && blocks(sp.chunk) > 512) sp.chunk *= 2;
+  while (sp.chunk >= 512 && sp.chunk < 4096 && blocks(sp.chunk) > sp.most) sp.chunk *= 2;
+  sp.chunks = max_len > 0 ? (int)((max_len + sp.chunk - 1) / sp.chunk) : 1;
+  const int64_t pieces = kv_most_pieces(B, (int)max_len, sp.heads, sp.most);
+  if (sp.chunk > kKvUnit && sp.chunks > 1 && B <= kPieceBatch && pieces < 65536) {  // (blockIdx.y's limit)
+    sp.chunk = 0;
+    sp.chunks = (int)pieces;
+  }
+  return sp;
 }
 
+// Pieces that are joined (0: every sequence is one piece).
+static int64_t att_slots(const AttSplit& sp) {
+  if (sp.chunk == 0) return sp.chunks;
+  return sp.chunks > 1 ? (int64_t)sp.batch * sp.chunks : 0;
+}
+
+// fp32 outputs and (maximum, sum) of every piece, then by the lengths each sequence's first piece and their number.
 size_t kv_attention_workspace(int64_t B, int64_t Hkv, int ratio, int D, int bits, int64_t max_len) {
-  const int chunk = att_chunk(B, Hkv, ratio, D * bits / 8, max_len);
-  const int64_t chunks = (max_len + chunk - 1) / chunk;
-  return chunks > 1 ? (size_t)(B * Hkv * ratio * chunks * (D + 2)) * sizeof(float) : 0;
+  const AttSplit sp = att_split(B, Hkv, ratio, D * bits / 8, max_len);
+  return (size_t)(att_slots(sp) * Hkv * ratio * (D + 2) + (sp.chunk == 0 ? 2 * B : 0)) * sizeof(float);
 }
 
 template <int D, int BITS>
 static hipError_t attention_launch(const void* q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* table,
                                    int64_t width, const int32_t* lengths, int64_t B, int ratio, float scale,
                                    int64_t max_len, KvShape sh, void* out, float* ws, hipStream_t st) {
-  const int chunk = att_chunk(B, sh.heads, ratio, D * BITS / 8, max_len);
-  const int chunks = max_len > 0 ? (int)((max_len + chunk - 1) / chunk) : 1;
+  AttSplit sp = att_split(B, sh.heads, ratio, D * BITS / 8, max_len);
+  sp.lengths = lengths;
+  sp.width = (int)width;
   const int heads = ratio < kAttHeads ? ratio : kAttHeads;
   const size_t sum = (size_t)(kAttWaves * heads * D + (3 * kAttWaves + 1) * kAttHeads) * sizeof(float);
-  const size_t ring = (size_t)kAttWaves * AttStage<D, BITS>::RING, lds = ring > sum ? ring : sum;
-  const dim3 grid((unsigned)(sh.heads * ((ratio + kAttHeads - 1) / kAttHeads)), (unsigned)chunks, (unsigned)B);
-  float* part_ml = ws == nullptr ? nullptr : ws + B * sh.heads * ratio * chunks * D;
+  const size_t ring = (size_t)kAttWaves * (AttStage<D, BITS>::RING + 64 * sizeof(int)), lds = ring > sum ? ring : sum;
+  const dim3 grid((unsigned)sp.heads, (unsigned)sp.chunks, sp.chunk ? (unsigned)B : 1u);
+  const int64_t slots = att_slots(sp), Hq = (int64_t)sh.heads * ratio;
+  float* part_ml = ws == nullptr ? nullptr : ws + slots * Hq * D;
+  int32_t* meta = ws == nullptr ? nullptr : reinterpret_cast<int32_t*>(part_ml + slots * Hq * 2);
   kv_attention_kernel<D, BITS><<<grid, dim3(64 * kAttWaves), lds, st>>>(
-      reinterpret_cast<const f16*>(q), q_stride, kc, vc, table, (int)width, lengths, max_len, sh, ratio,
-      scale * 1.4426950408889634f, chunk, chunks, reinterpret_cast<f16*>(out), ws, part_ml);
+      reinterpret_cast<const f16*>(q), q_stride, kc, vc, table, sp, sh, ratio, scale * 1.4426950408889634f,
+      reinterpret_cast<f16*>(out), ws, part_ml, meta);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || chunks == 1) return e;
-  int parts = 1;  // about eight chunks a part
-  while (parts * D < 1024 && 8 * parts < chunks) parts *= 2;
-  kv_join_kernel<<<dim3((unsigned)(B * sh.heads * ratio)), dim3(D, parts), 0, st>>>(
-      ws, part_ml, lengths, max_len, (int)width, sh, sh.heads * ratio, chunk, chunks, reinterpret_cast<f16*>(out));
+  if (e != hipSuccess || slots == 0) return e;
+  const int64_t pieces = sp.chunk ? sp.chunks : (sp.most / sp.heads + B) / B;
+  int parts = 1;  // about eight pieces a part
+  while (parts * D < 1024 && 8 * parts < pieces) parts *= 2;
+  kv_join_kernel<<<dim3((unsigned)(B * Hq)), dim3(D, parts), 0, st>>>(ws, part_ml, meta, sp, sh, (int)Hq,
+                                                                     reinterpret_cast<f16*>(out));
   return hipGetLastError();
 }
 

@@ -54,4 +54,28 @@ __host__ __device__ inline int64_t kv_length(const KvShape& s, int32_t length, i
   return n < (width << s.ps) ? n : width << s.ps;
 }
 
+// Attention's split: sequences are counted in units of kKvUnit tokens (an empty one as
+// one unit, whose block stores its zeros) and cut into pieces of at most 2^shift units,
+// the pieces of a sequence as even as whole units allow; pieces are numbered sequence
+// by sequence.
+constexpr int kKvUnit = 128;
+
+__host__ __device__ inline int kv_units(int len) { return len > 0 ? (len + kKvUnit - 1) / kKvUnit : 1; }
+
+// log2 of the units of a piece: up to 4 units while all heads' pieces are more than about
+// 512, and on while they are more than about `most`.
+__host__ __device__ inline int kv_piece_shift(int64_t total, int heads, int most) {
+  int shift = 0;
+  while (shift < 2 && total * heads > (512 << shift)) ++shift;
+  while (shift >= 2 && shift < 18 && total * heads > ((int64_t)most << shift)) ++shift;  // 2^18 units: any sequence
+  return shift;
+}
+__host__ __device__ inline int kv_pieces(int units, int shift) { return (units + (1 << shift) - 1) >> shift; }
+
+// The most pieces of a head: B sequences of at most max_len tokens.
+__host__ __device__ inline int64_t kv_most_pieces(int64_t B, int max_len, int heads, int most) {
+  const int64_t units = B * kv_units(max_len), pieces = (most > 512 ? most : 512) / heads + 1 + B;
+  return pieces < units ? pieces : units;
+}
+
 }  // namespace awq
