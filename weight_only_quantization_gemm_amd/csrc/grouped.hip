@@ -158,8 +158,8 @@ __device__ __forceinline__ int stage_bytes(unsigned char* dst, const unsigned ch
 // per instruction, which alone takes longer than the memory: 20 us against 13
 // below.)  The waves' tiles are summed through LDS in a fixed order.
 // One token through 2 of 8 experts of 11008 x 4096: 47 MB in 13 us (3.6 TB/s); 45
-// tokens x 6 over 64 3-bit experts of 2048 x 1408: 73 MB in 23 us (3.2 TB/s), the
-// vector ALU 28 % and the address units 50 % busy.
+// tokens x 6 over 64 3-bit experts of 2048 x 1408: 73 MB in 22 us (3.3 TB/s), the
+// vector ALU 25 % and the address units 50 % busy.
 template <int BITS, int RW, int S>
 struct RingShape {
   static constexpr int NW = BITS == 4 ? RW : (3 * RW + 3) / 4;  // 1 KB loads of a stage

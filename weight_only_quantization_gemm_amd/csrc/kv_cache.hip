@@ -109,7 +109,7 @@ __device__ __forceinline__ f16x8 read_row(KvHalf c, int64_t row, int lane) {
 // block takes consecutive tokens of one head (the next block the next head): the
 // division by the number of heads is the block's own, and a prompt's parameters,
 // 4 bytes a row, leave a block side by side.  8000 tokens x 32 heads of 128 to 8
-// bits: 198 MB in 46 us (4.3 TB/s; 50 us with loads that stay in the caches, 47
+// bits: 198 MB in 41 to 46 us (4.3 to 4.8 TB/s; 50 us with loads that stay in the caches, 47
 // with the quantizer left out), read back in 30 us (6.6 TB/s).
 template <int D, int BITS>
 __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(const f16* __restrict__ k, const f16* __restrict__ v,

@@ -10,8 +10,9 @@
 // pairs, a lane's rank among the 64 pairs of its wave coming from ballots on the
 // bits of the expert.  No order depends on timing.
 // All of it is bound by launches and latency: up to kSmallPairs pairs one block
-// does everything in one launch (45 tokens x 6 of 64 experts: one launch of
-// 6 us where four took 10); beyond, three launches.  The sum is bound by memory.
+// does everything in one launch (32 tokens x 6 of 64 experts: 5.5 us, where a
+// launch for each step took 10.4); beyond, three launches (16384 tokens x 8 of
+// 128: 16 us).  The sum is bound by memory.
 #include "awq_common.h"
 #include "awq_internal.h"
 
@@ -68,8 +69,8 @@ struct RouteArgs {
 // Tokens t0 .. t0 + count - 1, one for each run of L lanes in turn (V logits per
 // lane, E <= L V); lane j of the run writes the j-th choice and its weight, and
 // the expert to copy [count * top_k] too.  Four tokens a wave (L = 16) share every
-// instruction of the choice; one token a wave was bound by the vector ALU (16384
-// tokens x 8 of 128: 13.8 us against 6).
+// instruction of the choice; one token a wave was bound by the vector ALU (choosing
+// and counting 16384 tokens x 8 of 128: 13.8 us against 8.6).
 template <int V, int L>
 __device__ inline void route_tokens(const RouteArgs& a, int64_t t0, int count, int E, int32_t* __restrict__ experts,
                                     int* copy) {
@@ -282,7 +283,9 @@ __global__ __launch_bounds__(kMoeThreads) void plan_place_kernel(const int32_t* 
         rows, pos);
 }
 
-// out[t][n] = sum_j weights[t][j] y[pos[t * k + j]][n], 8 channels per thread.
+// out[t][n] = sum_j weights[t][j] y[pos[t * k + j]][n], 8 channels per thread.  Every
+// byte is moved once: 8192 tokens x 4 rows of 4096, 336 MB in 58 us (5.8 TB/s; 67
+// us with one row's load under way at a time, kept in the caches).
 __global__ __launch_bounds__(256) void combine_kernel(const f16* __restrict__ y, int64_t R,
                                                       const int32_t* __restrict__ pos,
                                                       const float* __restrict__ weights, int64_t T, int top_k,
