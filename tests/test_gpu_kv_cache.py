@@ -334,6 +334,32 @@ def test_attention_query_magnitudes(gain, bits):
     assert np.all(np.abs(y - ref) <= tol)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_attention_has_no_bias_over_long_sequences(bits):
+    """The output of 100000 tokens of no common direction is a small difference of large sums: the
+    mean error over the channels (in which roundings of the output cancel, as 5 standard
+    deviations of their mean allow) stays within what the weights' 2^-22 and the products' 2^-22
+    of those sums leave."""
+    n, D, r = 100000, 128, 5
+    c = random_cache(n // 16 + 1, 1, D, 16, bits, 29)
+    q = np.random.default_rng(30).standard_normal((1, r, D)).astype(np.float16)
+    table, lengths = np.random.default_rng(31).permutation(n // 16 + 1)[None].astype(np.int32), np.array([n], np.int32)
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(lengths))).astype(np.float64)
+    h = host_cache(c)
+    pg, at = table[0, np.arange(n) // 16], np.arange(n) % 16
+    kc, vc = (unpack(h[x + "_codes"][pg, 0, at], bits).astype(np.float64) for x in "kv")
+    kp, vp = (h[x + "_params"][pg, 0, at].astype(np.float64) for x in "kv")
+    s = D ** -0.5 * (q[0].astype(np.float64) @ ((kc - kp[:, 1:]) * kp[:, :1]).T)
+    p = np.exp(s - s.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    out, mag = p @ ((vc - vp[:, 1:]) * vp[:, :1]), p @ ((vc + vp[:, 1:]) * vp[:, :1])
+    err = (y[0] - out).reshape(r, D // 8, 8)
+    rounding = 2.0 ** -11 * np.sqrt((out ** 2).mean())  # at most half a step each
+    for i in range(8):
+        e = err[:, :, i]
+        assert abs(e.mean()) <= 2.0 ** -21 * mag.mean() + 5 * rounding / np.sqrt(3 * e.size)
+
+
 @pytest.mark.parametrize("n", [40, 5000])
 def test_attention_of_nan(n):
     """A NaN in one query head makes that head's output NaN, in one chunk and in many, and no other."""

@@ -3,12 +3,16 @@
 // For a sequence of n tokens, a query head's row q and the key-value head it
 // belongs to:  s_t = a q . k_t,  out = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m)
 // over t < n, with k_t = scale_t (code_t - zero_t) and v_t alike.  The codes are
-// never expanded to fp16 values.  A 4- or 8-bit whole number c in the low bits
-// of a half is the fp16 subnormal c 2^-24, which the matrix cores take exactly,
-// so unpacking is one mask (and a shift for every second pair); scale and zero
-// point, one of each per token, stay outside the products:
-//   q . k_t = scale_t (2^24 q . [c_t] - zero_t sum(q)),
-//   sum_t p_t v_t = 2^24 sum_t (p_t scale_t) [c_t] - sum_t (p_t scale_t) zero_t.
+// never expanded to fp16 values.  An 8-bit whole number c in the low bits of a
+// half is the fp16 subnormal c 2^-24, which the matrix cores take, so unpacking is
+// a mask and a shift; a 4-bit one is brought to bits 4 .. 7 and is c 2^-20.  (The
+// products of subnormal operands are cut off below 2^-24 of what an operand without
+// leading zeros would make: 4-bit codes in bits 0 .. 3 lost 2^-18 of a product,
+// which the difference below made 4e-4 of the output of 54000 tokens; the two more
+// shifts a word cost 2 % of the time, 10 % at 64 channels.)  Scale and zero
+// point, one of each per token, stay outside the products; u = 2^20 or 2^24:
+//   q . k_t = scale_t (u q . [c_t] - zero_t sum(q)),
+//   sum_t p_t v_t = u sum_t (p_t scale_t) [c_t] - sum_t (p_t scale_t) zero_t.
 // Everything but the operands q (fp16 as given) and w_t = p_t scale_t is kept in
 // fp32; w_t enters the products as the sum of two fp16 numbers, which leaves
 // 2^-22 of it (one would add an error of the size of the output's own rounding).
@@ -21,9 +25,9 @@
 //
 // Bound by reading the cache: 64 sequences of 4096 tokens x 8 heads of 128 at 4
 // bits, 287 MB in 61 us (4.7 TB/s); 32 of 2000 to 6000 at 8 bits, 269 MB in 62 us;
-// 64 ragged ones of 2000 to 6000 tokens at 4 bits 279 MB in 67 us, the last blocks
+// 64 ragged ones of 2000 to 6000 tokens at 4 bits 279 MB in 68 us, the last blocks
 // leaving units idle; one of 2000 tokens 10 us, launches and latency.  The vector
-// ALU is busy 49 % of the time.
+// ALU is busy about half of the time.
 //
 // Lanes.  With l = 16 b + n, the products are 16 x 16 x 32:
 //   scores  A = codes of 16 tokens (row n: token; lane's channels D/4 b ..),
@@ -43,7 +47,6 @@ constexpr int kAttWaves = 4;
 constexpr int kAttStep = 32;       // tokens a wave takes at a time
 constexpr int kAttHeads = 16;      // query heads of a block: columns of a product
 constexpr float kSlack = 8.f;      // a score may pass the running maximum by this (log2) before all is rescaled
-constexpr float kTwo24 = 16777216.f;
 constexpr int kNonTemporal = 2;    // cache policy of the code loads: every line is used once (54 against 61 us on long sequences)
 constexpr int kAttWindow = 1024;   // tokens whose pages a wave's lanes hold, 16 each
 
@@ -56,10 +59,10 @@ __host__ __device__ constexpr int att_channel(int n, int c) {
   return n * (D / 16) + c;
 }
 
-// Whether tile c's codes come times 16 (the upper nibble of each byte).
-template <int BITS>
-__host__ __device__ constexpr bool att_times16(int c) {
-  return BITS == 4 && (c & 1);
+// Four words of halves whose bits 0 .. 15 are four 4-bit codes: code k of each times 16.
+template <int k>
+__device__ __forceinline__ u32x4 nibbles(u32x4 x) {
+  return (k == 0 ? x << 4 : (k == 1 ? x : (k == 2 ? x >> 4 : x >> 8))) & 0x00F000F0u;
 }
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -152,6 +155,7 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
     float* __restrict__ part_ml, int32_t* __restrict__ meta) {
   using A = AttStage<D, BITS>;
   constexpr int TILES = D / 16, RB = A::RB;
+  constexpr float kUnit = BITS == 4 ? 1048576.f : 16777216.f;  // codes enter the products divided by this
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -230,48 +234,26 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
   const int turns = steps > wave ? (steps - wave + kAttWaves - 1) / kAttWaves : 0;
   if (turns > 0) issue(wave, 0, pages);
 
-  // q: columns past the block's heads repeat the last one and are never stored.  At 4 bits a head
-  // is multiplied by the power of two that brings its largest channel to 2^14 .. 2^15 (larger ones
-  // stay), so that the sixteenth of a small q, the operand of an upper nibble, keeps its bits; the
-  // factor takes it back (1 us of 70 for 64 sequences of 2000 to 6000 tokens).  A negative factor
-  // goes to q's sign, so that larger sums are larger scores; one of 0 is taken as 2^-100, which
-  // leaves a masked score (-infinity) what it is.
+  // q: columns past the block's heads repeat the last one and are never stored.  A negative
+  // factor goes to q's sign, so that larger sums are larger scores; one of 0 is taken as
+  // 2^-100, which leaves a masked score (-infinity) what it is.
+  const float factor = fmaxf(fabsf(scale_log2) * kUnit, 7.888609e-31f);
   const int hn = n < heads ? n : heads - 1;
   const f16* qrow = q + seq * q_stride + (int64_t)(hk * ratio + h0 + hn) * D;
   f16x8 qf[D / 32];
-#pragma unroll
-  for (int s = 0; s < D / 32; ++s) qf[s] = *reinterpret_cast<const f16x8*>(qrow + b * (D / 4) + 8 * s);
-  int up = 0;
-  if constexpr (BITS == 4) {
-    float most = 0.f;
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)qf[s][j]));
-    most = fmaxf(most, __shfl_xor(most, 16, kWave));
-    most = fmaxf(most, __shfl_xor(most, 32, kWave));
-    int e = 15;
-    if (most > 0.f) (void)frexpf(most, &e);  // most in [2^(e - 1), 2^e)
-    up = e < 15 ? 15 - e : 0;
-  }
-  const float factor = fmaxf(ldexpf(fabsf(scale_log2) * kTwo24, -up), 7.888609e-31f);
   float qz = 0.f;
-  const float gain = ldexpf(scale_log2 < 0.f ? -1.f : 1.f, up);
 #pragma unroll
   for (int s = 0; s < D / 32; ++s) {
-    f16x8 x;
+    f16x8 x = *reinterpret_cast<const f16x8*>(qrow + b * (D / 4) + 8 * s);
+    if (scale_log2 < 0.f) x = -x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = (f16)((float)qf[s][j] * gain);
-      qz += (float)x[j];
-    }
-    const f16 t = (f16)0.0625f;
-    if (BITS == 4) qf[s] = f16x8{x[0], x[1], x[2] * t, x[3] * t, x[4], x[5], x[6] * t, x[7] * t};
+    for (int j = 0; j < 8; ++j) qz += (float)x[j];
+    if (BITS == 4) qf[s] = x;
     else qf[s] = f16x8{x[0], x[2], x[1], x[3], x[4], x[6], x[5], x[7]};
   }
   qz += __shfl_xor(qz, 16, kWave);
   qz += __shfl_xor(qz, 32, kWave);
-  qz *= -1.f / kTwo24;
+  qz *= -1.f / kUnit;
 
   // Weights are kept as 2^(factor x - ref), ref following the largest score less
   // the exponent F that brings the largest value scale to 2^6 .. 2^7: a weight
@@ -311,8 +293,8 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
       for (int t = 0; t < D / 32; ++t) {
         u32x4 a;
         if (BITS == 4) {
-          const uint32_t w8 = w[t] >> 8;
-          a = u32x4{w[t] & 0x000F000Fu, w[t] & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
+          const uint32_t x = w[t];
+          a = u32x4{(x << 4) & 0x00F000F0u, x & 0x00F000F0u, (x >> 4) & 0x00F000F0u, (x >> 8) & 0x00F000F0u};
         } else {
           a = u32x4{w[2 * t] & 0x00FF00FFu, (w[2 * t] >> 8) & 0x00FF00FFu, w[2 * t + 1] & 0x00FF00FFu,
                     (w[2 * t + 1] >> 8) & 0x00FF00FFu};
@@ -413,16 +395,14 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
     if constexpr (BITS == 4) {
 #pragma unroll
       for (int g = 0; g < TILES / 4; ++g) {  // halves of the lane's words
-        u32x4 x, x8;
+        u32x4 x;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; ++j)
           x[j] = perm(v[2 * j + 1][g / 2], v[2 * j][g / 2], g % 2 ? 0x07060302u : 0x05040100u);
-          x8[j] = x[j] >> 8;
-        }
-        mac(x & 0x000F000Fu, o[4 * g]);
-        mac(x & 0x00F000F0u, o[4 * g + 1]);
-        mac(x8 & 0x000F000Fu, o[4 * g + 2]);
-        mac(x8 & 0x00F000F0u, o[4 * g + 3]);
+        mac(nibbles<0>(x), o[4 * g]);
+        mac(nibbles<1>(x), o[4 * g + 1]);
+        mac(nibbles<2>(x), o[4 * g + 2]);
+        mac(nibbles<3>(x), o[4 * g + 3]);
       }
     } else {
 #pragma unroll
@@ -478,7 +458,7 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         red_o[(wave * heads + n) * D + att_channel<D, BITS>(4 * b + r, c)] =
-            o[c][r] * (att_times16<BITS>(c) ? kTwo24 / 16.f : kTwo24) - oz[r];
+            o[c][r] * kUnit - oz[r];
   }
   __syncthreads();
   const int64_t head0 = (int64_t)seq * Hq + hk * ratio + h0;
@@ -583,8 +563,8 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
 // Where the bound leaves a choice (chunks above 128 tokens, several a sequence), batches of
 // up to kPieceBatch make it by the lengths on the device instead, which costs a block's
 // start up to 1 us and serves page tables made for longer sequences (bounds of 131072
-// tokens, by the bound / by the lengths: 8 sequences of 2000 44.5 / 15.8 us, 64 of 2000 to
-// 6000 161 / 67, 256 of 1000 212 / 62) and ragged batches (32 of up to 30000 127 / 110);
+// tokens, by the bound / by the lengths: 8 sequences of 2000 44.5 / 15.4 us, 64 of 2000 to
+// 6000 161 / 68, 256 of 1000 212 / 63) and ragged batches (32 of up to 30000 127 / 110);
 // with tight bounds 64 of 4096 61.6 / 60.8, 16 of up to 2000 17.0 / 17.3, one of 30000
 // 18.9 / 20.1.
 static AttSplit att_split(int64_t B, int64_t Hkv, int ratio, int row_bytes, int64_t max_len) {
