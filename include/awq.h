@@ -450,8 +450,9 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
  * awq_gemm_grouped -- row i of the ragged batch times its expert's matrix:
  *   y[i][n] = sum_k xs_i[k] * w_hat_e[n][k],   offsets[e] <= i < offsets[e+1]
  * with xs_i = x[rows[i] / top_k] (rows as a plan's: the tokens are gathered by
- * the product itself) or x[i] (rows NULL), divided by s[e] and rounded to fp16
- * as by awq_scale_input when s is given.
+ * the product itself) or x[i] (rows NULL), divided by s[e] when s is given:
+ * rounded to fp16 as by awq_scale_input, or for few rows (R <= 2 E or 16, where
+ * the kernel for few rows is chosen) kept to 22 bits as the sum of two fp16 numbers.
  *   x        device fp16 [x_rows][K]
  *   rows     device int32 [R] or NULL; an entry that leads outside x reads
  *            some row of x instead
@@ -461,7 +462,8 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
  *   packed, scales, zeros   device, the E matrices
  *   y        device fp16 [R][N]; rows from offsets[E] on are left as they were
  *   workspace  device, >= awq_gemm_grouped_workspace_bytes(R, K, s given)
- *            bytes: R * K * 2 rounded up to 256 with s, 0 (may be NULL) without
+ *            bytes: with s R * K * 4 (* 2 above R = 2 * AWQ_MAX_EXPERTS) rounded
+ *            up to 256, without 0 (may be NULL)
  * Accumulation is fp32 and y is rounded to fp16 once; code - zero is exact and
  * the group's scale is applied in fp32, so no weight is rounded.  The sizes of
  * the groups stay on the device; the result does not depend on timing.

@@ -154,11 +154,11 @@ def inputs(M, K, seed):
     return x.astype(np.float16)
 
 
-def assert_rows(y, x, w, what):
-    """y [n][N] against x [n][K] w^T."""
+def assert_rows(y, x, w, what, rounding=0.0):
+    """y [n][N] against x [n][K] w^T; `rounding`: of x, relative."""
     ref = x.astype(np.float64) @ w.T
     mag = np.abs(x.astype(np.float64)) @ np.abs(w).T
-    tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + w.shape[1] * 2.0 ** -23 * mag
+    tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + (w.shape[1] * 2.0 ** -23 + rounding) * mag
     y = y.astype(np.float64)
     with np.errstate(invalid="ignore"):
         near = np.abs(y - ref) <= tol
@@ -190,8 +190,13 @@ def check_grouped(sizes, N, K, bits, seed, gather=None, scaled=False, extra=0):
     for e in range(E):
         a, b = offsets[e], offsets[e + 1]
         if a < b:
-            xe = (xr[a:b].astype(np.float32) / s[e]).astype(np.float16) if scaled else xr[a:b]
-            assert_rows(y[a:b], xe, w[e], f"expert {e}")
+            if scaled and (R > max(2 * E, 16) or "ring" not in awq.awq_gemm_grouped_kernel(R, E, N, K, bits)):
+                xe = (xr[a:b].astype(np.float32) / s[e]).astype(np.float16)
+                assert_rows(y[a:b], xe, w[e], f"expert {e}")
+            elif scaled:  # two fp16 numbers: half a step of the second, 2^-11 of at most 2^-11 of x / s, and fp32's 2^-24
+                assert_rows(y[a:b], xr[a:b].astype(np.float64) / s[e], w[e], f"expert {e}", 2.0 ** -22 + 2.0 ** -24)
+            else:
+                assert_rows(y[a:b], xr[a:b], w[e], f"expert {e}")
     assert np.all(y[offsets[-1]:] == 7.0), "rows behind the last expert were written"
     return y
 
@@ -233,6 +238,32 @@ def test_grouped_scaled_input(bits, rows):
     note(f"grouped scaled bits={bits} rows={rows}")
     check_grouped([rows, 1, 0, 2 * rows], 136, 512, bits, seed=rows + bits, gather=2, scaled=True, extra=1)
     check_grouped([rows, 1, 0, 2 * rows], 136, 512, bits, seed=rows + bits, scaled=True)
+    check_grouped([9, 8, 7, 0, 1] + [0] * 9, 136, 512, bits, seed=rows + bits, gather=2, scaled=True, extra=1)
+
+
+@pytest.mark.parametrize("bits", [4, 3])
+@pytest.mark.parametrize("rows", [1, 8])
+def test_grouped_scaled_input_of_few_rows_is_not_rounded_to_fp16(bits, rows):
+    """x / s enters with 22 bits: no larger error than the roundings of y itself (each at most half
+    a step) and of fp32 sums leave, where x / s rounded to fp16 would miss by up to 2^-11 of each
+    of a few large products.  An x / s above fp16's largest number is infinity."""
+    N, K, E = 200, 512, 2
+    w, p, sc, z = layer(E, N, K, bits, 41)
+    x = inputs(2 * rows, K, 42)
+    x[:, 5] *= 30
+    s = np.exp(0.4 * np.random.default_rng(43).standard_normal((E, K))).astype(np.float32)
+    off = dev(np.array([0, rows, 2 * rows], np.int32))
+    assert "ring" in awq.awq_gemm_grouped_kernel(2 * rows, E, N, K, bits)
+    y = host(awq.awq_gemm_grouped(dev(x), p, sc, z, off, s=dev(s)))
+    for e in range(E):
+        a = e * rows
+        ref = (x[a:a + rows].astype(np.float64) / s[e]) @ w[e].T
+        mag = np.abs(x[a:a + rows].astype(np.float64) / s[e]) @ np.abs(w[e]).T
+        assert np.all(np.abs(y[a:a + rows] - ref) <= 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2.0 ** -20 * mag)
+    x[0, 9], s[0, 9] = 60000, 0.25
+    y = host(awq.awq_gemm_grouped(dev(x), p, sc, z, off, s=dev(s)))
+    with np.errstate(invalid="ignore"):
+        assert np.array_equal(y[0].astype(np.float64), np.inf * w[0, :, 9], equal_nan=True)
 
 
 @pytest.mark.parametrize("bits", [4, 3])

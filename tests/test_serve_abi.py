@@ -61,7 +61,8 @@ BAD = {
                       dict(renormalize=2)],
     "awq_gemm_grouped": [dict(R=0), dict(x_rows=0), dict(x_rows=9, rows=None), dict(top_k=0), dict(E=0), dict(E=1025),
                          dict(N=0), dict(K=100), dict(group=64), dict(bits=8), dict(R=(1 << 24) + 1), dict(K=1 << 21), dict(K=(1 << 17) + 128),
-                         dict(R=1 << 24, N=1 << 20, s=None), dict(R=1 << 24, s=FAKE)],
+                         dict(R=1 << 24, N=1 << 20, s=None), dict(R=1 << 24, s=FAKE),
+                         dict(R=2048, E=1024, N=1 << 19, s=FAKE)],
     "awq_moe_combine": [dict(T=0), dict(R=0), dict(top_k=0), dict(N=12), dict(N=0), dict(T=1 << 24, N=1 << 20)],
     "awq_kv_write": [dict(T=0), dict(T=(1 << 22) + 1), dict(T=1 << 22, H=64, k_stride=8192, v_stride=8192), dict(H=0), dict(H=1025), dict(D=96), dict(page=24), dict(page=8),
                      dict(page=2048), dict(pages=0), dict(pages=1 << 27), dict(bits=3), dict(k_stride=128),
@@ -88,7 +89,8 @@ def test_workspaces():
                         ("awq_kv_attention", awq.awq_kv_attention_workspace_bytes(3, 8, 2, 128, 4, 1024))):
         assert need > 0 and need % 256 == 0
         assert call(entry, workspace_bytes=need - 1) == WS_SMALL
-    assert awq.awq_gemm_grouped_workspace_bytes(10, 256, True) == 10 * 256 * 2
+    assert awq.awq_gemm_grouped_workspace_bytes(10, 256, True) == 10 * 256 * 4
+    assert awq.awq_gemm_grouped_workspace_bytes(2049, 256, True) == 2049 * 256 * 2
     assert awq.awq_gemm_grouped_workspace_bytes(10, 256, False) == 0
     assert awq.awq_gemm_grouped_workspace_bytes(10, 100, True) == 0
     assert awq.awq_moe_workspace_bytes(0, 8, 2) == 0 and awq.awq_moe_workspace_bytes(5, 8, 65) == 0

@@ -101,7 +101,8 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
 
 size_t awq_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int32_t scaled) {
   if (R < 1 || R > AWQ_MAX_PAIRS || K < 1 || K > kMaxGroupedK || K % AWQ_GROUP != 0 || scaled == 0) return 0;
-  return ((size_t)R * (size_t)K * 2 + 255) / 256 * 256;
+  const size_t bytes = R <= 2 * AWQ_MAX_EXPERTS ? 4 : 2;  // x / s of few rows is two numbers
+  return ((size_t)R * (size_t)K * bytes + 255) / 256 * 256;
 }
 
 int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t top_k, const int32_t* offsets,

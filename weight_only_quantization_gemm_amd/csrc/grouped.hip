@@ -103,13 +103,14 @@ __device__ inline int64_t x_row(const int32_t* __restrict__ rows, int i, int top
   return r < 0 ? 0 : (r < x_rows ? r : x_rows - 1);
 }
 
-// xs[i] = fp16(fp32(x of row i) / s of its expert): the input side of the
-// per-channel scaling, one block per row of the ragged batch.
+// xs[i] = fp16(fp32(x of row i) / s of its expert), the input side of the
+// per-channel scaling, and where `lo` is given what that rounding took off (0 of an
+// infinity), rounded to fp16 too: one block per row of the ragged batch.
 __global__ __launch_bounds__(256) void scale_rows_kernel(const f16* __restrict__ x, int64_t x_rows,
                                                          const int32_t* __restrict__ rows, int top_k,
                                                          const int32_t* __restrict__ offsets,
                                                          const float* __restrict__ s, int E, int R, int64_t K,
-                                                         f16* __restrict__ xs) {
+                                                         f16* __restrict__ xs, f16* __restrict__ lo) {
   const int i = (int)blockIdx.x;
   const RowTile t = find_tile(offsets, E, R, i, 1);
   if (t.rows == 0) return;
@@ -118,10 +119,16 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const f16* __restrict__
   f16* dst = xs + (int64_t)t.row * K;
   for (int64_t k = threadIdx.x * 8; k < K; k += 256 * 8) {
     const f16x8 v = *reinterpret_cast<const f16x8*>(src + k);
-    f16x8 o;
+    f16x8 o, rest;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = (f16)((float)v[j] / sc[k + j]);
+    for (int j = 0; j < 8; ++j) {
+      const float q = (float)v[j] / sc[k + j];
+      o[j] = (f16)q;
+      const float r = q - (float)o[j];
+      rest[j] = (f16)(fabsf(r) < INFINITY ? r : 0.f);
+    }
     *reinterpret_cast<f16x8*>(dst + k) = o;
+    if (lo != nullptr) *reinterpret_cast<f16x8*>(lo + (int64_t)t.row * K + k) = rest;
   }
 }
 
@@ -160,6 +167,10 @@ __device__ __forceinline__ int stage_bytes(unsigned char* dst, const unsigned ch
 // One token through 2 of 8 experts of 11008 x 4096: 47 MB in 13 us (3.6 TB/s); 45
 // tokens x 6 over 64 3-bit experts of 2048 x 1408: 73 MB in 22 us (3.3 TB/s), the
 // vector ALU 25 % and the address units 50 % busy.
+// PAIRS: a scaled x of few rows is two fp16 numbers, the second at x + lo (x / s
+// rounded to one adds an error of the size of y's own rounding, more where a few
+// channels of few rows make most of the sums).  The tile is then 8 rows, the second
+// numbers its rows 8 .. 15, and the two products of a row are added at the end.
 template <int BITS, int RW, int S>
 struct RingShape {
   static constexpr int NW = BITS == 4 ? RW : (3 * RW + 3) / 4;  // 1 KB loads of a stage
@@ -176,18 +187,19 @@ struct RingShape {
   }
 };
 
-template <int BITS, int RW, int S>
+template <int BITS, int RW, int S, bool PAIRS>
 __global__ __launch_bounds__(512) void grouped_ring_kernel(
-    const f16* __restrict__ x, int64_t x_rows, const int32_t* __restrict__ rows, int top_k,
+    const f16* __restrict__ x, int64_t lo, int64_t x_rows, const int32_t* __restrict__ rows, int top_k,
     const int32_t* __restrict__ offsets, const uint32_t* __restrict__ packed, const f16* __restrict__ scales,
     const uint8_t* __restrict__ zeros, f16* __restrict__ y, int R, int E, int64_t N, int64_t K, int nt, int waves) {
   using Q = RingShape<BITS, RW, S>;
+  constexpr int kRows = PAIRS ? 8 : 16;  // of a tile
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int G = (int)(K / kGroup), P2 = (G + 1) / 2;
   const int lane = threadIdx.x & 63, nl = lane & 15, kq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mb = (int)blockIdx.x / nt;
-  const RowTile tile = find_tile(offsets, E, R, mb, 16);
+  const RowTile tile = find_tile(offsets, E, R, mb, kRows);
   if (tile.rows == 0) return;
   const int64_t W = BITS == 4 ? K / 8 : 3 * (K / 32);
   const int64_t n0 = (int64_t)((int)blockIdx.x - mb * nt) * (16 * RW), first = (int64_t)tile.expert * N + n0;
@@ -219,7 +231,9 @@ __global__ __launch_bounds__(512) void grouped_ring_kernel(
   sl += stage_bytes(sl, reinterpret_cast<const unsigned char*>(scales), first * G * 2, (int64_t)cols * G * 2,
                     ssw, waves, wave, lane, threadIdx.x);
   zl += stage_bytes(zl, zeros, first * P2, (int64_t)cols * P2, ScaleSwizzle(0), waves, wave, lane, threadIdx.x);
-  const f16* xs = x + x_row(rows, tile.row + (nl < tile.rows ? nl : tile.rows - 1), top_k, x_rows) * K + kq * 32;
+  const int xr = nl & (kRows - 1);
+  const f16* xs = x + x_row(rows, tile.row + (xr < tile.rows ? xr : tile.rows - 1), top_k, x_rows) * K + kq * 32;
+  if (PAIRS && nl >= kRows) xs += lo;
   struct Fragment {
     f16x8 a[4];
   };
@@ -303,7 +317,10 @@ __global__ __launch_bounds__(512) void grouped_ring_kernel(
   for (int i = threadIdx.x; i < tile.rows * NC; i += waves * 64) {
     const int m = i / NC, c = i - m * NC;
     float v = 0.f;
-    for (int u = 0; u < waves; ++u) v += red[(u * 16 + m) * PITCH + c];
+    for (int u = 0; u < waves; ++u) {
+      v += red[(u * 16 + m) * PITCH + c];
+      if (PAIRS) v += red[(u * 16 + m + kRows) * PITCH + c];
+    }
     if (n0 + c < N) y[(int64_t)(tile.row + m) * N + n0 + c] = (f16)v;
   }
 }
@@ -572,7 +589,7 @@ static int pipe_stages_that_fit(int64_t G, int bits) {
 }
 
 template <int BITS, int AB, int WMW>
-static hipError_t pipe_launch(const f16* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
+static hipError_t pipe_launch(const f16* x, int64_t, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
                               const void* packed, const void* scales, const void* zeros, void* y, int64_t R, int E,
                               int64_t N, int64_t K, hipStream_t st) {
   if (pipe_stages_that_fit<AB, WMW>(K / kGroup, BITS) == 3)
@@ -581,12 +598,12 @@ static hipError_t pipe_launch(const f16* x, int64_t x_rows, const int32_t* rows,
 }
 
 template <int BITS, int RW>
-static hipError_t ring_launch(const f16* x, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
+static hipError_t ring_launch(const f16* x, int64_t lo, int64_t x_rows, const int32_t* rows, int top_k, const int32_t* offsets,
                               const void* packed, const void* scales, const void* zeros, void* y, int64_t R, int E,
                               int64_t N, int64_t K, hipStream_t st) {
   constexpr int S = 2;  // deeper rings cost blocks per compute unit: 3 and 4 stages were 2 .. 30 % slower
   const int G = (int)(K / kGroup);
-  const int64_t nt = (N + 16 * RW - 1) / (16 * RW), blocks = nt * row_tiles(R, E, 16);
+  const int64_t nt = (N + 16 * RW - 1) / (16 * RW), blocks = nt * row_tiles(R, E, lo ? 8 : 16);
   // Waves per block: ten for each compute unit in all, or eight a block.  One token through 2 of 8
   // experts of 11008 x 4096: 17.2, 14.8, 12.6, 13.1 us with 1, 2, 4, 8; 45 tokens x 6 over 64 3-bit
   // experts of 2048 x 1408: 23.0, 23.5, 30.0, 36.7 us.
@@ -594,10 +611,11 @@ static hipError_t ring_launch(const f16* x, int64_t x_rows, const int32_t* rows,
   while (waves < 8 && 2 * waves <= G && blocks * waves < 2500) waves *= 2;
   if (KernelPlan* p = active_plan())
     return plan_record(p, "grouped_ring_kernel<%d,%d,%d> block=%d grid=%lld", BITS, RW, S, 64 * waves, (long long)blocks);
-  grouped_ring_kernel<BITS, RW, S><<<dim3((unsigned)blocks), dim3(64 * waves), RingShape<BITS, RW, S>::bytes(waves, G),
-                                     st>>>(
-      x, x_rows, rows, top_k, offsets, reinterpret_cast<const uint32_t*>(packed), reinterpret_cast<const f16*>(scales),
-      reinterpret_cast<const uint8_t*>(zeros), reinterpret_cast<f16*>(y), (int)R, E, N, K, (int)nt, waves);
+  auto kernel = lo ? grouped_ring_kernel<BITS, RW, S, true> : grouped_ring_kernel<BITS, RW, S, false>;
+  kernel<<<dim3((unsigned)blocks), dim3(64 * waves), RingShape<BITS, RW, S>::bytes(waves, G), st>>>(
+      x, lo, x_rows, rows, top_k, offsets, reinterpret_cast<const uint32_t*>(packed),
+      reinterpret_cast<const f16*>(scales), reinterpret_cast<const uint8_t*>(zeros), reinterpret_cast<f16*>(y), (int)R, E,
+      N, K, (int)nt, waves);
   return hipGetLastError();
 }
 
@@ -623,13 +641,23 @@ static Kernel grouped_choice(int64_t R, int64_t E, int64_t N, int64_t K, int bit
   return R > E && RingShape<4, 4, 2>::bytes(8, (int)G) <= kGrpLds ? Kernel::ring4 : Kernel::ring2;
 }
 
+// Whether a scaled x is two fp16 numbers, in tiles of half as many rows: costs 2 % while experts
+// have a row or two (2 rows of 8 experts of 11008 x 4096 16.5 -> 16.8 us, 60 of 64 of 2048 x 1408
+// 16.8 -> 17.5, 16 of 8 40.3 -> 42.8) and 15 to 25 % at five and seven.  More rows are rounded as
+// awq_scale_input rounds them, an error that averages to that of y's own rounding.
+static bool paired(Kernel choice, int64_t R, int64_t E) {
+  return (choice == Kernel::ring2 || choice == Kernel::ring4) && (R <= 2 * E || R <= 16);
+}
+
 // Whether the chosen kernel's grid (2^32 threads at most) covers the batch.
 bool gemm_grouped_fits(int64_t R, int64_t E, int64_t N, int64_t K, int bits, bool scaled) {
   if (scaled && R >= (int64_t(1) << 24)) return false;  // a block of 256 threads per row
   const int64_t nt = (N + kGBN - 1) / kGBN;
-  switch (grouped_choice(R, E, N, K, bits)) {
-    case Kernel::ring2: return (N + 31) / 32 * row_tiles(R, E, 16) < (int64_t(1) << 23);
-    case Kernel::ring4: return (N + 63) / 64 * row_tiles(R, E, 16) < (int64_t(1) << 23);
+  const Kernel choice = grouped_choice(R, E, N, K, bits);
+  const int64_t ring = row_tiles(R, E, scaled && paired(choice, R, E) ? 8 : 16);
+  switch (choice) {
+    case Kernel::ring2: return (N + 31) / 32 * ring < (int64_t(1) << 23);
+    case Kernel::ring4: return (N + 63) / 64 * ring < (int64_t(1) << 23);
     case Kernel::rows64: return nt * row_tiles(R, E, 64) + 127 < (int64_t(1) << 24);
     case Kernel::rows256: return nt * row_tiles(R, E, 256) + 127 < (int64_t(1) << 23);
   }
@@ -640,18 +668,23 @@ hipError_t launch_gemm_grouped(const void* x, int64_t x_rows, const int32_t* row
                                const float* s, const void* packed, const void* scales, const void* zeros, void* y,
                                int64_t R, int E, int64_t N, int64_t K, int bits, void* ws, hipStream_t st) {
   const f16* xp = reinterpret_cast<const f16*>(x);
+  const Kernel choice = grouped_choice(R, E, N, K, bits);
+  int64_t lo = 0;  // elements from x to the second halves of a scaled one
   if (s != nullptr && active_plan() == nullptr) {
-    scale_rows_kernel<<<dim3((unsigned)R), dim3(256), 0, st>>>(xp, x_rows, rows, top_k, offsets, s, E, (int)R, K,
-                                                               reinterpret_cast<f16*>(ws));
+    f16* xs = reinterpret_cast<f16*>(ws);
+    if (paired(choice, R, E)) lo = R * K;
+    scale_rows_kernel<<<dim3((unsigned)R), dim3(256), 0, st>>>(xp, x_rows, rows, top_k, offsets, s, E, (int)R, K, xs,
+                                                               lo ? xs + lo : nullptr);
     if (hipError_t e = hipGetLastError()) return e;
-    xp = reinterpret_cast<const f16*>(ws);
+    xp = xs;
     x_rows = R;
     rows = nullptr;
   }
 #define AWQ_GROUPED(launch, ...)                                                                          \
-  return bits == 4 ? launch<4, __VA_ARGS__>(xp, x_rows, rows, top_k, offsets, packed, scales, zeros, y, R, E, N, K, st) \
-                   : launch<3, __VA_ARGS__>(xp, x_rows, rows, top_k, offsets, packed, scales, zeros, y, R, E, N, K, st)
-  switch (grouped_choice(R, E, N, K, bits)) {
+  return bits == 4                                                                                        \
+             ? launch<4, __VA_ARGS__>(xp, lo, x_rows, rows, top_k, offsets, packed, scales, zeros, y, R, E, N, K, st) \
+             : launch<3, __VA_ARGS__>(xp, lo, x_rows, rows, top_k, offsets, packed, scales, zeros, y, R, E, N, K, st)
+  switch (choice) {
     case Kernel::ring2: AWQ_GROUPED(ring_launch, 2);
     case Kernel::ring4: AWQ_GROUPED(ring_launch, 4);
     case Kernel::rows64: AWQ_GROUPED(pipe_launch, 2, 1);
