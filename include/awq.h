@@ -558,7 +558,7 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
  *               used.  A sequence with no tokens gets out = 0
  *   out         device fp16 [B][Hq][D]
  *   max_len     host bound on the lengths (0: table_width * page), at most
- *               AWQ_MAX_KV_LENGTH.  Up to 256 sequences the work is split by
+ *               AWQ_MAX_KV_LENGTH.  Up to 1024 sequences the work is split by
  *               the lengths themselves, beyond by the bound
  *   workspace   device, >= awq_kv_attention_workspace_bytes(B, Hq, Hkv, D, bits,
  *               the bound) bytes; it needs no clearing and keeps nothing

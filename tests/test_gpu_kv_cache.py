@@ -210,20 +210,20 @@ def test_attention_many_sequences_take_larger_chunks():
 
 
 def test_attention_many_long_sequences_take_the_largest_chunks():
-    """Pieces whose pages are read in several runs of 1024 tokens; for more than 256 sequences
-    chunks of 4096 tokens and a second one behind them."""
+    """Pieces whose pages are read in several runs of 1024 tokens; for more than 1024
+    sequences chunks of 4096 tokens and a second one behind them."""
     n = np.random.default_rng(16).integers(2500, 4400, size=120)
     n[:4] = [4096, 4097, 4111, 0]
     check_attention(120, n, 8, 1, 64, 16, 4, seed=17)
-    n = np.random.default_rng(27).integers(0, 300, size=260)
-    n[[5, 100, 101, 259]] = [4400, 4096, 4097, 1025]
-    check_attention(260, n, 8, 1, 64, 16, 4, seed=28)
+    n = np.random.default_rng(27).integers(0, 300, size=1030)
+    n[[5, 100, 101, 1029]] = [4400, 4096, 4097, 1025]
+    check_attention(1030, n, 1, 2, 64, 16, 4, seed=28)
 
 
-@pytest.mark.parametrize("B", [1, 3, 64, 65, 255, 256, 257])
+@pytest.mark.parametrize("B", [1, 3, 64, 65, 255, 256, 257, 513, 1024, 1025])
 def test_attention_bound_far_above_the_lengths(B):
     """A page table made for 70000 tokens and sequences of a few hundred, some empty: the tokens
-    are shared out by the lengths, up to 256 sequences."""
+    are shared out by the lengths, up to 1024 sequences."""
     n = np.random.default_rng(B).integers(-100, 700, size=B)
     n[0] = 900
     check_attention(B, n, 2, 4, 64, 16, 4, seed=20 + B, width=4400 if B < 10 else 60)

@@ -100,52 +100,56 @@ struct AttSplit {
 };
 
 static_assert(kKvUnit == kAttStep * kAttWaves, "a unit is a step of every wave");
-constexpr int kPieceWindows = 4, kPieceBatch = 64 * kPieceWindows;
+constexpr int kPieceWindows = 4, kPieceRun = 64 * kPieceWindows, kPieceBatch = 1024;
 
-// The lengths of a batch and the pieces they make; lane i of window k holds sequence
-// 64 k + i.
+// The sequence of piece `slot`, counted from the lengths; lane i of window k holds
+// sequence s0 + 64 k + i of a run of sequences.
 struct PieceSplit {
-  int len[kPieceWindows], upto[kPieceWindows];  // pieces up to and with the sequence
-  int total, shift;
+  int seq, len;       // the piece's sequence and its length
+  int first, pieces;  // its first piece and their number
 
-  __device__ __forceinline__ void read(const AttSplit& sp, const KvShape& sh, int lane) {
-    int64_t units = 0;
+  // False where there are fewer pieces.
+  __device__ __forceinline__ bool find(const AttSplit& sp, const KvShape& sh, int lane, int slot) {
+    int held[kPieceWindows];
+    auto read = [&](int s0) {
 #pragma unroll
-    for (int k = 0; k < kPieceWindows; ++k)  // (sequences past the batch repeat its last and do not count)
-      len[k] = (int)kv_length(sh, sp.lengths[64 * k + lane < sp.batch ? 64 * k + lane : sp.batch - 1], sp.width, sp.max_len);
-#pragma unroll
-    for (int k = 0; k < kPieceWindows; ++k)
-      if (64 * k < sp.batch)
-        units += __builtin_amdgcn_readlane(wave_scan(64 * k + lane < sp.batch ? kv_units(len[k]) : 0), 63);
-    shift = kv_piece_shift(units, sp.heads, sp.most);
-    total = 0;
-#pragma unroll
-    for (int k = 0; k < kPieceWindows; ++k) {
-      upto[k] = total;
-      if (64 * k < sp.batch) {
-        upto[k] += wave_scan(64 * k + lane < sp.batch ? kv_pieces(kv_units(len[k]), shift) : 0);
-        total = __builtin_amdgcn_readlane(upto[k], 63);
+      for (int k = 0; k < kPieceWindows; ++k) {  // (sequences past the batch repeat its last and do not count)
+        const int s = s0 + 64 * k + lane;
+        held[k] = (int)kv_length(sh, sp.lengths[s < sp.batch ? s : sp.batch - 1], sp.width, sp.max_len);
       }
-    }
-  }
-  __device__ __forceinline__ static int pick(const int (&v)[kPieceWindows], int seq) {
-    int x = __builtin_amdgcn_readlane(v[0], seq & 63);
+    };
+    int64_t units = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < sp.batch; s0 += kPieceRun) {
+      read(s0);
 #pragma unroll
-    for (int k = 1; k < kPieceWindows; ++k) x = seq >> 6 == k ? __builtin_amdgcn_readlane(v[k], seq & 63) : x;
-    return x;
-  }
-  // The sequence of piece i (< total).
-  __device__ __forceinline__ int sequence(int i) const {
-    int seq = 0;
-#pragma unroll
-    for (int k = kPieceWindows - 1; k >= 0; --k) {
-      const uint64_t past = __ballot(upto[k] > i);
-      if (past) seq = 64 * k + __ffsll((unsigned long long)past) - 1;
+      for (int k = 0; k < kPieceWindows; ++k)
+        if (s0 + 64 * k < sp.batch)
+          units += __builtin_amdgcn_readlane(wave_scan(s0 + 64 * k + lane < sp.batch ? kv_units(held[k]) : 0), 63);
     }
-    return seq;
+    const int shift = kv_piece_shift(units, sp.heads, sp.most);
+    int total = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < sp.batch; s0 += kPieceRun) {
+      if (sp.batch > kPieceRun) read(s0);
+#pragma unroll
+      for (int k = 0; k < kPieceWindows; ++k)
+        if (s0 + 64 * k < sp.batch) {
+          const int upto = total + wave_scan(s0 + 64 * k + lane < sp.batch ? kv_pieces(kv_units(held[k]), shift) : 0);
+          total = __builtin_amdgcn_readlane(upto, 63);
+          const uint64_t past = __ballot(upto > slot);
+          if (past) {
+            const int at = __ffsll((unsigned long long)past) - 1;
+            seq = s0 + 64 * k + at;
+            len = __builtin_amdgcn_readlane(held[k], at);
+            pieces = kv_pieces(kv_units(len), shift);
+            first = __builtin_amdgcn_readlane(upto, at) - pieces;
+            return true;
+          }
+        }
+    }
+    return false;
   }
-  __device__ __forceinline__ int length(int seq) const { return pick(len, seq); }
-  __device__ __forceinline__ int end(int seq) const { return pick(upto, seq); }
 };
 
 template <int D, int BITS>
@@ -180,12 +184,11 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
   int pages, next = -1;
   if (sp.chunk == 0) {
     PieceSplit split;
-    split.read(sp, sh, lane);
     slot = (int)blockIdx.y;
-    if (slot >= split.total) return;
-    seq = split.sequence(slot);
-    const int len = split.length(seq), units = kv_units(len), pieces = kv_pieces(units, split.shift);
-    const int span = (units + pieces - 1) / pieces * kKvUnit, first = split.end(seq) - pieces;
+    if (!split.find(sp, sh, lane, slot)) return;
+    seq = split.seq;
+    const int len = split.len, pieces = split.pieces, first = split.first;
+    const int span = (kv_units(len) + pieces - 1) / pieces * kKvUnit;
     if (slot == first && blockIdx.x == 0 && tid == 0) {
       meta[2 * seq] = first;
       meta[2 * seq + 1] = pieces;
@@ -564,7 +567,7 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
 // up to kPieceBatch make it by the lengths on the device instead, which costs a block's
 // start up to 1 us and serves page tables made for longer sequences (bounds of 131072
 // tokens, by the bound / by the lengths: 8 sequences of 2000 44.5 / 15.4 us, 64 of 2000 to
-// 6000 161 / 68, 256 of 1000 212 / 63) and ragged batches (32 of up to 30000 127 / 110);
+// 6000 161 / 68, 256 of 1000 212 / 63, 300 of 700 180 / 64) and ragged batches (32 of up to 30000 127 / 110);
 // with tight bounds 64 of 4096 61.6 / 60.8, 16 of up to 2000 17.0 / 17.3, one of 30000
 // 18.9 / 20.1.
 static AttSplit att_split(int64_t B, int64_t Hkv, int ratio, int row_bytes, int64_t max_len) {
