@@ -166,7 +166,7 @@ __device__ __forceinline__ int stage_bytes(unsigned char* dst, const unsigned ch
 // below.)  The waves' tiles are summed through LDS in a fixed order.
 // One token through 2 of 8 experts of 11008 x 4096: 47 MB in 13 us (3.6 TB/s); 45
 // tokens x 6 over 64 3-bit experts of 2048 x 1408: 73 MB in 22 us (3.3 TB/s), the
-// vector ALU 25 % and the address units 50 % busy.
+// vector ALU 26 % and the address units 51 % busy.
 // PAIRS: a scaled x of few rows is two fp16 numbers, the second at x + lo (x / s
 // rounded to one adds an error of the size of y's own rounding, more where a few
 // channels of few rows make most of the sums).  The tile is then 8 rows, the second
