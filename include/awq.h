@@ -480,8 +480,8 @@ int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t
                      size_t workspace_bytes, void* stream);
 
 /* awq_gemm_grouped_kernel -- the kernel awq_gemm_grouped launches for these
- * sizes, as awq_gemm_kernel says it of the single product: a host-only dry run
- * (160 bytes always suffice). */
+ * sizes without s, as awq_gemm_kernel says it of the single product: a host-only
+ * dry run (160 bytes always suffice). */
 int awq_gemm_grouped_kernel(int64_t R, int32_t E, int64_t N, int64_t K, int32_t group, int32_t bits, char* out,
                             size_t out_bytes);
 

@@ -192,7 +192,7 @@ def test_attention_heads(H, r, D, bits):
     check_attention(3, [77, 1, 300], H, r, D, 16, bits, seed=H + r + D + bits)
 
 
-@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("page", [16, 32, 128, 1024])
 @pytest.mark.parametrize("lengths", [[0], [1], [15, 16, 17], [31, 32, 33, 0, 64], [127, 128, 129, 2], [0, 0],
                                      [1000, 3, 1025, 512], [-4, 5], [2049, 4100]])
 def test_attention_lengths(lengths, page):

@@ -121,8 +121,8 @@ int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t
   AWQ_REQUIRE(top_k >= 1, AWQ_ERROR_INVALID_VALUE, "top_k must be >= 1 (got %d)", top_k);
   AWQ_REQUIRE(x_rows >= 1 && x_rows <= AWQ_MAX_PAIRS && (rows || x_rows >= R), AWQ_ERROR_INVALID_VALUE,
               "x_rows=%lld outside [1, 2^24], or fewer than R without rows", (long long)x_rows);
-  AWQ_REQUIRE(awq::gemm_grouped_fits(R, E, N, K, bits, s != nullptr), AWQ_ERROR_INVALID_VALUE, "R=%lld rows of N=%lld exceed one launch",
-              (long long)R, (long long)N);
+  AWQ_REQUIRE(awq::gemm_grouped_fits(R, E, N, K, bits, s != nullptr), AWQ_ERROR_INVALID_VALUE,
+              "R=%lld rows of N=%lld exceed one launch", (long long)R, (long long)N);
   const size_t need = awq_gemm_grouped_workspace_bytes(R, K, s != nullptr);
   AWQ_REQUIRE(workspace || need == 0, AWQ_ERROR_INVALID_VALUE, "workspace must not be NULL (%zu bytes needed)", need);
   if (int st2 = check_aligned({{x, "x"}, {rows, "rows"}, {offsets, "offsets"}, {s, "s"}, {packed, "packed"},

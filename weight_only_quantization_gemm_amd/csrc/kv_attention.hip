@@ -47,7 +47,7 @@ constexpr int kAttWaves = 4;
 constexpr int kAttStep = 32;       // tokens a wave takes at a time
 constexpr int kAttHeads = 16;      // query heads of a block: columns of a product
 constexpr float kSlack = 8.f;      // a score may pass the running maximum by this (log2) before all is rescaled
-constexpr int kNonTemporal = 2;    // cache policy of the code loads: every line is used once (54 against 61 us on long sequences)
+constexpr int kNonTemporal = 2;    // cache policy of the code loads: every line is used once (54 us against 61)
 constexpr int kAttWindow = 1024;   // tokens whose pages a wave's lanes hold, 16 each
 
 // Channel of the cache row that product row n of tile c of the output stands for.
@@ -567,9 +567,9 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
 // up to kPieceBatch make it by the lengths on the device instead, which costs a block's
 // start up to 1 us and serves page tables made for longer sequences (bounds of 131072
 // tokens, by the bound / by the lengths: 8 sequences of 2000 44.5 / 15.4 us, 64 of 2000 to
-// 6000 161 / 68, 256 of 1000 212 / 63, 300 of 700 180 / 64) and ragged batches (32 of up to 30000 127 / 110);
-// with tight bounds 64 of 4096 61.6 / 60.8, 16 of up to 2000 17.0 / 17.3, one of 30000
-// 18.9 / 20.1.
+// 6000 161 / 68, 256 of 1000 212 / 63, 300 of 700 180 / 64) and ragged batches (32 of up to
+// 30000 127 / 113); with tight bounds 64 of 4096 61.6 / 61.5, 16 of up to 2000 17.0 / 17.0,
+// one of 30000 18.9 / 20.1.
 static AttSplit att_split(int64_t B, int64_t Hkv, int ratio, int row_bytes, int64_t max_len) {
   AttSplit sp{};
   sp.max_len = max_len;
