@@ -490,7 +490,7 @@ int awq_gemm_grouped_kernel(int64_t R, int32_t E, int64_t N, int64_t K, int32_t 
  * fp32 in order of j, rounded to fp16 once.  Pairs with pos outside [0, R)
  * (dropped ones) add nothing.
  *   y        device fp16 [R][N]
- *   out      device fp16 [T][N]
+ *   out      device fp16 [T][N], apart from y
  * Requires N % 8 == 0, 8 <= N <= 2^20, and T, top_k, R as above.
  */
 int awq_moe_combine(const void* y, int64_t R, const int32_t* pos, const float* weights, int64_t T, int32_t top_k,
@@ -556,7 +556,7 @@ int awq_kv_read(const void* k_codes, const void* k_params, const void* v_codes, 
  *               absent
  *   lengths     device int32 [B]; at most table_width * page and max_len are
  *               used.  A sequence with no tokens gets out = 0
- *   out         device fp16 [B][Hq][D]
+ *   out         device fp16 [B][Hq][D], apart from q
  *   max_len     host bound on the lengths (0: table_width * page), at most
  *               AWQ_MAX_KV_LENGTH.  Up to 1024 sequences the work is split by
  *               the lengths themselves, beyond by the bound

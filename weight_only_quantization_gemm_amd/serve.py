@@ -27,9 +27,12 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle,
 
 def _like(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, index: int) -> None:
     """_need, on the given device."""
-    if isinstance(t, torch.Tensor) and t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    _need(t, name, dtype, ndim)
+    if isinstance(t, torch.Tensor):
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+        if t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+            return
+    _need(t, name, dtype, ndim)  # says what is wrong
 
 
 def _run(index: int, fn, *args) -> None:
@@ -222,8 +225,9 @@ def _cache_args(cache: dict, head_dim: int, index: int):
     _like(kp, "k_params", torch.float16, 4, index)
     _like(vc, "v_codes", torch.int32, 4, index)
     _like(vp, "v_params", torch.float16, 4, index)
-    pages, heads, page, words = shape = kc.shape
-    if vc.shape != shape or kp.shape != (pages, heads, page, 2) or vp.shape != kp.shape:
+    shape, params = kc.shape, kp.shape
+    pages, heads, page, words = shape
+    if vc.shape != shape or vp.shape != params or params != (pages, heads, page, 2):
         raise ValueError("k_codes, k_params, v_codes and v_params are not of one cache")
     if words * 32 != head_dim * bits:
         raise ValueError(f"the cache's rows of {words} words do not hold {bits}-bit heads of {head_dim}")
