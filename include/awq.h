@@ -451,8 +451,9 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
  *   y[i][n] = sum_k xs_i[k] * w_hat_e[n][k],   offsets[e] <= i < offsets[e+1]
  * with xs_i = x[rows[i] / top_k] (rows as a plan's: the tokens are gathered by
  * the product itself) or x[i] (rows NULL), divided by s[e] when s is given:
- * rounded to fp16 as by awq_scale_input, or for few rows (R <= 2 E or 16, where
- * the kernel for few rows is chosen) kept to 22 bits as the sum of two fp16 numbers.
+ * kept to 22 bits as the sum of two fp16 numbers for few rows (R <= 5 E or 16, and at
+ * most 2048, where the kernel for few rows is chosen), else rounded to fp16 as by
+ * awq_scale_input.  An x / s beyond fp16's largest number is infinite either way.
  *   x        device fp16 [x_rows][K]
  *   rows     device int32 [R] or NULL; an entry that leads outside x reads
  *            some row of x instead

@@ -9,6 +9,7 @@
 // Arithmetic (as the decode kernels of the single product): code - zero exact
 // in fp16, fp32 sums per 128-channel group on the matrix cores, the group's
 // scale applied in fp32, one rounding of y to fp16.
+#include "awq.h"
 #include "awq_common.h"
 #include "awq_internal.h"
 #include "mfma_pipe.h"
@@ -641,12 +642,15 @@ static Kernel grouped_choice(int64_t R, int64_t E, int64_t N, int64_t K, int bit
   return R > E && RingShape<4, 4, 2>::bytes(8, (int)G) <= kGrpLds ? Kernel::ring4 : Kernel::ring2;
 }
 
-// Whether a scaled x is two fp16 numbers, in tiles of half as many rows: costs 2 % while experts
-// have a row or two (2 rows of 8 experts of 11008 x 4096 16.5 -> 16.8 us, 60 of 64 of 2048 x 1408
-// 16.8 -> 17.5, 16 of 8 40.3 -> 42.8) and 15 to 25 % at five and seven.  More rows are rounded as
-// awq_scale_input rounds them, an error that averages to that of y's own rounding.
+// Whether a scaled x is two fp16 numbers, in tiles of half as many rows.  One number's rounding is
+// as large an error as that of y (2.9e-4 of it in all, against 2.1e-4 with two).  Two cost, over the
+// shapes above, 2 % at one row an expert, 3 to 6 at two, 7 to 18 at four (45 tokens x 6 over 64 3-bit
+// experts of 2048 x 1408: 25.5 -> 28.7 us), 12 to 23 at five, 17 to 30 at seven, and the pipelined
+// kernel would make every product twice: up to five rows an expert x / s enters with 22 bits,
+// beyond rounded as awq_scale_input rounds it.  (Two numbers of more than 2048 rows have no room
+// in the workspace.)
 static bool paired(Kernel choice, int64_t R, int64_t E) {
-  return (choice == Kernel::ring2 || choice == Kernel::ring4) && (R <= 2 * E || R <= 16);
+  return (choice == Kernel::ring2 || choice == Kernel::ring4) && R <= 2 * AWQ_MAX_EXPERTS && (R <= 5 * E || R <= 16);
 }
 
 // Whether the chosen kernel's grid (2^32 threads at most) covers the batch.

@@ -128,8 +128,8 @@ def awq_gemm_grouped(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
     """Row i of the ragged batch times the matrix of its expert e (offsets[e] <= i < offsets[e+1]):
     y fp16 [R][N].  packed int32 [E][N][words], scales fp16 [E][N][G], zeros uint8 [E][N][ceil(G/2)].
     Row i reads x[rows[i] / top_k] (rows int32 [R], as a plan's), or x[i] without rows; with s
-    (fp32 [E][K]) it is divided by s[e] first, rounded to fp16 as awq_scale_input does
-    or, for few rows (R <= 2 E or 16), kept to 22 bits.  Rows from offsets[E] on
+    (fp32 [E][K]) it is divided by s[e] first: for few rows (R <= 5 E or 16, and at most 2048)
+    kept to 22 bits, else rounded to fp16 as awq_scale_input does.  Rows from offsets[E] on
     are left as they were (in a new `out`: unset)."""
     _need(x, "x", torch.float16, 2)
     index = x.get_device()
