@@ -3,14 +3,14 @@
 // For a sequence of n tokens, a query head's row q and the key-value head it
 // belongs to:  s_t = a q . k_t,  out = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m)
 // over t < n, with k_t = scale_t (code_t - zero_t) and v_t alike.  The codes are
-// never expanded to fp16 values.  An 8-bit whole number c in the low bits of a
-// half is the fp16 subnormal c 2^-24, which the matrix cores take, so unpacking is
-// a mask and a shift; a 4-bit one is brought to bits 4 .. 7 and is c 2^-20.  (The
-// products of subnormal operands are cut off below 2^-24 of what an operand without
-// leading zeros would make: 4-bit codes in bits 0 .. 3 lost 2^-18 of a product,
-// which the difference below made 4e-4 of the output of 54000 tokens; the two more
-// shifts a word cost 2 % of the time, 10 % at 64 channels.)  Scale and zero
-// point, one of each per token, stay outside the products; u = 2^20 or 2^24:
+// never expanded to fp16 values.  A whole number c below 2^10 in the bits of a half is
+// the fp16 subnormal c 2^-24, which the matrix cores take, so unpacking is a shift and
+// a mask.  (The products of a subnormal operand are cut off as if it had no leading
+// zeros, at 2^-24 of the largest of a sum: codes are therefore brought to the top, 4-bit
+// ones to bits 6 .. 9 and 8-bit ones to bits 2 .. 9.  Of long sequences, whose output is
+// a small difference, codes two bits lower made errors of up to 0.7 of the output's
+// rounding, with a mean; the shifts cost 1 to 2 % of the time.)  Scale and zero
+// point, one of each per token, stay outside the products; u = 2^18 or 2^22:
 //   q . k_t = scale_t (u q . [c_t] - zero_t sum(q)),
 //   sum_t p_t v_t = u sum_t (p_t scale_t) [c_t] - sum_t (p_t scale_t) zero_t.
 // Everything but the operands q (fp16 as given) and w_t = p_t scale_t is kept in
@@ -59,10 +59,10 @@ __host__ __device__ constexpr int att_channel(int n, int c) {
   return n * (D / 16) + c;
 }
 
-// Four words of halves whose bits 0 .. 15 are four 4-bit codes: code k of each times 16.
+// Four words of halves whose bits 0 .. 15 are four 4-bit codes: code k of each times 64.
 template <int k>
 __device__ __forceinline__ u32x4 nibbles(u32x4 x) {
-  return (k == 0 ? x << 4 : (k == 1 ? x : (k == 2 ? x >> 4 : x >> 8))) & 0x00F000F0u;
+  return (k == 0 ? x << 6 : (k == 1 ? x << 2 : (k == 2 ? x >> 2 : x >> 6))) & 0x03C003C0u;
 }
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
     float* __restrict__ part_ml, int32_t* __restrict__ meta) {
   using A = AttStage<D, BITS>;
   constexpr int TILES = D / 16, RB = A::RB;
-  constexpr float kUnit = BITS == 4 ? 1048576.f : 16777216.f;  // codes enter the products divided by this
+  constexpr float kUnit = BITS == 4 ? 262144.f : 4194304.f;  // codes enter the products divided by this
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -297,10 +297,10 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
         u32x4 a;
         if (BITS == 4) {
           const uint32_t x = w[t];
-          a = u32x4{(x << 4) & 0x00F000F0u, x & 0x00F000F0u, (x >> 4) & 0x00F000F0u, (x >> 8) & 0x00F000F0u};
+          a = u32x4{(x << 6) & 0x03C003C0u, (x << 2) & 0x03C003C0u, (x >> 2) & 0x03C003C0u, (x >> 6) & 0x03C003C0u};
         } else {
-          a = u32x4{w[2 * t] & 0x00FF00FFu, (w[2 * t] >> 8) & 0x00FF00FFu, w[2 * t + 1] & 0x00FF00FFu,
-                    (w[2 * t + 1] >> 8) & 0x00FF00FFu};
+          a = u32x4{(w[2 * t] << 2) & 0x03FC03FCu, (w[2 * t] >> 6) & 0x03FC03FCu, (w[2 * t + 1] << 2) & 0x03FC03FCu,
+                    (w[2 * t + 1] >> 6) & 0x03FC03FCu};
         }
         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), qf[t], acc, 0, 0, 0);
       }
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
         u32x4 a;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          a[j] = perm(v[2 * j + 1][c / 4], v[2 * j][c / 4], 0x0C040C00u + 0x00010001u * (c % 4));
+          a[j] = perm(v[2 * j + 1][c / 4], v[2 * j][c / 4], 0x0C040C00u + 0x00010001u * (c % 4)) << 2;
         mac(a, o[c]);
       }
     }
