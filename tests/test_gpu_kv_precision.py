@@ -57,3 +57,69 @@ def test_error_over_long_sequences_is_that_of_rounding_the_output(D, bits):
     note(f"rms error / rounding {np.sqrt((err ** 2).mean()) / rounding:.4f}, mean {err.mean() / rounding * np.sqrt(err.size):.2f} deviations")
     assert np.sqrt((err ** 2).mean()) <= 1.01 * rounding
     assert abs(err.mean()) <= 5 * rounding / np.sqrt(err.size)
+
+
+def large_scores(n, D, bits, r, q_size, key_scale, scale, seed, winner=None):
+    """One sequence of n tokens of equal keys (token `winner`'s scale twice theirs): output, and the
+    definition's with the tolerance of its weights, which are equal or 0 and 1."""
+    g = np.random.default_rng(seed)
+    c = random_cache(n // 16 + 1, 1, D, 16, bits, seed)
+    c["k_codes"].copy_(c["k_codes"][:1, :, :1].clone().expand_as(c["k_codes"]))
+    c["k_params"][..., 0] = key_scale
+    c["k_params"][..., 1] = 2 ** (bits - 1)
+    kc = unpack(host(c["k_codes"])[0, 0, 0], bits) - 2.0 ** (bits - 1)
+    q = np.minimum(np.abs(g.standard_normal((1, r, D))) * q_size + q_size / 4, 60000)
+    q = (q * np.where(kc > 0, 1, -1) * np.sign(scale)).astype(np.float16)  # scores above 0
+    if winner is not None:
+        c["k_params"][winner // 16, 0, winner % 16, 0] = 2 * key_scale
+    table = np.arange(n // 16 + 1, dtype=np.int32)[None]
+    h = host_cache(c)
+    s = scale * (q[0].astype(np.float64) @ kc) * key_scale
+    assert np.all(np.isfinite(s)) and s.min() > 100  # twice the score: e^100 times the weight
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(np.array([n], np.int32)), scale=scale)).astype(np.float64)[0]
+    at = np.arange(n) if winner is None else np.array([winner])
+    vc = unpack(h["v_codes"][at // 16, 0, at % 16], bits).astype(np.float64)
+    vp = h["v_params"][at // 16, 0, at % 16].astype(np.float64)
+    ref, mag = ((vc - vp[:, 1:]) * vp[:, :1]).mean(0), ((vc + vp[:, 1:]) * vp[:, :1]).mean(0)
+    return y, ref, 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + (64 + n // 128) * 2.0 ** -22 * mag, s
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("n,winner", [(1, None), (40, None), (40, 17), (700, None), (700, 699), (6000, None), (6000, 3001)])
+def test_large_scores_weigh_tokens_as_small_ones_do(n, winner, bits):
+    """Scores of 2^12 to 2^90: equal ones share the output, the largest one takes it, in one piece and
+    in several.  Large queries and keys at the default scale, and ordinary ones at large scales."""
+    D, r = 128, 3
+    for size, key, scale in ((4.0, 2.0, D ** -0.5), (300.0, 20.0, D ** -0.5), (20000.0, 3000.0, D ** -0.5),
+                             (20000.0, 8000.0, -1.0), (1.0, 0.1, 1e12), (1.0, 0.1, -2.0 ** 64), (20000.0, 8000.0, 2.0 ** 64),
+                             (0.01, 0.001, 2.0 ** 40)):
+        y, ref, tol, s = large_scores(n, D, bits, r, size, key, scale, 71, winner)
+        note(f"scores of 2^{np.log2(s.max()):.1f}")
+        assert np.all(np.abs(y - ref) <= tol), (size, key, scale, y[0, :4], ref[:4])
+
+
+def test_large_scores_in_pieces_of_ragged_sequences():
+    """A batch split by the lengths, scores of 2^40 and more: each sequence of equal keys gives its mean."""
+    g = np.random.default_rng(72)
+    lengths = np.array([5000, 0, 1, 129, 2600, 17], np.int32)
+    D, page = 64, 16
+    c = random_cache(700, 2, D, page, 4, 73)
+    c["k_codes"].copy_(c["k_codes"][:1, :, :1].clone().expand_as(c["k_codes"]))
+    c["k_params"][..., 0] = 4000.0
+    c["k_params"][..., 1] = 7
+    table = g.permutation(700)[:600].reshape(6, 100)
+    table = np.concatenate([table, g.integers(0, 700, size=(6, 400))], 1).astype(np.int32)
+    q = (g.standard_normal((6, 8, D)) * 8000).astype(np.float16)
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(lengths), scale=2.0 ** 10)).astype(np.float64)
+    h = host_cache(c)
+    for b, n in enumerate(lengths):
+        t = np.arange(n)
+        for k in range(2):
+            if n == 0:
+                assert np.all(y[b] == 0)
+                continue
+            vc = unpack(h["v_codes"][table[b, t // page], k, t % page], 4).astype(np.float64)
+            vp = h["v_params"][table[b, t // page], k, t % page].astype(np.float64)
+            ref, mag = ((vc - vp[:, 1:]) * vp[:, :1]).mean(0), ((vc + vp[:, 1:]) * vp[:, :1]).mean(0)
+            tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + (64 + n // 128) * 2.0 ** -22 * mag
+            assert np.all(np.abs(y[b, 4 * k:4 * k + 4] - ref) <= tol)

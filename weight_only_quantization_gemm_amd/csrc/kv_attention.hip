@@ -41,6 +41,8 @@
 #include "kv_common.h"
 #include "mfma_pipe.h"
 
+#include <cmath>
+
 namespace awq {
 
 constexpr int kAttWaves = 4;
@@ -49,6 +51,9 @@ constexpr int kAttHeads = 16;      // query heads of a block: columns of a produ
 constexpr float kSlack = 8.f;      // a score may pass the running maximum by this (log2) before all is rescaled
 constexpr int kNonTemporal = 2;    // cache policy of the code loads: every line is used once (54 us against 61)
 constexpr int kAttWindow = 1024;   // tokens whose pages a wave's lanes hold, 16 each
+
+// Codes enter the products divided by this.
+constexpr float att_unit(int bits) { return bits == 4 ? 262144.f : 4194304.f; }
 
 // Channel of the cache row that product row n of tile c of the output stands for.
 template <int D, int BITS>
@@ -155,11 +160,11 @@ struct PieceSplit {
 template <int D, int BITS>
 __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_attention_kernel(
     const f16* __restrict__ q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* __restrict__ table, AttSplit sp,
-    KvShape sh, int ratio, float scale_log2, f16* __restrict__ out, float* __restrict__ part_o,
+    KvShape sh, int ratio, float signed_factor, f16* __restrict__ out, float* __restrict__ part_o,
     float* __restrict__ part_ml, int32_t* __restrict__ meta) {
   using A = AttStage<D, BITS>;
   constexpr int TILES = D / 16, RB = A::RB;
-  constexpr float kUnit = BITS == 4 ? 262144.f : 4194304.f;  // codes enter the products divided by this
+  constexpr float kUnit = att_unit(BITS);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -238,9 +243,8 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
   if (turns > 0) issue(wave, 0, pages);
 
   // q: columns past the block's heads repeat the last one and are never stored.  A negative
-  // factor goes to q's sign, so that larger sums are larger scores; one of 0 is taken as
-  // 2^-100, which leaves a masked score (-infinity) what it is.
-  const float factor = fmaxf(fabsf(scale_log2) * kUnit, 7.888609e-31f);
+  // factor goes to q's sign, so that larger sums are larger scores.
+  const float factor = fabsf(signed_factor);
   const int hn = n < heads ? n : heads - 1;
   const f16* qrow = q + seq * q_stride + (int64_t)(hk * ratio + h0 + hn) * D;
   f16x8 qf[D / 32];
@@ -248,7 +252,7 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
 #pragma unroll
   for (int s = 0; s < D / 32; ++s) {
     f16x8 x = *reinterpret_cast<const f16x8*>(qrow + b * (D / 4) + 8 * s);
-    if (scale_log2 < 0.f) x = -x;
+    if (signed_factor < 0.f) x = -x;
 #pragma unroll
     for (int j = 0; j < 8; ++j) qz += (float)x[j];
     if (BITS == 4) qf[s] = x;
@@ -258,14 +262,17 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
   qz += __shfl_xor(qz, 32, kWave);
   qz *= -1.f / kUnit;
 
-  // Weights are kept as 2^(factor x - ref), ref following the largest score less
-  // the exponent F that brings the largest value scale to 2^6 .. 2^7: a weight
-  // times a value scale then uses fp16's range from the top.
+  // Weights are kept as 2^(factor (s - top) + F), top following the largest sum and F
+  // the exponent that brings the largest value scale to 2^6 .. 2^7: a weight times a value
+  // scale then uses fp16's range from the top.  Sums are subtracted before they are multiplied:
+  // the difference is exact near the top, so the weight of the top itself is 2^F whatever the
+  // size of the scores (factor s - (factor top - F) would be off by half a unit of factor top,
+  // in the exponent).
   f32x4 o[TILES], oz = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < TILES; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float ref = 0.f, l = 0.f;
-  float top_seen = -INFINITY, limit = -INFINITY;  // largest sum seen; the one past which ref has to move
+  float l = 0.f;
+  float top_seen = -INFINITY, base = 0.f;         // the top, and what is subtracted (0 while there is none)
   float wide_limit = 0.f;                         // largest value scale that F allows for
   int F = 0;
 
@@ -331,23 +338,23 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
     }
     float wide = (float)__builtin_bit_cast(f16, widest.x);
     // rarely: a new maximum or a larger value scale; every lane then rescales what it holds
-    if (__ballot(top > limit || wide > wide_limit)) {
+    if (__ballot((top - top_seen) * factor > kSlack || wide > wide_limit)) {
       top = fmaxf(top, __shfl_xor(top, 16, kWave));
       top = fmaxf(top, __shfl_xor(top, 32, kWave));
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) wide = fmaxf(wide, __shfl_xor(wide, off, kWave));
-      const bool first = top_seen == -INFINITY;
+      const float was = top_seen;
+      int more = -F;  // by how much F changes
       top_seen = fmaxf(top_seen, top);
-      limit = top_seen == -INFINITY ? -INFINITY : top_seen + kSlack / factor;
+      base = top_seen == -INFINITY ? 0.f : top_seen;
       if (wide > wide_limit) {
         int e;
         frexpf(wide, &e);  // wide in [2^(e - 1), 2^e)
         F = 7 - e;
         wide_limit = ldexpf(1.f, e);
       }
-      const float now = top_seen == -INFINITY ? 0.f : fmaf(top_seen, factor, -(float)F);
-      const float alpha = first ? 0.f : exp2f(ref - now);
-      ref = now;
+      more += F;
+      const float alpha = was == -INFINITY ? 0.f : exp2f(fmaf(was - base, factor, (float)more));
       l *= alpha;
 #pragma unroll
       for (int c = 0; c < TILES; ++c)
@@ -359,7 +366,7 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
     f16x8 whi, wlo;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(s[j], factor, -ref));
+      const float p = __builtin_amdgcn_exp2f(fmaf(s[j] - base, factor, (float)F));
       l += p;
       const float w = fmaf(p, (float)as_f16x2(vp[j]).x, 0.f);
       whi[j] = (f16)w;
@@ -444,16 +451,18 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
   __syncthreads();  // the rings become the place of the sum
 
   // Join the waves: each output in LDS [wave][head][D], then its share of the sum,
-  // 2^(ref - largest ref), and the sums in the order of the waves.
+  // 2^(factor (top - largest top) - F), and the sums in the order of the waves.
   l += __shfl_xor(l, 16, kWave);
   l += __shfl_xor(l, 32, kWave);
   float* red_o = reinterpret_cast<float*>(smem);
   float* red_m = red_o + kAttWaves * heads * D;  // [wave][16]
   float* red_l = red_m + kAttWaves * kAttHeads;
-  float* share = red_l + kAttWaves * kAttHeads;  // [wave][16], then the head's sum [16]
+  float* red_f = red_l + kAttWaves * kAttHeads;
+  float* share = red_f + kAttWaves * kAttHeads;  // [wave][16], then the head's sum [16]
   if (b == 0) {
-    red_m[wave * kAttHeads + n] = top_seen == -INFINITY ? -INFINITY : ref;
+    red_m[wave * kAttHeads + n] = top_seen;
     red_l[wave * kAttHeads + n] = l;
+    red_f[wave * kAttHeads + n] = (float)F;
   }
   if (n < heads) {
 #pragma unroll
@@ -472,11 +481,11 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
 #pragma unroll
     for (int w = 0; w < kAttWaves; ++w) {
       const float mw = red_m[w * kAttHeads + n];
-      const float f = mw == -INFINITY ? 0.f : exp2f(mw - mx);
+      const float f = mw == -INFINITY ? 0.f : exp2f(fmaf(mw - mx, factor, -red_f[w * kAttHeads + n]));
       share[w * kAttHeads + n] = f;
       sum = fmaf(f, red_l[w * kAttHeads + n], sum);
     }
-    share[kAttWaves * kAttHeads + n] = sum == 0.f ? 0.f : 1.f / sum;
+    share[kAttWaves * kAttHeads + n] = sum == 0.f ? 0.f : 1.f / sum;  // (the top's own weight is 1: 0 is no token)
     if (!whole && n < heads) {
       const int64_t at = (int64_t)slot * Hq + hk * ratio + h0 + n;
       part_ml[2 * at] = mx;
@@ -509,7 +518,7 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
 __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__ part_o,
                                                        const float* __restrict__ part_ml,
                                                        const int32_t* __restrict__ meta, AttSplit sp, KvShape sh,
-                                                       int Hq, f16* __restrict__ out) {
+                                                       int Hq, float factor, f16* __restrict__ out) {
   __shared__ float red[2 * 1024], top[16];
   const int64_t head = blockIdx.x;
   const int D = (int)blockDim.x, d = (int)threadIdx.x, part = (int)threadIdx.y, parts = (int)blockDim.y;
@@ -538,7 +547,7 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
 #pragma unroll 4
   for (int c = part; c < used; c += parts) {
     const float m = ml[(int64_t)c * Hq * 2];
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
+    const float f = m == -INFINITY ? 0.f : exp2f((m - mx) * factor);
     sum = fmaf(f, ml[(int64_t)c * Hq * 2 + 1], sum);
     acc = fmaf(f, po[(int64_t)c * Hq * D], acc);
   }
@@ -609,21 +618,23 @@ static hipError_t attention_launch(const void* q, int64_t q_stride, KvHalf kc, K
   sp.lengths = lengths;
   sp.width = (int)width;
   const int heads = ratio < kAttHeads ? ratio : kAttHeads;
-  const size_t sum = (size_t)(kAttWaves * heads * D + (3 * kAttWaves + 1) * kAttHeads) * sizeof(float);
+  const size_t sum = (size_t)(kAttWaves * heads * D + (4 * kAttWaves + 1) * kAttHeads) * sizeof(float);
   const size_t ring = (size_t)kAttWaves * (AttStage<D, BITS>::RING + 64 * sizeof(int)), lds = ring > sum ? ring : sum;
   const dim3 grid((unsigned)sp.heads, (unsigned)sp.chunks, sp.chunk ? (unsigned)B : 1u);
   const int64_t slots = att_slots(sp), Hq = (int64_t)sh.heads * ratio;
   float* part_ml = ws == nullptr ? nullptr : ws + slots * Hq * D;
   int32_t* meta = ws == nullptr ? nullptr : reinterpret_cast<int32_t*>(part_ml + slots * Hq * 2);
+  // A scale of 0 is taken as one that leaves a masked score (-infinity) what it is.
+  const float factor = std::fmax(std::fabs(scale) * 1.4426950408889634f * att_unit(BITS), 7.888609e-31f);
   kv_attention_kernel<D, BITS><<<grid, dim3(64 * kAttWaves), lds, st>>>(
-      reinterpret_cast<const f16*>(q), q_stride, kc, vc, table, sp, sh, ratio, scale * 1.4426950408889634f,
+      reinterpret_cast<const f16*>(q), q_stride, kc, vc, table, sp, sh, ratio, std::copysign(factor, scale),
       reinterpret_cast<f16*>(out), ws, part_ml, meta);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || slots == 0) return e;
   const int64_t pieces = sp.chunk ? sp.chunks : (sp.most / sp.heads + B) / B;
   int parts = 1;  // about eight pieces a part
   while (parts * D < 1024 && 8 * parts < pieces) parts *= 2;
-  kv_join_kernel<<<dim3((unsigned)(B * Hq)), dim3(D, parts), 0, st>>>(ws, part_ml, meta, sp, sh, (int)Hq,
+  kv_join_kernel<<<dim3((unsigned)(B * Hq)), dim3(D, parts), 0, st>>>(ws, part_ml, meta, sp, sh, (int)Hq, factor,
                                                                      reinterpret_cast<f16*>(out));
   return hipGetLastError();
 }
