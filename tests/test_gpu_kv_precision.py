@@ -123,3 +123,108 @@ def test_large_scores_in_pieces_of_ragged_sequences():
             ref, mag = ((vc - vp[:, 1:]) * vp[:, :1]).mean(0), ((vc + vp[:, 1:]) * vp[:, :1]).mean(0)
             tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + (64 + n // 128) * 2.0 ** -22 * mag
             assert np.all(np.abs(y[b, 4 * k:4 * k + 4] - ref) <= tol)
+
+
+def one_channel_scores(steps, scale_of_values, D, bits, seed):
+    """One sequence whose scores are known: q is 1 in channel 0, a key's code there `steps` (a token's,
+    whole) from its zero point, its scale 2^-4, the attention's scale 1: score steps / 16, exactly.
+    Values: random codes, the given scales.  Returns the output, the definition's weights, values and
+    the values' magnitudes (code + zero) scale."""
+    n = len(steps)
+    c = random_cache(-(-n // 16), 1, D, 16, bits, seed)
+    kw = np.full((c["k_codes"].shape[0] * 16, D), 2 ** (bits - 1))
+    kw[:n, 0] += steps
+    assert kw.min() >= 0 and kw.max() < 2 ** bits
+    c["k_codes"].copy_(dev(pack(kw, bits).reshape(c["k_codes"].shape)))
+    c["k_params"][..., 0] = 2.0 ** -4
+    c["k_params"][..., 1] = 2 ** (bits - 1)
+    vs = np.ones(kw.shape[0])
+    vs[:n] = scale_of_values
+    c["v_params"][..., 0] = dev(vs.reshape(-1, 1, 16).astype(np.float16))
+    q = np.zeros((1, 1, D), np.float16)
+    q[0, 0, 0] = 1
+    table = np.arange(kw.shape[0] // 16, dtype=np.int32)[None]
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(np.array([n], np.int32)), scale=1.0)).astype(np.float64)[0, 0]
+    h, t = host_cache(c), np.arange(n)
+    vc = unpack(h["v_codes"][t // 16, 0, t % 16], bits).astype(np.float64)
+    vp = h["v_params"][t // 16, 0, t % 16].astype(np.float64)
+    p = np.exp(np.asarray(steps) / 16.0)
+    return y, p / p.sum(), (vc - vp[:, 1:]) * vp[:, :1], (vc + vp[:, 1:]) * vp[:, :1]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [2, 3, 17, 300])
+def test_weights_enter_with_22_bits(n, D, bits):
+    """Scores are exact here, so that the weights show: exp2's argument rounds twice (2^-23 of at most
+    0.7: 2^-23 of the weight), exp2 and the value scale's product once each, two fp16 numbers leave
+    2^-22: 2^-20.9 in all; sums of at most 10 steps, waves and products in fp32, 2^-19.5 of the
+    magnitudes.  Weights of one fp16 number (2^-12) are seen, where there are enough for their
+    roundings not to be small by chance: the bound refuses them."""
+    g = np.random.default_rng(n + D + bits)
+    steps = g.integers(-8, 8, size=n) if bits == 4 else g.integers(-11, 12, size=n)
+    vs = np.exp(0.5 * g.standard_normal(n)).astype(np.float16)
+    y, p, v, mag = one_channel_scores(steps, vs, D, bits, 81 + n)
+    ref = p @ v
+    tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2.0 ** -19 * (p @ mag)
+    assert bool(np.all(np.abs(y - ref) <= tol))
+    w = p * vs.astype(np.float64)
+    once = (w / w.max() * 100).astype(np.float16).astype(np.float64) * w.max() / 100 / vs.astype(np.float64)
+    assert n < 17 or bool(np.any(np.abs(once @ v - ref) > tol))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("n,wide", [(40, 0), (40, 39), (300, 150), (700, 3), (4000, 0), (4000, 3999)])
+def test_a_large_value_of_no_weight_leaves_the_others_their_bits(n, wide, bits):
+    """One token's value scale is the largest that is written (of a row from -65504 to 65504), all
+    others' the smallest, and its weight e^-60: the others' weights keep their 22 bits."""
+    D = 64
+    g = np.random.default_rng(n + wide + bits)
+    steps = g.integers(-8, 8, size=n) if bits == 4 else g.integers(-64, 0, size=n)
+    vs = np.full(n, 2.0 ** -14, np.float16)
+    vs[wide] = np.float16(131008 / (2 ** bits - 1))
+    # the scores' range is 0.5 .. 4 here; the wide token's is pushed down by its key's own scale
+    c = random_cache(-(-n // 16), 1, D, 16, bits, 91)
+    kw = np.full((c["k_codes"].shape[0] * 16, D), 2 ** (bits - 1))
+    kw[:n, 0] += steps
+    kw[wide, 0] = 0
+    c["k_codes"].copy_(dev(pack(kw, bits).reshape(c["k_codes"].shape)))
+    ks = np.full(kw.shape[0], 2.0 ** -4)
+    ks[wide] = 64 / 2.0 ** (bits - 1)
+    c["k_params"][..., 0] = dev(ks.reshape(-1, 1, 16).astype(np.float16))
+    c["k_params"][..., 1] = 2 ** (bits - 1)
+    full = np.ones(kw.shape[0])
+    full[:n] = vs
+    c["v_params"][..., 0] = dev(full.reshape(-1, 1, 16).astype(np.float16))
+    q = np.zeros((1, 1, D), np.float16)
+    q[0, 0, 0] = 1
+    table = np.arange(kw.shape[0] // 16, dtype=np.int32)[None]
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(np.array([n], np.int32)), scale=1.0)).astype(np.float64)[0, 0]
+    h, t = host_cache(c), np.arange(n)
+    vc = unpack(h["v_codes"][t // 16, 0, t % 16], bits).astype(np.float64)
+    vp = h["v_params"][t // 16, 0, t % 16].astype(np.float64)
+    s = np.where(t == wide, -64.0, steps / 16.0)
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    ref, mag = p @ ((vc - vp[:, 1:]) * vp[:, :1]), p @ ((vc + vp[:, 1:]) * vp[:, :1])
+    assert p[wide] * 131008 < 1e-4 * mag.min()
+    # exp2's argument of up to 2^2.6 rounds by 2^-21; sums of up to 64 steps, waves and pieces
+    assert bool(np.all(np.abs(y - ref) <= 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2.0 ** -18 * mag))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_value_scales_that_grow_and_fall_along_a_sequence(bits):
+    """Value scales over the whole range that is written, in random order and in runs, with weights
+    that rise and fall: the exponent that the weights share moves up and down."""
+    D, n = 64, 3000
+    g = np.random.default_rng(95)
+    top = np.log2(131008 / (2 ** bits - 1))
+    for vs in (np.exp2(g.uniform(-14, top, n)), np.exp2(-14 + (top + 14) * np.abs(np.sin(np.arange(n) / 200.0))),
+               np.exp2(np.where(np.arange(n) % 64 < 32, -14, top)), np.exp2(np.linspace(top, -14, n))):
+        steps = g.integers(-8, 8, size=n) if bits == 4 else (110 * np.sin(np.arange(n) / 317.0)).astype(int)
+        y, p, v, mag = one_channel_scores(steps, vs.astype(np.float16), D, bits, 96)
+        ref = p @ v
+        # exp2's argument of up to 2^4.4 rounds by 2^-19.6
+        tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2.0 ** -17.5 * (p @ mag)
+        near = (np.abs(y - ref) <= tol) | ((y == np.copysign(np.inf, ref)) & (np.abs(ref) + tol >= 65520))
+        assert near.all()

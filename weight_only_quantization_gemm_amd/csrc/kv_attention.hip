@@ -70,9 +70,6 @@ __device__ __forceinline__ u32x4 nibbles(u32x4 x) {
   return (k == 0 ? x << 6 : (k == 1 ? x << 2 : (k == 2 ? x >> 2 : x >> 6))) & 0x03C003C0u;
 }
 
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-__device__ inline u16x2 as_u16x2(uint32_t v) { return __builtin_bit_cast(u16x2, v); }
-
 __device__ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); }
 
 // A stage of a wave's ring: 32 tokens' keys, values and parameters, moved
@@ -262,9 +259,11 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
   qz += __shfl_xor(qz, 32, kWave);
   qz *= -1.f / kUnit;
 
-  // Weights are kept as 2^(factor (s - top) + F), top following the largest sum and F
-  // the exponent that brings the largest value scale to 2^6 .. 2^7: a weight times a value
-  // scale then uses fp16's range from the top.  Sums are subtracted before they are multiplied:
+  // Weights are kept as 2^(factor (s - top) + F), top following the largest sum and F the
+  // exponent that brings the largest weight times its value scale to 2^6 .. 2^7 (and on to 2^15
+  // before all is rescaled): of any other, two fp16 numbers then leave at most 2^-31 of that one.
+  // (Not the largest value scale alone: one of a token of no weight would push all others off
+  // fp16's lower end.)  Sums are subtracted before they are multiplied:
   // the difference is exact near the top, so the weight of the top itself is 2^F whatever the
   // size of the scores (factor s - (factor top - F) would be off by half a unit of factor top,
   // in the exponent).
@@ -273,8 +272,7 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
   for (int c = 0; c < TILES; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
   float l = 0.f;
   float top_seen = -INFINITY, base = 0.f;         // the top, and what is subtracted (0 while there is none)
-  float wide_limit = 0.f;                         // largest value scale that F allows for
-  int F = 0;
+  float F = 0.f, most = 0.f;                      // most: the largest weight times value scale when last rescaled
 
   auto compute = [&](int i, const unsigned char* st) {
     float s[8];
@@ -328,33 +326,42 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
         vp[j] = live ? vp[j] : 0u;
       }
     }
-    // the largest score and the largest value scale (positive: ordered as its bits are)
     float top = s[0];
-    u16x2 widest = as_u16x2(vp[0]);
 #pragma unroll
-    for (int j = 1; j < 8; ++j) {
-      top = fmaxf(top, s[j]);
-      widest = __builtin_elementwise_max(widest, as_u16x2(vp[j]));
-    }
-    float wide = (float)__builtin_bit_cast(f16, widest.x);
-    // rarely: a new maximum or a larger value scale; every lane then rescales what it holds
-    if (__ballot((top - top_seen) * factor > kSlack || wide > wide_limit)) {
+    for (int j = 1; j < 8; ++j) top = fmaxf(top, s[j]);
+    // rarely: a new maximum
+    const bool moved = __ballot((top - top_seen) * factor > kSlack) != 0;
+    float alpha = 1.f;
+    if (moved) {
       top = fmaxf(top, __shfl_xor(top, 16, kWave));
       top = fmaxf(top, __shfl_xor(top, 32, kWave));
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) wide = fmaxf(wide, __shfl_xor(wide, off, kWave));
       const float was = top_seen;
-      int more = -F;  // by how much F changes
       top_seen = fmaxf(top_seen, top);
       base = top_seen == -INFINITY ? 0.f : top_seen;
-      if (wide > wide_limit) {
-        int e;
-        frexpf(wide, &e);  // wide in [2^(e - 1), 2^e)
-        F = 7 - e;
-        wide_limit = ldexpf(1.f, e);
-      }
-      more += F;
-      const float alpha = was == -INFINITY ? 0.f : exp2f(fmaf(was - base, factor, (float)more));
+      alpha = was == -INFINITY ? 0.f : exp2f((was - base) * factor);
+    }
+    float w[8], sum = 0.f, big = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float p = __builtin_amdgcn_exp2f(fmaf(s[j] - base, factor, F));
+      sum += p;
+      w[j] = fmaf(p, (float)as_f16x2(vp[j]).x, 0.f);
+      big = fmaxf(big, w[j]);
+    }
+    // then, or where a weight times its value scale grows too large: what a lane holds is rescaled
+    if (moved || __ballot(big > 32768.f)) {
+      big = fmaxf(big, __shfl_xor(big, 16, kWave));
+      big = fmaxf(big, __shfl_xor(big, 32, kWave));
+      most = fmaxf(most * alpha, big);
+      int e;
+      frexpf(most, &e);  // most in [2^(e - 1), 2^e)
+      const float now = most > 0.f ? fminf(fmaxf(F + (float)(7 - e), -40.f), 40.f) : F, by = exp2f(now - F);
+      F = now;
+      most *= by;
+      sum *= by;
+      alpha *= by;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] *= by;
       l *= alpha;
 #pragma unroll
       for (int c = 0; c < TILES; ++c)
@@ -363,14 +370,12 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
 #pragma unroll
       for (int r = 0; r < 4; ++r) oz[r] *= alpha;
     }
+    l += sum;
     f16x8 whi, wlo;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(s[j] - base, factor, (float)F));
-      l += p;
-      const float w = fmaf(p, (float)as_f16x2(vp[j]).x, 0.f);
-      whi[j] = (f16)w;
-      wlo[j] = (f16)fmaf((float)whi[j], -1.f, w);
+      whi[j] = (f16)w[j];
+      wlo[j] = (f16)fmaf((float)whi[j], -1.f, w[j]);
     }
     auto mac = [&](u32x4 a, f32x4& acc) {
       const f16x8 af = __builtin_bit_cast(f16x8, a);
