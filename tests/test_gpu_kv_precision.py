@@ -228,3 +228,24 @@ def test_value_scales_that_grow_and_fall_along_a_sequence(bits):
         tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2.0 ** -17.5 * (p @ mag)
         near = (np.abs(y - ref) <= tol) | ((y == np.copysign(np.inf, ref)) & (np.abs(ref) + tol >= 65520))
         assert near.all()
+
+
+def test_many_heads_of_sequences_of_several_pieces():
+    """64 heads, a few sequences of 20000 tokens among short and empty ones: pieces of more than one
+    window of pages, joined for every head (three heads are checked)."""
+    H, D, page, heads = 64, 64, 16, [0, 31, 63]
+    g = np.random.default_rng(97)
+    lengths = g.integers(0, 300, size=12).astype(np.int32)
+    lengths[[0, 5, 11]] = [20000, 19999, 18433]
+    lengths[3] = 0
+    table = g.integers(0, 1500, size=(12, 1250)).astype(np.int32)  # pages shared between sequences
+    c = random_cache(1500, H, D, page, 4, 98)
+    q = g.standard_normal((12, H, D)).astype(np.float16)
+    y = host(awq.awq_kv_attention(dev(q), c, dev(table), dev(lengths)))
+    # units of 128 tokens of 64 heads, 1536 pieces of which fill the chip: pieces of 32 units, four windows
+    units = int(np.maximum(1, -(-lengths // 128)).sum())
+    assert 16 * 1536 < units * H <= 32 * 1536 and lengths[0] > 4 * 32 * 128
+    sub = {k: v[:, heads] for k, v in host_cache(c).items()}
+    ref, tol = attend_ref(q[:, heads], sub, table, lengths, D ** -0.5, 4, 160)
+    assert bool(np.all(np.abs(y[:, heads] - ref) <= tol))
+    assert np.all(y[3] == 0)
