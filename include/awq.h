@@ -470,9 +470,11 @@ int awq_moe_route(const void* logits, int32_t logit_bytes, int64_t T, int32_t E,
  * the groups stay on the device; the result does not depend on timing.
  * Requires R, x_rows in [1, 2^24] (x_rows >= R without rows), E in
  * [1, AWQ_MAX_EXPERTS], bits 4 or 3, group == AWQ_GROUP, K % group == 0,
- * K <= 2^17, and a batch one launch covers (at 256 rows of an expert or more on
- * average R * N < 2^39; a scaled batch R < 2^24).  x, y and the workspace do not
- * overlap.
+ * K <= 2^17, and a batch one launch covers: with N rounded up to whole tiles,
+ * N * (R + (BM - 1) * min(E, R)) < 2^39 in tiles of BM = 256 rows, 2^38 of 64, 2^33 of
+ * 16 (ring kernel of 64 columns) or 2^32 (of 32), of which awq_gemm_grouped_kernel
+ * names the kernel or refuses the batch (x / s as two numbers: tiles of 8 rows, 2^32 and
+ * 2^31); a scaled batch R < 2^24.  x, y and the workspace do not overlap.
  */
 size_t awq_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int32_t scaled);
 int awq_gemm_grouped(const void* x, int64_t x_rows, const int32_t* rows, int32_t top_k, const int32_t* offsets,
