@@ -37,8 +37,9 @@
  * AWQ_ERROR_DEVICE) nothing was launched and no output was touched.
  * awq_last_error() returns a thread-local message describing the last failure
  * of the calling thread.  No call aborts or throws across this interface.
- * Non-finite values in W, X or x are outside the contract: they do not crash
- * the library, but the outputs are then unspecified.
+ * Non-finite values in W, X or x, and in the s, y, weights, k, v, q and cache
+ * parameters that an output depends on, are outside the contract: they do not
+ * crash the library, but the outputs are then unspecified.
  *
  * Thread safety.  Calls are reentrant; calls on different streams may overlap
  * when they do not share output or workspace buffers.

@@ -249,3 +249,10 @@ def test_many_heads_of_sequences_of_several_pieces():
     ref, tol = attend_ref(q[:, heads], sub, table, lengths, D ** -0.5, 4, 160)
     assert bool(np.all(np.abs(y[:, heads] - ref) <= tol))
     assert np.all(y[3] == 0)
+
+
+def test_a_cache_without_heads_is_refused():
+    c = awq.empty_kv_cache(2, 0, 64, device=DEV)
+    i = torch.zeros(1, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="heads"):
+        awq.awq_kv_attention(torch.zeros(1, 2, 64, dtype=torch.float16, device=DEV), c, i[:, None].contiguous(), i)

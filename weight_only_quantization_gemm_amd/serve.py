@@ -86,7 +86,8 @@ def _plan_workspace(T: int, E: int, top_k: int) -> int:
 
 def awq_moe_plan(experts: torch.Tensor, num_experts: int) -> dict:
     """The plan of given choices (int32 [T][top_k]; an id outside [0, num_experts) drops the
-    pair): offsets [E+1], rows and pos [T*top_k] as awq_gemm_grouped and awq_moe_combine take."""
+    pair): offsets [E+1], rows and pos [T*top_k] as awq_gemm_grouped and awq_moe_combine take.  They
+    share one allocation, which any of them keeps alive whole (as do awq_moe_route's results)."""
     _need(experts, "experts", torch.int32, 2)
     T, top_k = experts.shape
     need = _plan_workspace(T, num_experts, top_k)
@@ -298,7 +299,7 @@ def awq_kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, len
     arrays, pages, Hkv, page, bits = _cache_args(cache, D, index)
     if page_table.shape[0] != B or lengths.shape[0] != B:
         raise ValueError("page_table must be int32 [B][width] and lengths int32 [B]")
-    if Hq % Hkv:
+    if Hkv < 1 or Hq % Hkv:
         raise ValueError(f"q's {Hq} heads are not a multiple of the cache's {Hkv}")
     if max_len < 0:
         raise ValueError(f"max_len must be >= 0, got {max_len}")
