@@ -355,7 +355,8 @@ __global__ __launch_bounds__(64 * kAttWaves, D * BITS <= 512 ? 4 : 1) void kv_at
       most = fmaxf(most * alpha, big);
       int e;
       frexpf(most, &e);  // most in [2^(e - 1), 2^e)
-      const float now = most > 0.f ? fminf(fmaxf(F + (float)(7 - e), -40.f), 40.f) : F, by = exp2f(now - F);
+      const float now = most > 0.f ? fminf(fmaxf(F + (float)(7 - e), -40.f), 40.f) : F;
+      const float by = ldexpf(1.f, (int)(now - F));  // exact
       F = now;
       most *= by;
       sum *= by;
