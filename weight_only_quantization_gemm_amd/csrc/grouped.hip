@@ -166,8 +166,8 @@ __device__ __forceinline__ int stage_bytes(unsigned char* dst, const unsigned ch
 // per instruction, which alone takes longer than the memory: 20 us against 13
 // below.)  The waves' tiles are summed through LDS in a fixed order.
 // One token through 2 of 8 experts of 11008 x 4096: 47 MB in 13 us (3.6 TB/s); 45
-// tokens x 6 over 64 3-bit experts of 2048 x 1408: 73 MB in 22 us (3.3 TB/s), the
-// vector ALU 26 % and the address units 51 % busy.
+// tokens x 6 over 64 3-bit experts of 2048 x 1408: 73 MB in 22 us (3.3 TB/s), 24 with a
+// scaled x (PAIRS below), the vector ALU 28 % and the address units 57 % busy: latency.
 // PAIRS: a scaled x of few rows is two fp16 numbers, the second at x + lo (x / s
 // rounded to one adds an error of the size of y's own rounding, more where a few
 // channels of few rows make most of the sums).  The tile is then 8 rows, the second
@@ -644,8 +644,8 @@ static Kernel grouped_choice(int64_t R, int64_t E, int64_t N, int64_t K, int bit
 
 // Whether a scaled x is two fp16 numbers, in tiles of half as many rows.  One number's rounding is
 // as large an error as that of y (2.9e-4 of it in all, against 2.1e-4 with two).  Two cost, over the
-// shapes above, 2 % at one row an expert, 3 to 6 at two, 7 to 18 at four (45 tokens x 6 over 64 3-bit
-// experts of 2048 x 1408: 25.5 -> 28.7 us), 12 to 23 at five, 17 to 30 at seven, and the pipelined
+// shapes above, 3 to 5 % at one row an expert, 4 to 6 at two, 7 to 19 at four (45 tokens x 6 over 64
+// 3-bit experts of 2048 x 1408: 25.5 -> 28.6 us), 12 to 23 at five, 18 to 37 at seven, and the pipelined
 // kernel would make every product twice: up to five rows an expert x / s enters with 22 bits,
 // beyond rounded as awq_scale_input rounds it.  (Two numbers of more than 2048 rows have no room
 // in the workspace.)

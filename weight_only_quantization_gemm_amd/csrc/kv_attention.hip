@@ -24,10 +24,10 @@
 // depend on timing.
 //
 // Bound by reading the cache: 64 sequences of 4096 tokens x 8 heads of 128 at 4
-// bits, 287 MB in 61 us (4.7 TB/s); 32 of 2000 to 6000 at 8 bits, 269 MB in 62 us;
-// 64 ragged ones of 2000 to 6000 tokens at 4 bits 279 MB in 68 us, the last blocks
+// bits, 285 MB in 62 us (4.6 TB/s); 32 of 2000 to 6000 at 8 bits, 269 MB in 64 us;
+// 64 ragged ones of 2000 to 6000 tokens at 4 bits 279 MB in 69 us, the last blocks
 // leaving units idle; one of 2000 tokens 10 us, launches and latency.  The vector
-// ALU is busy about half of the time.
+// ALU is busy 55 % of the time.
 //
 // Lanes.  With l = 16 b + n, the products are 16 x 16 x 32:
 //   scores  A = codes of 16 tokens (row n: token; lane's channels D/4 b ..),
@@ -573,18 +573,19 @@ __global__ __launch_bounds__(1024) void kv_join_kernel(const float* __restrict__
 // chunks grow to 512 tokens while there are more than 512 blocks, and on to 4096 while
 // there are more than about one and a half times what the compute units hold at once (by
 // the rows' bytes, which size the ring; one at 256 bytes).  Measured, us at chunks of 128 /
-// 256 / 512 / 1024 / 2048 / 4096 tokens: one sequence of 30000, 8 heads: 30.4 / 22.4 /
-// 18.9; 16 of up to 2000: 20.9 / 17.6 / 16.4 / 17.9; 4 of up to 5000, 32 heads: - / 25.8 /
-// 22.3 / 24.6 / 32.1 / 41.7; 64 of up to 6000, 8 heads: - / - / 80.6 / 69.7 / 71 / 89;
-// 8-bit rows of 256 channels, 4 of up to 9000: 58.2 / 43.8 / 35.1 / 28.8.  Up to 512 tokens
-// one block does without a join: 9.4 us where four chunks and a second launch take 9.5.
+// 256 / 512 / 1024 / 2048 / 4096 tokens: one sequence of 30000, 8 heads: 31.2 / 22.5 /
+// 19.1 / 19.6; 16 of up to 2000: 20.0 / 18.7 / 16.8 / 17.8 / 22.0 / 21.9; 4 of up to 5000, 32
+// heads: 32.0 / 25.0 / 22.8 / 25.3 / 32.5 / 41.2; 64 of up to 6000, 8 heads: 161 / 110 / 91.3 /
+// 74.4 / 72.0 / 95.8; 8-bit rows of 256 channels, 4 of up to 9000: 63.7 / 45.8 / 35.4 / 28.4.
+// Up to 512 tokens one block does without a join: 9.8 us where four chunks and a second launch
+// take 10.8.
 // Where the bound leaves a choice (chunks above 128 tokens, several a sequence), batches of
 // up to kPieceBatch make it by the lengths on the device instead, which costs a block's
 // start up to 1 us and serves page tables made for longer sequences (bounds of 131072
-// tokens, by the bound / by the lengths: 8 sequences of 2000 44.5 / 15.4 us, 64 of 2000 to
-// 6000 161 / 68, 256 of 1000 212 / 63, 300 of 700 180 / 64) and ragged batches (32 of up to
-// 30000 127 / 113); with tight bounds 64 of 4096 61.6 / 61.5, 16 of up to 2000 17.0 / 17.0,
-// one of 30000 18.9 / 20.1.
+// tokens, by the bound / by the lengths: 8 sequences of 2000 46.4 / 15.6 us, 64 of 2000 to
+// 6000 162 / 70, 256 of 1000 196 / 64, 300 of 700 183 / 65) and ragged batches (32 of up to
+// 30000 136 / 116); with tight bounds 64 of 4096 61.8 / 62.4, 16 of up to 2000 16.7 / 17.2,
+// one of 30000 19.1 / 20.4.
 static AttSplit att_split(int64_t B, int64_t Hkv, int ratio, int row_bytes, int64_t max_len) {
   AttSplit sp{};
   sp.max_len = max_len;
