@@ -579,6 +579,132 @@ int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const
                      int32_t bits, float scale, int64_t max_len, void* workspace, size_t workspace_bytes,
                      void* stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Around the layers: the norm between two blocks, the product in 8-bit
+ * integers, and the choice of the next token.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * awq_norm -- ends a block and begins the next: the block's output y enters the
+ * residual stream h, and the next block's input x is normed from that.  Per
+ * token t (all arithmetic fp32):
+ *   h_out[t] = round_h( h[t] + scale * gate[r] * P(y[t]) )
+ *   x[t]     = round_16( Q(h_out[t]) )
+ * with P(y) = y, or the norm of y by post_weight and post_bias; Q the norm by
+ * weight and bias; the norm of a row v
+ *   kind AWQ_NORM_RMS:    v * r * weight [+ bias],  r = 1 / sqrt(mean(v^2) + eps)
+ *   kind AWQ_NORM_LAYER:  (v - mean(v)) * r * weight [+ bias],
+ *                         r = 1 / sqrt(mean((v - mean(v))^2) + eps)
+ *   h            device [T][N], fp16 (h_bytes = 2) or fp32 (4); token t's row
+ *                starts at h + t * h_stride (elements, a multiple of 8, >= N)
+ *   y            device fp16, rows at y + t * y_stride; NULL: x is normed from
+ *                h as it is, and nothing of the residual's arguments is given
+ *   post_weight, post_bias   device fp16 [N] or NULL
+ *   gate         device fp16 [gates][N] or NULL (1)
+ *   gate_rows    device int32 [T]: token t's row r of gate; a row outside
+ *                [0, gates) adds nothing (padding).  NULL: gates is 1, or T
+ *                (row t)
+ *   weight, bias device fp16 [N]; weight NULL: only h_out is computed
+ *   h_out        device, as h, rows of N; may be h itself (h_stride == N)
+ *   x            device fp16 [T][N]; with x_scales int8 [T][N], the rows in 8
+ *                bits that awq_gemm_i8 takes
+ *   x_scales     device fp32 [T] or NULL.  With it (kind rms, no bias) the
+ *                codes are those of the unrounded row, in which r drops out:
+ *                with v = h_out[t] * weight (fp32), code = rint(127 v / max|v|),
+ *                exactly, and x_scales[t] = r * max|v| / 127; a row of zeros has
+ *                codes and scale 0
+ * Requires T in [1, 2^24], N % 8 == 0, 8 <= N <= 65536, eps >= 0 and finite,
+ * |scale| finite.  Apart from h_out = h no output overlaps an input or another.
+ */
+#define AWQ_NORM_RMS 0
+#define AWQ_NORM_LAYER 1
+int awq_norm(const void* h, int32_t h_bytes, int64_t h_stride, const void* y, int64_t y_stride,
+             const void* post_weight, const void* post_bias, const void* gate, const int32_t* gate_rows, int64_t gates,
+             float scale, const void* weight, const void* bias, int32_t kind, float eps, void* h_out, void* x,
+             float* x_scales, int64_t T, int64_t N, void* stream);
+
+/*
+ * Rows in 8 bits: int8 codes in [-127, 127] and one fp32 scale a row,
+ *   code[k] = rint(127 v[k] / max|v|)  exactly (half to even),  scale = max|v| / 127
+ * (a row of zeros: codes and scale 0), the row standing for code * scale.
+ *
+ * awq_quantize_rows -- activations: v = x, or x / s (fp32, rounded once) with
+ * the per-channel input scales s that awq_quantize finds.
+ *   x       device fp16; row m at x + m * x_stride (elements, a multiple of 8, >= K)
+ *   s       device fp32 [K] or NULL
+ *   codes   device int8 [M][K]   out
+ *   scales  device fp32 [M]      out
+ * awq_pack_i8 -- weights: v = W, or W * s (fp32, rounded once).
+ *   W       device fp16 [N][K];  codes int8 [N][K], scales fp32 [N]   out
+ * Require K % AWQ_GROUP == 0, K <= 2^17, M and N in [1, 2^24].
+ */
+int awq_quantize_rows(const void* x, int64_t x_stride, const float* s, int64_t M, int64_t K, void* codes, float* scales,
+                      void* stream);
+int awq_pack_i8(const void* W, const float* s, int64_t N, int64_t K, void* codes, float* scales, void* stream);
+
+/*
+ * awq_gemm_i8 -- the product of rows in 8 bits, a scale for each token and each
+ * channel:  y[m][n] = x_scales[m] * scales[n] * sum_k xc[m][k] * codes[n][k].
+ * The sum is a whole number, exact in 32 bits (127^2 * 2^17 < 2^31); the result
+ * is rounded to fp32 at each scale, and once more to fp16.
+ *   x         x_scales given: device int8 [M][K] (rows of awq_quantize_rows or
+ *             awq_norm).  x_scales NULL: device fp16 [M][K], quantised on the way
+ *             as by awq_quantize_rows with s
+ *   s         device fp32 [K] or NULL; only with x_scales NULL
+ *   codes, scales   device int8 [N][K], fp32 [N] (awq_pack_i8's)
+ *   y         device fp16 (y_bytes = 2) or fp32 (4) [M][N], apart from the inputs
+ *   workspace device, >= awq_gemm_i8_workspace_bytes(M, N, K, x_scales given)
+ *             bytes (may be NULL where that is 0); it needs no clearing and keeps
+ *             nothing
+ * Requires M in [1, 2^22], N in [1, 2^24], M * N <= 2^36, K % AWQ_GROUP == 0,
+ * K <= 2^17.
+ */
+size_t awq_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t quantized);
+int awq_gemm_i8(const void* x, const float* x_scales, const float* s, const void* codes, const float* scales, void* y,
+                int32_t y_bytes, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/* awq_gemm_i8_kernel -- the product's kernel for these sizes, as awq_gemm_kernel says
+ * it of the W4A16 product: a host-only dry run (160 bytes always suffice). */
+int awq_gemm_i8_kernel(int64_t M, int64_t N, int64_t K, int32_t quantized, char* out, size_t out_bytes);
+
+/*
+ * awq_sample -- one token of each of B rows of logits, from given random numbers.
+ * Per row, with temperature t, top_k k, top_p p, min_p m and random number u:
+ *   weights   w_i = exp((l_i - max l) / t); t not above 0 (or NaN): the first of
+ *             the largest logits has weight 1, the others none
+ *   order     by logit, largest first, the lower index first where equal
+ *   top-k     the first k (k < 1 or k >= V: all)
+ *   top-p     of those, the ones before which the sum of weights is below p times
+ *             their sum, and always the first (p >= 1 or NaN: all)
+ *   min-p     of those, the ones with w_i >= m, and always the first (m <= 0 or
+ *             NaN: all)
+ *   token     the first index i, in index order, of the remaining ones at which
+ *             their weights' sum up to i exceeds u times their sum (u below 0 or
+ *             NaN counts as 0; from 1 on the last one)
+ * Weights are computed in 64 bits and summed as multiples of 2^-43, exactly and in
+ * any order; a weight below 2^-44 counts as none.  A logit of -infinity or NaN is
+ * never chosen; where there is no other the token is -1 and its probability 0.
+ * Logits of +infinity share all the weight.
+ *   logits       device, fp16 (logit_bytes = 2) or fp32 (4); row b starts at
+ *                logits + b * stride (elements, any number >= V)
+ *   temperature, top_p, min_p   device fp32 [B], or NULL: *_value for every row
+ *   top_k        device int32 [B], or NULL: top_k_value for every row
+ *   u            device fp32 [B]
+ *   tokens       device int32 [B]   out
+ *   probs        device fp32 [B] or NULL   out: the token's share of the
+ *                remaining weights
+ *   workspace    device, >= awq_sample_workspace_bytes(B, V, logit_bytes) bytes (may
+ *                be NULL where that is 0); it needs no clearing and keeps nothing
+ * The values for every row must be numbers (not NaN).  Requires 1 <= B <= 2^20,
+ * 1 <= V <= 2^20, B * stride < 2^40.
+ */
+size_t awq_sample_workspace_bytes(int64_t B, int64_t V, int32_t logit_bytes);
+int awq_sample(const void* logits, int32_t logit_bytes, int64_t stride, int64_t B, int64_t V, const float* temperature,
+               float temperature_value, const int32_t* top_k, int32_t top_k_value, const float* top_p,
+               float top_p_value, const float* min_p, float min_p_value, const float* u, int32_t* tokens, float* probs,
+               void* workspace, size_t workspace_bytes, void* stream);
+
 /* Message for a status code; message for the calling thread's last failure. */
 const char* awq_status_string(int status);
 const char* awq_last_error(void);

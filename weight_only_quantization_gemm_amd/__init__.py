@@ -32,6 +32,17 @@ from .api import (  # noqa: F401
     empty_packed,
     packed_words,
 )
+from .block import (  # noqa: F401
+    NORM_KINDS,
+    awq_gemm_i8,
+    awq_gemm_i8_kernel,
+    awq_gemm_i8_workspace_bytes,
+    awq_norm,
+    awq_pack_i8,
+    awq_quantize_rows,
+    awq_sample,
+    awq_sample_workspace_bytes,
+)
 from .serve import (  # noqa: F401
     KV_BITS,
     KV_HEAD_DIMS,

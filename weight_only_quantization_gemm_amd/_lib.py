@@ -12,6 +12,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libawq.so")
 
 c_i32, c_i64, c_size, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+c_f32 = ctypes.c_float
 
 # name -> (restype, argtypes), mirroring include/awq.h
 SIGNATURES = {
@@ -64,6 +65,16 @@ SIGNATURES = {
     "awq_kv_attention_workspace_bytes": (c_size, [c_i64, c_i32, c_i32, c_i32, c_i32, c_i64]),
     "awq_kv_attention": (ctypes.c_int, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i32,
                                         c_i32, c_i32, c_i64, c_i32, c_i32, ctypes.c_float, c_i64, c_vp, c_size, c_vp]),
+    "awq_norm": (ctypes.c_int, [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_f32, c_vp, c_vp, c_i32,
+                                c_f32, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp]),
+    "awq_quantize_rows": (ctypes.c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "awq_pack_i8": (ctypes.c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "awq_gemm_i8_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i32]),
+    "awq_gemm_i8": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_size, c_vp]),
+    "awq_gemm_i8_kernel": (ctypes.c_int, [c_i64, c_i64, c_i64, c_i32, ctypes.c_char_p, c_size]),
+    "awq_sample_workspace_bytes": (c_size, [c_i64, c_i64, c_i32]),
+    "awq_sample": (ctypes.c_int, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_f32, c_vp, c_i32, c_vp, c_f32, c_vp, c_f32,
+                                  c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
     "awq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "awq_last_error": (ctypes.c_char_p, []),
     "awq_version": (ctypes.c_int, []),

@@ -16,7 +16,8 @@ LIB = os.path.join(PKG, "libawq.so")
 CEILINGS_LIB = os.path.join(PKG, "libawq_ceilings.so")
 
 SOURCES = ["awq_api.hip", "awq_api_serve.hip", "stats.hip", "gram.hip", "quant.hip", "loss.hip", "gemv.hip", "skinny.hip",
-           "gemm.hip", "gemm_pipe.hip", "moe.hip", "grouped.hip", "kv_cache.hip", "kv_attention.hip"]
+           "gemm.hip", "gemm_pipe.hip", "moe.hip", "grouped.hip", "kv_cache.hip", "kv_attention.hip",
+           "awq_api_block.hip", "norm.hip", "rows_i8.hip", "gemm_i8.hip", "sample.hip"]
 CEILINGS_SOURCES = ["ceilings.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "awq_common.h"
 #include "kv_common.h"
 
 namespace awq {
@@ -125,6 +126,48 @@ size_t kv_attention_workspace(int64_t B, int64_t Hkv, int ratio, int D, int bits
 hipError_t launch_kv_attention(const void* q, int64_t q_stride, KvHalf kc, KvHalf vc, const int32_t* table,
                                int64_t width, const int32_t* lengths, int64_t B, int ratio, int D, int bits,
                                float scale, int64_t max_len, KvShape sh, void* out, void* ws, hipStream_t st);
+
+// norm.hip: the residual sum and the next block's norm (fields as awq_norm's arguments)
+struct NormArgs {
+  const void* h;
+  int64_t h_stride;
+  const f16* y;
+  int64_t y_stride;
+  const f16 *post_weight, *post_bias, *gate;
+  const int32_t* gate_rows;
+  int64_t gates;
+  const f16 *weight, *bias;
+  void *h_out, *x;
+  float* x_scales;
+  int64_t T, N;
+  float scale, eps;
+  int kind;
+};
+hipError_t launch_norm(const NormArgs& a, int h_bytes, hipStream_t st);
+
+// rows_i8.hip: rows to 8 bits, of x / s (divide) or x * s; s may be null
+hipError_t launch_rows_i8(const void* x, int64_t stride, const float* s, bool divide, int64_t M, int64_t K, void* codes,
+                          float* scales, hipStream_t st);
+
+// gemm_i8.hip: the product in 8-bit integers
+size_t gemm_i8_workspace(int64_t M, int64_t N, int64_t K, bool quantized);
+hipError_t launch_gemm_i8(const void* x, const float* x_scales, const float* s, const void* codes, const float* scales,
+                          void* y, int y_bytes, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t st);
+
+// sample.hip: the token of each row of logits (fields as awq_sample's arguments)
+struct SampleArgs {
+  const void* logits;
+  int64_t stride, V;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p, *u;
+  int32_t* tokens;
+  float* probs;
+  float temperature_value, top_p_value, min_p_value;
+  int32_t top_k_value;
+};
+size_t sample_workspace(int64_t B, int64_t V, int logit_bytes);
+hipError_t launch_sample(const SampleArgs& a, int logit_bytes, int64_t B, hipStream_t st);
 
 // Dry runs of the product dispatch.  While a KernelPlan is installed on the
 // calling thread, each product launcher writes the kernel it would launch (its

@@ -1,0 +1,167 @@
+// The norm between two blocks: the block's output enters the residual stream,
+// and the next block's input is normed from that, as fp16 or as rows of 8 bits.
+//
+// A row stays in the registers of the L threads that share it from its one read to
+// its last write, so every byte moves once; two statistics (post-norm) make two
+// joins over the row, a layer norm's mean and variance two each, the second from
+// the differences to the mean, so nothing cancels.  Bound by memory, at a decoding
+// step's sizes by the launch and the chain load - join - store.
+#include "awq.h"
+#include "awq_internal.h"
+#include "row_common.h"
+
+namespace awq {
+
+template <typename H>
+struct RowVec;
+template <>
+struct RowVec<f16> {
+  typedef f16x8 type;
+};
+template <>
+struct RowVec<float> {
+  typedef f32x8 type;
+};
+
+__device__ __forceinline__ f32x8 as_f32(f16x8 v) { return widen(v); }
+__device__ __forceinline__ f32x8 as_f32(f32x8 v) { return v; }
+
+// mean (0 unless layer) and 1 / sqrt(variance + eps) of the row v.
+template <int L, int PER>
+__device__ __forceinline__ void statistics(const f32x8 (&v)[PER], const bool (&live)[PER], int64_t N, bool layer,
+                                           float eps, float* part, float* mean, float* r) {
+  constexpr int W = L / 64;
+  float sum = 0.f;
+  *mean = 0.f;
+  if (layer) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += v[p][u];  // 0 beyond the row
+    *mean = row_join<L>(sum, part, AddOp()) / (float)N;
+  }
+  sum = 0.f;
+#pragma unroll
+  for (int p = 0; p < PER; ++p)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float d = live[p] ? v[p][u] - *mean : 0.f;
+      sum = fmaf(d, d, sum);
+    }
+  sum = row_join<L>(sum, part + W, AddOp());
+  *r = 1.f / sqrtf(sum / (float)N + eps);
+}
+
+template <typename H, int L, int PER>
+__global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
+  typedef typename RowVec<H>::type HV;
+  constexpr int ROWS = L < 256 ? 256 / L : 1, W = L / 64;
+  __shared__ float part[5 * W];
+  const int lane = threadIdx.x % L;
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * ROWS + threadIdx.x / L;
+  if (t >= a.T) return;  // a whole wave of its own row (L = 64) or the whole block
+  const bool layer = a.kind == AWQ_NORM_LAYER;
+  bool live[PER];
+  int64_t at[PER];
+  f32x8 h[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    at[p] = (int64_t)(p * L + lane) * 8;
+    live[p] = at[p] < a.N;
+    h[p] = f32x8{};
+    if (live[p]) h[p] = as_f32(*reinterpret_cast<const HV*>(reinterpret_cast<const H*>(a.h) + t * a.h_stride + at[p]));
+  }
+  float mean, r;
+  if (a.y != nullptr) {
+    f32x8 y[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      y[p] = f32x8{};
+      if (live[p]) y[p] = widen(*reinterpret_cast<const f16x8*>(a.y + t * a.y_stride + at[p]));
+    }
+    if (a.post_weight != nullptr) {
+      statistics<L>(y, live, a.N, layer, a.eps, part, &mean, &r);
+#pragma unroll
+      for (int p = 0; p < PER; ++p)
+        if (live[p]) {
+          const f32x8 w = widen(*reinterpret_cast<const f16x8*>(a.post_weight + at[p]));
+          y[p] = (y[p] - mean) * r * w;
+          if (a.post_bias != nullptr) y[p] += widen(*reinterpret_cast<const f16x8*>(a.post_bias + at[p]));
+        }
+    }
+    int64_t row = a.gates > 1 ? t : 0;
+    if (a.gate_rows != nullptr) row = a.gate_rows[t];
+    const bool adds = a.gate == nullptr || (row >= 0 && row < a.gates);
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      if (live[p]) {
+        f32x8 g = f32x8{} + a.scale;
+        if (a.gate != nullptr && adds) g = widen(*reinterpret_cast<const f16x8*>(a.gate + row * a.N + at[p])) * a.scale;
+        if (adds) h[p] += y[p] * g;
+        const HV kept = __builtin_convertvector(h[p], HV);
+        h[p] = as_f32(kept);
+        *reinterpret_cast<HV*>(reinterpret_cast<H*>(a.h_out) + t * a.N + at[p]) = kept;
+      }
+  }
+  if (a.weight == nullptr) return;
+  statistics<L>(h, live, a.N, layer, a.eps, part + 2 * W, &mean, &r);
+  f32x8 w[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    w[p] = f32x8{};
+    if (live[p]) w[p] = widen(*reinterpret_cast<const f16x8*>(a.weight + at[p]));
+  }
+  if (a.x_scales == nullptr) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      if (live[p]) {
+        f32x8 x = (h[p] - mean) * r * w[p];
+        if (a.bias != nullptr) x += widen(*reinterpret_cast<const f16x8*>(a.bias + at[p]));
+        *reinterpret_cast<f16x8*>(reinterpret_cast<f16*>(a.x) + t * a.N + at[p]) = __builtin_convertvector(x, f16x8);
+      }
+    return;
+  }
+  float top = 0.f;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    w[p] *= h[p];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(w[p][u]));
+  }
+  top = row_join<L>(top, part + 4 * W, MaxOp());
+  const float by = 127.f / top;
+#pragma unroll
+  for (int p = 0; p < PER; ++p)
+    if (live[p]) {
+      float c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) c[u] = code_of(w[p][u], by, top);
+      *reinterpret_cast<u32x2*>(reinterpret_cast<int8_t*>(a.x) + t * a.N + at[p]) =
+          u32x2{code_word(c[0], c[1], c[2], c[3]), code_word(c[4], c[5], c[6], c[7])};
+    }
+  if (lane == 0) a.x_scales[t] = r * (top / 127.f);
+}
+
+template <int L, int PER>
+static hipError_t norm_launch(const NormArgs& a, int h_bytes, hipStream_t st) {
+  constexpr int THREADS = L < 256 ? 256 : L, ROWS = THREADS / L;
+  const int64_t blocks = (a.T + ROWS - 1) / ROWS;
+  const unsigned wide = blocks < 65536 ? (unsigned)blocks : 65536u;
+  const dim3 grid(wide, (unsigned)((blocks + wide - 1) / wide)), block(THREADS);
+  if (h_bytes == 2) norm_kernel<f16, L, PER><<<grid, block, 0, st>>>(a);
+  else norm_kernel<float, L, PER><<<grid, block, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm(const NormArgs& a, int h_bytes, hipStream_t st) {
+  if (a.N <= 512) return norm_launch<64, 1>(a, h_bytes, st);
+  if (a.N <= 1024) return norm_launch<64, 2>(a, h_bytes, st);
+  if (a.N <= 2048) return norm_launch<256, 1>(a, h_bytes, st);
+  if (a.N <= 4096) return norm_launch<512, 1>(a, h_bytes, st);
+  if (a.N <= 8192) return norm_launch<1024, 1>(a, h_bytes, st);
+  if (a.N <= 16384) return norm_launch<1024, 2>(a, h_bytes, st);
+  if (a.N <= 32768) return norm_launch<1024, 4>(a, h_bytes, st);
+  return norm_launch<1024, 8>(a, h_bytes, st);
+}
+
+}  // namespace awq

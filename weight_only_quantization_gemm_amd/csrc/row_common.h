@@ -1,0 +1,66 @@
+// Rows held in registers: sums and maxima over the threads that share a row,
+// and the rounding of a row to 8 bits.
+#pragma once
+
+#include "awq_common.h"
+
+namespace awq {
+
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x8 widen(f16x8 v) { return __builtin_convertvector(v, f32x8); }
+
+// A wave's join of v by `op` (0 its neutral element), in every lane: shifts within
+// rows of 16 lanes, then each row's last lane broadcast to the rows above.
+template <typename Op>
+__device__ __forceinline__ float wave_join(float v, Op op) {
+  auto step = [&](int other) { v = op(v, __int_as_float(other)); };
+  step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x111, 0xF, 0xF, false));  // row_shr 1, 2, 4, 8
+  step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x112, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x114, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x118, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));  // row_bcast 15, 31
+  step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+struct AddOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct MaxOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+
+// The same over the L threads of a row (L = 64: a wave, otherwise the whole block)
+// by way of part [L / 64], which no thread may still be reading: callers take
+// another part for each join between two barriers of their own.
+template <int L, typename Op>
+__device__ __forceinline__ float row_join(float v, float* part, Op op) {
+  v = wave_join(v, op);
+  if constexpr (L > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    lds_barrier();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < L / 64; ++w) v = op(v, part[w]);
+  }
+  return v;
+}
+
+// rint(127 v / top) exactly, for top = max |v| over the row; by = 127 / top rounded.
+// The product v * by is within 2^-15 of 127 v / top, so its nearest whole number
+// is the wanted one unless it lies closer than that to a half; there (one value in
+// ten thousand) the quotient is formed in 64 bits, whose 53 can hold every half
+// and miss none: 127 v / top is a half itself or at least 2^-26 away from it.
+__device__ __forceinline__ float code_of(float v, float by, float top) {
+  const float q = v * by, r = rintf(q);
+  if (fabsf(q - r) <= 0.4999f) return r;  // false for a NaN too: by overflows where top is tiny
+  return top > 0.f ? (float)rint(127.0 * (double)v / (double)top) : 0.f;
+}
+
+// Four codes as the bytes of a word.
+__device__ __forceinline__ uint32_t code_word(float a, float b, float c, float d) {
+  return ((uint32_t)(int)a & 255u) | ((uint32_t)(int)b & 255u) << 8 | ((uint32_t)(int)c & 255u) << 16 |
+         (uint32_t)(int)d << 24;
+}
+
+}  // namespace awq
