@@ -1,319 +1,699 @@
 // The next token of each row of logits: temperature, top-k, top-p and min-p, and
 // the choice by a given random number, without sorting the row.
 //
-// One block takes one row.  The order of the tokens (logit descending, then index)
-// only matters at the border of what is kept, which a search digit by digit over
-// the logits' order-preserving images finds: by counts for top-k, by weights for
-// top-p.  Weights are whole multiples of 2^-43, so their sums are the same in any
-// order and the result does not depend on timing.  The choice itself walks the
-// row's sums in index order.
+// One block takes one row and keeps it in registers (16-byte pieces, up to 16 a
+// thread; what is beyond is read again from the caches).  What is kept is always a
+// first part of the tokens in order (logit descending, then index), so all that
+// has to be found is its border:
+//   few tokens kept (top-k up to kListK, or min-p alone): a logit that at least k
+//   tokens reach, from the threads' own maxima, leaves a list short enough to sort;
+//   otherwise: a histogram of the weights (and counts) over equal steps of the
+//   logit finds the border's bin, whose tokens are then sorted.  A bin with more
+//   tokens than the list holds (ties) is searched digit by digit instead.
+// The choice walks sums in index order: over the list where it holds all that is
+// kept, over the row otherwise.
+//
+// Weights are whole multiples of 2^-43, so their sums are exact in any order and
+// the result does not depend on timing; as a double a thread's sum stays below
+// 2^53 (2^10 tokens of at most 2^43), a row's below 2^63 as a 64-bit number.
 #include "awq_internal.h"
 #include "row_common.h"
 
 namespace awq {
 
-constexpr int kSampleThreads = 1024, kSampleWaves = kSampleThreads / 64;
-constexpr double kWeightOne = 8796093022208.0;  // 2^43: a row of 2^20 tokens sums to at most 2^63
+constexpr double kWeightOne = 8796093022208.0;  // 2^43
+constexpr int kBins = 2048, kList = 2048, kExpTable = 512;
+constexpr double kExpRate = 738.6598609351493;  // kExpTable log2(e)
 
-// Order-preserving image of a logit; 0: one that is never chosen (-inf, NaN).
+// Order-preserving image of a logit (never 0 for one that can be chosen: not -inf, not NaN).
 __device__ __forceinline__ uint32_t logit_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);  // -0 becomes +0
-  return v > -INFINITY ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float key_logit(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-__device__ __forceinline__ uint64_t shfl64(uint64_t v, int lane) {
-  return (uint64_t)(uint32_t)__shfl((int)(uint32_t)v, lane, kWave) |
-         (uint64_t)(uint32_t)__shfl((int)(uint32_t)(v >> 32), lane, kWave) << 32;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t shifted64(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+  return (uint64_t)hi << 32 | lo;
 }
 __device__ __forceinline__ uint64_t scan64(uint64_t v) {  // inclusive, over the wave
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t o = shfl64(v, lane >= d ? lane - d : lane);
-    v += lane >= d ? o : 0;
-  }
+  v += shifted64<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8, then the rows' sums to the rows above
+  v += shifted64<0x112, 0xF>(v);
+  v += shifted64<0x114, 0xF>(v);
+  v += shifted64<0x118, 0xF>(v);
+  v += shifted64<0x142, 0xA>(v);
+  v += shifted64<0x143, 0xC>(v);
   return v;
 }
+__device__ __forceinline__ uint64_t lane64(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane) |
+         (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32;
+}
 
-// A row's 16-byte pieces: piece j holds the E elements from j E - lead on.
-template <typename T>
-struct LogitRow {
-  static constexpr int E = 16 / sizeof(T);
+template <int THREADS>
+struct SampleShared {
+  uint64_t list[kList];      // entries, or the bins' weights
+  uint32_t counts[kBins];    // the bins' counts
+  double table[kExpTable];   // 2^(j / kExpTable)
+  uint32_t maxima[THREADS];  // images of the threads' largest logits
+  uint64_t part[2][THREADS / 64];
+  uint64_t found[4];
+  float most[2][THREADS / 64];
+  int n;
+};
+
+// What is kept: tokens above value, and of those equal to it the indices up to last.
+struct Border {
+  float value;
+  int last;
+  __device__ __forceinline__ bool keeps(float x, int i) const { return x > value || (x == value && i <= last); }
+};
+
+// A row, without the pieces its threads hold.
+template <typename T, int THREADS>
+struct SampleShape {
+  static constexpr int E = 16 / sizeof(T), WAVES = THREADS / 64;
   typedef T vec __attribute__((ext_vector_type(E)));
+  SampleShared<THREADS>& sh;
   const T* base;  // 16-byte aligned, lead elements before the row
-  int lead, V, pieces;
-  __device__ LogitRow(const T* row, int V_) : V(V_) {
-    lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-    base = row - lead;
-    pieces = (lead + V + E - 1) / E;
-  }
-  // keys of the piece's elements; 0 outside the row
-  __device__ __forceinline__ void keys(int j, uint32_t (&k)[E]) const {
+  int lead, V, cw;  // cw: chunks (64 pieces) of a wave; wave w has chunks w cw .. w cw + cw - 1
+  bool infinite;    // some logit is +inf: those weigh 1 and all others nothing
+  double top, rate; // largest logit, kExpTable log2(e) / temperature
+
+  // Piece j: elements j E - lead .. + E - 1, NaN outside the row.
+  __device__ __forceinline__ vec load(int j) const {
     const int first = j * E - lead;
+    vec x;
     if (first >= 0 && first + E <= V) {
-      const vec v = *reinterpret_cast<const vec*>(base + (int64_t)j * E);
-#pragma unroll
-      for (int u = 0; u < E; ++u) k[u] = logit_key((float)v[u]);
+      x = *reinterpret_cast<const vec*>(base + (int64_t)j * E);
     } else {
 #pragma unroll
-      for (int u = 0; u < E; ++u)
-        k[u] = first + u >= 0 && first + u < V ? logit_key((float)base[(int64_t)j * E + u]) : 0u;
+      for (int e = 0; e < E; ++e)
+        x[e] = first + e >= 0 && first + e < V ? base[(int64_t)j * E + e] : (T)__builtin_nanf("");
     }
-  }
-};
-
-// The kept part of a row: tokens above key, and of those equal to it the indices up to last.
-struct Border {
-  uint32_t key;
-  int last;
-  __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= last); }
-};
-
-struct Weigher {
-  double top, by;  // largest logit, 1 / temperature
-  float topf;
-  __device__ __forceinline__ double operator()(uint32_t key) const {
-    const float v = key_logit(key);
-    if (v == topf) return 1.0;
-    const double z = ((double)v - top) * by;
-    return z > -31.0 ? exp(z) : 0.0;  // below 2^-44; false for a NaN (infinite logits, infinite temperature)
-  }
-};
-__device__ __forceinline__ uint64_t fixed(double w) { return (uint64_t)rint(w * kWeightOne); }
-
-template <typename T>
-struct SampleRow {
-  LogitRow<T> row;
-  uint64_t* sums;     // [chunks]: of each wave's 64 pieces
-  uint64_t* weights;  // [256]
-  uint32_t* counts;   // [256]
-  uint64_t* found;    // [4]
-  static constexpr int E = LogitRow<T>::E;
-
-  // sums[c] of amount(key, index) over chunk c; returns the row's sum.
-  template <typename F>
-  __device__ uint64_t chunk_sums(F amount) {
-    const int lane = threadIdx.x & 63, chunks = (row.pieces + 63) / 64;
-    for (int c = threadIdx.x >> 6; c < chunks; c += kSampleWaves) {
-      const uint64_t s = scan64(piece_sum(c * 64 + lane, amount));
-      if (lane == 63) sums[c] = s;
-    }
-    __syncthreads();
-    uint64_t total = 0;
-    for (int c = lane; c < chunks; c += 64) total += sums[c];
-    return shfl64(scan64(total), 63);
-  }
-  template <typename F>
-  __device__ uint64_t piece_sum(int j, F amount) const {
-    uint64_t s = 0;
-    if (j < row.pieces) {
-      uint32_t k[E];
-      row.keys(j, k);
+    if (infinite)
 #pragma unroll
-      for (int u = 0; u < E; ++u)
-        if (k[u] != 0) s += amount(k[u], j * E - row.lead + u);
+      for (int e = 0; e < E; ++e) x[e] = (float)x[e] == INFINITY ? (T)0.f : (T)-INFINITY;
+    return x;
+  }
+  __device__ __forceinline__ int piece(int u) const { return ((int)(threadIdx.x >> 6) * cw + u) * 64 + (threadIdx.x & 63); }
+  static __device__ __forceinline__ float largest(vec x) {
+    if constexpr (E == 8) {
+      const auto a = __builtin_elementwise_max(x.lo, x.hi);
+      const auto b = __builtin_elementwise_max(a.lo, a.hi);
+      return fmaxf((float)b.x, (float)b.y);
+    } else {
+      return fmaxf(fmaxf((float)x[0], (float)x[1]), fmaxf((float)x[2], (float)x[3]));
     }
-    return s;
   }
 
-  // After chunk_sums: the first index at which the sums exceed `target` (below the total), and
-  // its key; by the first wave, returned to every thread.
-  template <typename F>
-  __device__ int locate(uint64_t target, F amount, uint32_t* key) {
-    const int lane = threadIdx.x & 63, chunks = (row.pieces + 63) / 64;
-    if (threadIdx.x < 64) {
-      uint64_t before = 0;
-      int c0 = 0;
-      for (; c0 < chunks; c0 += 64) {
-        const uint64_t upto = scan64(c0 + lane < chunks ? sums[c0 + lane] : 0);
-        const uint64_t over = __ballot(before + upto > target);
-        if (over != 0) {
-          const int at = __builtin_ctzll(over);
-          c0 += at;
-          before += at == 0 ? 0 : shfl64(upto, at - 1);
-          break;
-        }
-        before += shfl64(upto, 63);
-      }
-      const int j = c0 * 64 + lane;
-      const uint64_t mine = piece_sum(j, amount), upto = before + scan64(mine);
-      const uint64_t over = __ballot(upto > target);
-      if (over != 0 && lane == __builtin_ctzll(over)) {
-        uint64_t sum = upto - mine;
-        uint32_t k[E];
-        row.keys(j, k);
-        bool done = false;
+  // The weight times 2^43, rounded to a whole number: exp(z) = 2^(i / 512) (1 + g), g = exp(f ln2 / 512)
+  // - 1 to the third power of f, |f| <= 1/2 (the fourth is below 2^-46).  Below z = -31 it is none.
+  __device__ __forceinline__ double weight(float x) const {
+    constexpr double c1 = 0.0013538030870311431, c2 = 9.163913992275265e-07, c3 = 4.1353783506767136e-10;  // (ln2/512)^n / n!
+    constexpr double least = -31.0 * kExpRate;
+    const double y = fmax(((double)x - top) * rate, least);  // `least` for a NaN too
+    const double n = rint(y), f = y - n;
+    const int i = (int)n;
+    const double t = sh.table[i & (kExpTable - 1)];
+    const double g = f * fma(f, fma(f, c3, c2), c1);
+    return rint(ldexp(fma(t, g, t), (i >> 9) + 43));
+  }
+
+  __device__ __forceinline__ uint64_t target_of(float share, uint64_t total) const {
+    const double at = (share > 0.f ? (double)share : 0.0) * (double)total;
+    const uint64_t target = at < (double)total ? (uint64_t)at : total - 1;
+    return target < total ? target : total - 1;
+  }
+  // the weight times 2^43 before its rounding
+  __device__ __forceinline__ double exact_weight(float x) const {
+    return (double)x == top ? kWeightOne : kWeightOne * exp(fmax(((double)x - top) * rate, -31.0 * kExpRate) / kExpRate);
+  }
+
+  // Sum over the block; inclusive sums up to this thread in *upto where asked for.
+  __device__ __forceinline__ uint64_t block_sum(uint64_t mine, int which, uint64_t* upto = nullptr) const {
+    const uint64_t s = scan64(mine);
+    if ((threadIdx.x & 63) == 63) sh.part[which][threadIdx.x >> 6] = s;
+    lds_barrier();
+    uint64_t all = 0, before = 0;
 #pragma unroll
-        for (int u = 0; u < E; ++u)
-          if (!done && k[u] != 0) {
-            sum += amount(k[u], j * E - row.lead + u);
-            if (sum > target) {
-              done = true;
-              found[0] = (uint64_t)(uint32_t)(j * E - row.lead + u);
-              found[1] = k[u];
+    for (int w = 0; w < WAVES; ++w) {
+      if (w == (int)(threadIdx.x >> 6)) before = all;
+      all += sh.part[which][w];
+    }
+    if (upto) *upto = before + s;
+    return all;
+  }
+
+  // Sorts list[0 .. n) descending (n <= kList; entries up to the next power of two become 0).
+  __device__ __forceinline__ void sort(int n) {
+    int size = 2;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += THREADS) sh.list[i] = 0;
+    lds_barrier();
+    const bool one_wave = size <= 128;
+    if (!one_wave || threadIdx.x < 64) {
+      for (int run = 2; run <= size; run *= 2)
+        for (int step = run / 2; step > 0; step /= 2) {
+          for (int i = threadIdx.x; i < size / 2; i += THREADS) {
+            const int a = 2 * i - (i & (step - 1)), b = a + step;
+            const uint64_t x = sh.list[a], y = sh.list[b];
+            if ((x < y) == ((a & run) == 0)) {
+              sh.list[a] = y;
+              sh.list[b] = x;
             }
           }
-      }
+          if (one_wave) __asm__ volatile("" ::: "memory");  // a wave's LDS accesses are done in order
+          else lds_barrier();
+        }
     }
-    __syncthreads();
-    const int index = (int)found[0];
-    *key = (uint32_t)found[1];
-    __syncthreads();
-    return index;
+    lds_barrier();
   }
+  static __device__ __forceinline__ uint64_t entry(float x, int i) { return (uint64_t)logit_key(x) << 32 | (uint32_t)~i; }
+  static __device__ __forceinline__ float entry_logit(uint64_t e) { return key_logit((uint32_t)(e >> 32)); }
 
-  // The border below which nothing is kept, searched within what `b` keeps: of the tokens in
-  // order, the one at which count (rank_at > 0: the rank_at-th token) or weight (the first
-  // token with the weight up to it at least `least`) is reached.  b stays where it is not reached.
-  __device__ void cut(Border* b, const Weigher& weigher, uint64_t rank_at, double least) {
+  // SampleRow::cut digit by digit over the logits' images, for many tokens of nearly one logit.
+  static __device__ __noinline__ Border cut_by_digits(const SampleShape s, const Border old, uint64_t rank_at, double least) {
+    return s.digits(old, rank_at, least);
+  }
+  __device__ __forceinline__ Border digits(const Border old, uint64_t rank_at, double least) const {
+    Border b = old;
     const bool by_count = rank_at > 0;
     uint32_t prefix = 0;
-    uint64_t above = 0;    // counts or weights of the tokens above the digits fixed so far
-    uint64_t equal = 0;    // tokens with the key found
+    uint64_t above = 0, equal = 0;  // counts or weights above the digits fixed so far; tokens with the key found
     for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSampleThreads) {
-        counts[i] = 0;
-        weights[i] = 0;
+      for (int i = threadIdx.x; i < 256; i += THREADS) {
+        sh.counts[i] = 0;
+        sh.list[i] = 0;
       }
-      __syncthreads();
-      for (int j = threadIdx.x; j < row.pieces; j += kSampleThreads) {
-        uint32_t k[E];
-        row.keys(j, k);
-#pragma unroll
-        for (int u = 0; u < E; ++u)
-          if (k[u] != 0 && b->keeps(k[u], j * E - row.lead + u) &&
-              (shift == 24 || (k[u] >> (shift + 8)) == prefix)) {
-            const uint32_t d = (k[u] >> shift) & 255u;
-            atomicAdd(&counts[d], 1u);
-            if (!by_count) atomicAdd(reinterpret_cast<unsigned long long*>(&weights[d]), (unsigned long long)fixed(weigher(k[u])));
-          }
+      lds_barrier();
+      for (int u = 0; u < cw; ++u) {
+        const vec x = load(piece(u));
+        const int j = piece(u);
+        for (int e = 0; e < E; ++e) {
+          const float l = (float)x[e];
+          const uint32_t key = logit_key(l);
+          if (!old.keeps(l, j * E - lead + e) || (shift < 24 && (key >> (shift + 8)) != prefix)) continue;
+          const uint64_t w = (uint64_t)weight(l);
+          if (w == 0) continue;
+          const uint32_t d = (key >> shift) & 255u;
+          atomicAdd(&sh.counts[d], 1u);
+          if (!by_count) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.list[d]), (unsigned long long)w);
+        }
       }
-      __syncthreads();
+      lds_barrier();
       if (threadIdx.x == 0) {
-        found[0] = 256;
+        sh.found[0] = 256;
         uint64_t sum = above;
         for (int d = 255; d >= 0; --d) {
-          if (counts[d] == 0) continue;
-          const uint64_t next = sum + (by_count ? counts[d] : weights[d]);
+          if (sh.counts[d] == 0) continue;
+          const uint64_t next = sum + (by_count ? sh.counts[d] : sh.list[d]);
           if (by_count ? next >= rank_at : (double)next >= least) {
-            found[0] = d;
-            found[1] = sum;
-            found[2] = counts[d];
+            sh.found[0] = d;
+            sh.found[1] = sum;
+            sh.found[2] = sh.counts[d];
             break;
           }
           sum = next;
         }
       }
-      __syncthreads();
-      const uint32_t d = (uint32_t)found[0];
-      above = found[1];
-      equal = found[2];
-      __syncthreads();
-      if (d == 256) return;  // not reached: everything stays
+      lds_barrier();
+      const uint32_t d = (uint32_t)sh.found[0];
+      above = sh.found[1];
+      equal = sh.found[2];
+      lds_barrier();
+      if (d == 256) return old;
       prefix = prefix << 8 | d;
     }
-    // of the `equal` tokens with that key, the first ones
-    uint64_t stay;
+    const float value = key_logit(prefix);
+    // of the `equal` tokens with that logit the first `stay`
+    uint64_t stay = 1;
     if (by_count) {
       stay = rank_at - above;
     } else {
-      const uint64_t one = fixed(weigher(prefix));
-      stay = 1;
-      while (stay < equal && (double)(above + stay * one) < least) {
-        const double more = one > 0 ? floor((least - (double)(above + stay * one)) / (double)one) : 1.0;
+      const double one = weight(value);  // above 0
+      while (stay < equal && (double)above + (double)stay * one < least) {
+        const double more = floor((least - ((double)above + (double)stay * one)) / one);
         stay += more < 1.0 ? 1 : more < (double)(equal - stay) ? (uint64_t)more : equal - stay;
       }
     }
-    int last = b->last;
-    if (prefix > b->key) last = 0x7FFFFFFF;
-    if (stay < equal) {
-      const Border old = *b;
-      const uint32_t key = prefix;
-      auto is = [=](uint32_t k, int i) -> uint64_t { return k == key && old.keeps(k, i) ? 1 : 0; };
-      chunk_sums(is);
-      uint32_t unused;
-      last = locate(stay - 1, is, &unused);
+    b.last = value > old.value ? 0x7FFFFFFF : old.last;
+    b.value = value;
+    if (stay >= equal) return b;
+    // the stay-th of them in index order: its wave, its chunk, its lane, its element
+    auto count = [&](vec x, int j) {
+      uint64_t c = 0;
+      for (int e = 0; e < E; ++e) c += (float)x[e] == value && old.keeps((float)x[e], j * E - lead + e) ? 1 : 0;
+      return c;
+    };
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint64_t mine = 0;
+    for (int u = 0; u < cw; ++u) mine += count(load(piece(u)), piece(u));
+    block_sum(mine, 0);
+    int w = 0;
+    while (w < WAVES - 1 && sh.part[0][w] < stay) stay -= sh.part[0][w++];
+    for (int u = wave; u < cw; u += WAVES) {
+      const int j = (w * cw + u) * 64 + lane;
+      const uint64_t s = scan64(count(load(j), j));
+      if (lane == 63) sh.list[u] = s;
     }
-    b->key = prefix;
-    b->last = last;
+    lds_barrier();
+    if (wave == 0) {
+      int u = 0;
+      while (u < cw - 1 && sh.list[u] < stay) stay -= sh.list[u++];
+      const int j = (w * cw + u) * 64 + lane;
+      const vec x = load(j);
+      const uint64_t own = count(x, j), upto = scan64(own);
+      if (own > 0 && upto >= stay && upto - own < stay) {
+        uint64_t left = stay - (upto - own);
+        for (int e = 0; e < E; ++e)
+          if ((float)x[e] == value && old.keeps((float)x[e], j * E - lead + e) && --left == 0) sh.found[0] = (uint64_t)(j * E - lead + e);
+      }
+    }
+    lds_barrier();
+    b.last = (int)sh.found[0];
+    lds_barrier();
+    return b;
   }
 };
 
-template <typename T>
-__global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a) {
-  extern __shared__ uint64_t sums[];
-  __shared__ uint64_t weights[256], found[4], part[kSampleWaves];
-  __shared__ uint32_t counts[256];
+template <typename T, int THREADS, int NV>
+struct SampleRow : SampleShape<T, THREADS> {
+  typedef SampleShape<T, THREADS> Shape;
+  using typename Shape::vec;
+  using Shape::E, Shape::WAVES, Shape::sh, Shape::lead, Shape::cw, Shape::top;
+  using Shape::load, Shape::piece, Shape::weight, Shape::block_sum, Shape::sort, Shape::largest, Shape::entry,
+      Shape::entry_logit, Shape::target_of, Shape::exact_weight;
+  vec v[NV];  // this thread's pieces of the first NV chunks of its wave
+  __device__ explicit SampleRow(const Shape& shape) : Shape(shape) {}
+
+  // f(piece, its number) for this thread's pieces, of those held and those that are not.  Only for what
+  // takes few registers beside them.  The empty asm hides that every pass sees the same values and
+  // indices: what one pass makes of them would otherwise be kept in registers for the next.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (u < cw) {
+        int j = piece(u);
+        __asm__ volatile("" : "+v"(v[u]), "+v"(j));
+        f(v[u], j);
+      }
+    for (int u = NV; u < cw; ++u) f(load(piece(u)), piece(u));
+  }
+  // The same with all pieces read again (from the caches), the next one under way.
+  template <typename F>
+  __device__ __forceinline__ void each_again(F f) const {
+    vec next = load(piece(0));
+#pragma unroll 1
+    for (int u = 0; u < cw; ++u) {
+      const vec x = next;
+      if (u + 1 < cw) next = load(piece(u + 1));
+      f(x, piece(u));
+    }
+  }
+
+  // list = the tokens that reach `least` and pass `also`, in any order; their number (more than
+  // kList: only some are in the list).
+  template <bool HELD, typename F>
+  __device__ __forceinline__ int gather(float least, F also) {
+    if (threadIdx.x == 0) sh.n = 0;
+    lds_barrier();
+    auto put = [&](vec x, int j) {
+      if (largest(x) >= least)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float l = (float)x[e];
+          const int i = j * E - lead + e;
+          if (l >= least && l > -INFINITY && also(l, i)) {
+            const int at = atomicAdd(&sh.n, 1);
+            if (at < kList) sh.list[at] = entry(l, i);
+          }
+        }
+    };
+    if constexpr (HELD) each(put);
+    else each_again(put);
+    lds_barrier();
+    const int n = sh.n;
+    lds_barrier();
+    return n;
+  }
+
+  // A logit that at least k tokens reach (k <= THREADS), the smallest live one if the threads with a
+  // live logit are fewer: by halving the range of the threads' maxima until few more than k remain.
+  __device__ __forceinline__ float reached_by(int k) {
+    if (threadIdx.x < 64) {
+      uint32_t key[WAVES], lo = ~0u, hi = 0u;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        key[w] = sh.maxima[w * 64 + threadIdx.x];
+        lo = key[w] < lo ? key[w] : lo;
+        hi = key[w] > hi ? key[w] : hi;
+      }
+#pragma unroll
+      for (int d = 32; d >= 1; d /= 2) {
+        const uint32_t l = (uint32_t)__shfl_xor((int)lo, d, kWave), h = (uint32_t)__shfl_xor((int)hi, d, kWave);
+        lo = l < lo ? l : lo;
+        hi = h > hi ? h : hi;
+      }
+      lo = lo > 0 ? lo : 1u;
+      // at least k maxima reach lo, unless lo is 1
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        int count = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) count += __popcll(__ballot(key[w] >= mid));
+        if (count >= k) {
+          lo = mid;
+          if (count <= k + k / 8 + 4) break;
+        } else {
+          hi = mid - 1;
+        }
+      }
+      if (threadIdx.x == 0) sh.found[0] = lo;
+    }
+    lds_barrier();
+    const uint32_t lo = (uint32_t)sh.found[0];
+    lds_barrier();
+    return lo <= 1u ? -INFINITY : key_logit(lo);
+  }
+
+  // Of the sorted list's first n entries, how many are kept.
+  __device__ __forceinline__ int kept_of_list(int n, int k, float p, double low) {
+    constexpr int Q = kList / THREADS;
+    if (k >= 1 && k < n) n = k;
+    double w[Q];
+    uint64_t upto[Q], carry = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = q * THREADS + threadIdx.x;
+      w[q] = 0.0;
+      upto[q] = 0;
+      if (q * THREADS < n) {
+        w[q] = i < n ? weight(entry_logit(sh.list[i])) : 0.0;
+        const uint64_t all = block_sum((uint64_t)w[q], q & 1, &upto[q]);
+        upto[q] += carry;
+        carry += all;
+      }
+    }
+    const double least = (double)p * (double)carry;
+    uint64_t kept = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = q * THREADS + threadIdx.x;
+      const bool in = i < n && (p >= 1.f || (double)(upto[q] - (uint64_t)w[q]) < least) && w[q] >= low;
+      kept += i == 0 || in ? 1 : 0;
+    }
+    lds_barrier();
+    return (int)block_sum(kept, 0);
+  }
+
+  // The token at `share` of the first n entries of the list; its probability.
+  __device__ __forceinline__ int choose_of_list(int n, float share, float* prob) {
+    constexpr int Q = kList / THREADS;
+    lds_barrier();
+    for (int i = threadIdx.x; i < n; i += THREADS) sh.list[i] = sh.list[i] << 32 | sh.list[i] >> 32;  // by index
+    lds_barrier();
+    sort(n);
+    uint64_t w[Q], upto[Q], total = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = q * THREADS + threadIdx.x;
+      w[q] = upto[q] = 0;
+      if (q * THREADS < n) {
+        w[q] = i < n ? (uint64_t)weight(key_logit((uint32_t)sh.list[i])) : 0;
+        const uint64_t all = block_sum(w[q], q & 1, &upto[q]);
+        upto[q] += total;
+        total += all;
+      }
+    }
+    const uint64_t target = target_of(share, total);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (upto[q] > target && upto[q] - w[q] <= target) sh.found[0] = sh.list[q * THREADS + threadIdx.x];
+    lds_barrier();
+    const uint64_t e = sh.found[0];
+    *prob = (float)(exact_weight(key_logit((uint32_t)e)) / (double)total);
+    return (int)~(uint32_t)(e >> 32);
+  }
+  // The token at `share` of all that b keeps with weights from low on.
+  __device__ __forceinline__ int choose_of_row(const Border& b, double low, float share, float* prob) {
+    auto amount = [&](vec x, int j) {
+      double s = 0.0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float l = (float)x[e];
+        const double w = weight(l);
+        s += b.keeps(l, j * E - lead + e) && w >= low ? w : 0.0;
+      }
+      return s;
+    };
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double mine = 0.0;
+    each_again([&](vec x, int j) { mine += amount(x, j); });
+    lds_barrier();
+    const uint64_t total = block_sum((uint64_t)mine, 0);
+    uint64_t target = target_of(share, total);
+    // the wave, then its chunk, then the lane and its element
+    int w = 0;
+    while (w < WAVES - 1 && sh.part[0][w] <= target) target -= sh.part[0][w++];
+    lds_barrier();
+    for (int u = wave; u < cw; u += WAVES) {
+      const int j = (w * cw + u) * 64 + lane;
+      const uint64_t s = scan64((uint64_t)amount(load(j), j));
+      if (lane == 63) sh.list[u] = s;
+    }
+    lds_barrier();
+    if (wave == 0) {
+      int u = 0;
+      while (u < cw - 1 && sh.list[u] <= target) target -= sh.list[u++];
+      const int j = (w * cw + u) * 64 + lane;
+      const vec x = load(j);
+      const uint64_t own = (uint64_t)amount(x, j), upto = scan64(own);
+      const uint64_t over = __ballot(upto > target);
+      if (lane == __builtin_ctzll(over)) {
+        uint64_t sum = upto - own;
+        bool done = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float l = (float)x[e];
+          const int i = j * E - lead + e;
+          const double we = weight(l);
+          sum += b.keeps(l, i) && we >= low ? (uint64_t)we : 0;
+          if (!done && sum > target) {
+            done = true;
+            sh.found[0] = entry(l, i);
+          }
+        }
+      }
+    }
+    lds_barrier();
+    const uint64_t e = sh.found[0];
+    *prob = (float)(exact_weight(entry_logit(e)) / (double)total);
+    return (int)~(uint32_t)e;
+  }
+
+  // Narrows b to the tokens up to the rank_at-th in order (rank_at > 0), or up to the first at which the
+  // weights reach the share p of all of b's; everything stays where that is not reached.
+  __device__ __forceinline__ void cut(Border* b, uint64_t rank_at, float p, float range) {
+    constexpr int PER = kBins / THREADS;
+    const bool by_count = rank_at > 0;
+    const float step = fminf((float)kBins / range, 1e30f);
+    auto bin_of = [&](float x) { return (int)fminf(((float)top - x) * step, (float)(kBins - 1)); };
+    for (int i = threadIdx.x; i < kBins; i += THREADS) {
+      sh.list[i] = 0;
+      sh.counts[i] = 0;
+    }
+    lds_barrier();
+    each_again([&](vec x, int j) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float l = (float)x[e];
+        if (!b->keeps(l, j * E - lead + e)) continue;
+        const uint64_t w = (uint64_t)weight(l);
+        if (w == 0) continue;  // cannot be chosen, kept or not
+        const int bin = bin_of(l);
+        if (by_count) atomicAdd(&sh.counts[bin], 1u);
+        else atomicAdd(reinterpret_cast<unsigned long long*>(&sh.list[bin]), (unsigned long long)w);
+      }
+    });
+    lds_barrier();
+    uint64_t mine = 0, amount[PER];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int i = threadIdx.x * PER + q;
+      amount[q] = by_count ? sh.counts[i] : sh.list[i];
+      mine += amount[q];
+    }
+    uint64_t upto;
+    if (threadIdx.x == 0) sh.found[0] = kBins;
+    const uint64_t all_bins = block_sum(mine, 0, &upto);
+    uint64_t before = upto - mine;
+    const double least = (double)p * (double)all_bins;
+    auto reached = [&](uint64_t sum) { return by_count ? sum >= rank_at : (double)sum >= least; };
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      if (amount[q] > 0 && reached(before + amount[q]) && (before == 0 || !reached(before))) {
+        sh.found[0] = threadIdx.x * PER + q;
+        sh.found[1] = before;
+      }
+      before += amount[q];
+    }
+    lds_barrier();
+    const int bin = (int)sh.found[0];
+    const uint64_t above = sh.found[1];
+    lds_barrier();
+    if (bin == kBins) return;
+    const Border old = *b;
+    const int n = gather<false>(-INFINITY, [&](float l, int i) { return bin_of(l) == bin && old.keeps(l, i) && weight(l) > 0.0; });
+    if (n > kList) {
+      *b = Shape::cut_by_digits(*this, old, rank_at, least);  // by value: the pieces stay in registers
+      return;
+    }
+    sort(n);
+    // the entry at which it is reached
+    uint64_t carry = above;
+    for (int i0 = 0; i0 < n; i0 += THREADS) {
+      const int i = i0 + threadIdx.x;
+      const uint64_t own = i >= n ? 0 : by_count ? 1 : (uint64_t)weight(entry_logit(sh.list[i]));
+      uint64_t to;
+      const uint64_t all = block_sum(own, (i0 / THREADS) & 1, &to);
+      to += carry;
+      if (i < n && reached(to) && (to == own || !reached(to - own))) sh.found[0] = sh.list[i];
+      carry += all;
+    }
+    lds_barrier();
+    const uint64_t e = sh.found[0];
+    lds_barrier();
+    b->value = entry_logit(e);
+    b->last = (int)~(uint32_t)e;
+  }
+
+};
+
+// top-k up to which a list is tried at once: of 1024 threads' maxima the k-th leaves about
+// -1024 ln(1 - k / 1024) tokens, 904 at 600
+template <int THREADS>
+constexpr int kListK = THREADS * 600 / 1024;
+
+template <typename T, int THREADS, int NV>
+__global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
+  typedef SampleRow<T, THREADS, NV> Row;
+  constexpr int E = Row::E, WAVES = THREADS / 64;
+  __shared__ SampleShared<THREADS> sh;
   const int64_t r = blockIdx.x;
-  SampleRow<T> s{LogitRow<T>(reinterpret_cast<const T*>(a.logits) + r * a.stride, (int)a.V), sums, weights, counts, found};
-  constexpr int E = SampleRow<T>::E;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const T* start = reinterpret_cast<const T*>(a.logits) + r * a.stride;
+  const int lead = (int)((reinterpret_cast<uintptr_t>(start) & 15) / sizeof(T));
+  const int cw = ((lead + (int)a.V + E - 1) / E + THREADS - 1) / THREADS;
+  Row s(typename Row::Shape{sh, start - lead, lead, (int)a.V, cw, false, 0.0, 0.0});
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+    if (u < s.cw) s.v[u] = s.load(s.piece(u));
   const float t = a.temperature ? a.temperature[r] : a.temperature_value;
   const int32_t k = a.top_k ? a.top_k[r] : a.top_k_value;
-  const float p = a.top_p ? a.top_p[r] : a.top_p_value, m = a.min_p ? a.min_p[r] : a.min_p_value, u = a.u[r];
+  const float p = a.top_p ? a.top_p[r] : a.top_p_value, m = a.min_p ? a.min_p[r] : a.min_p_value, share = a.u[r];
 
-  uint64_t best = 0;  // the largest logit's image above the complement of its first index
-  for (int j = threadIdx.x; j < s.row.pieces; j += kSampleThreads) {
-    uint32_t key[E];
-    s.row.keys(j, key);
+  // the largest and smallest logit (NaN aside)
+  float most = -INFINITY, least = INFINITY;
+  s.each([&](typename Row::vec x, int) {
+    most = fmaxf(most, Row::largest(x));
+    least = fminf(least, -Row::largest(-x));
+  });
+  sh.maxima[tid] = most > -INFINITY ? logit_key(most) : 0u;
+  float hi = most, lo = least;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const uint64_t c = (uint64_t)key[e] << 32 | (uint32_t)~(j * E - s.row.lead + e);
-      best = key[e] != 0 && c > best ? c : best;
-    }
-  }
   for (int d = 32; d >= 1; d /= 2) {
-    const uint64_t o = shfl64(best, (threadIdx.x & 63) ^ d);
-    best = o > best ? o : best;
+    hi = fmaxf(hi, __shfl_xor(hi, d, kWave));
+    lo = fminf(lo, __shfl_xor(lo, d, kWave));
   }
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = best;
-  __syncthreads();
-  for (int i = 0; i < kSampleWaves; ++i) best = part[i] > best ? part[i] : best;
+  if ((tid & 63) == 0) {
+    sh.most[0][wave] = hi;
+    sh.most[1][wave] = lo;
+  }
+  for (int i = tid; i < kExpTable; i += THREADS) sh.table[i] = exp2((double)i / kExpTable);
+  lds_barrier();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    hi = fmaxf(hi, sh.most[0][w]);
+    lo = fminf(lo, sh.most[1][w]);
+  }
 
-  const uint32_t top_key = (uint32_t)(best >> 32);
-  const int first = (int)~(uint32_t)best;
-  if (best == 0 || !(t > 0.f)) {
-    if (threadIdx.x == 0) {
-      a.tokens[r] = best == 0 ? -1 : first;
-      if (a.probs) a.probs[r] = best == 0 ? 0.f : 1.f;
+  int token = -1;
+  float prob = 0.f;
+  if (hi > -INFINITY) {
+    if (!(t > 0.f) || k == 1 || p <= 0.f || m > 1.f) {  // the first in order alone
+      if (tid == 0) sh.n = 0x7FFFFFFF;
+      lds_barrier();
+      s.each([&](typename Row::vec x, int j) {
+        if (Row::largest(x) == hi)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if ((float)x[e] == hi) atomicMin(&sh.n, j * E - s.lead + e);
+      });
+      lds_barrier();
+      token = sh.n;
+      prob = 1.f;
+    } else {
+      if (hi == INFINITY) {
+        s.infinite = true;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+          if (u < s.cw) s.v[u] = s.load(s.piece(u));
+        sh.maxima[tid] = most == INFINITY ? logit_key(0.f) : 0u;
+        lds_barrier();
+        hi = 0.f;
+        lo = -INFINITY;
+      }
+      s.top = (double)hi;
+      s.rate = fmin(kExpRate / (double)t, 1e300);
+      const double low = m > 0.f ? (double)m * kWeightOne : 0.0;
+      const bool ranked = k >= 1 && k < a.V, shared_out = p < 1.f;
+      int n = kList + 1;
+      if (ranked && k <= kListK<THREADS>) n = s.template gather<true>(s.reached_by(k), [](float, int) { return true; });
+      else if (!shared_out && low > 0.0)  // w >= m is l >= hi + t ln m, here a little less
+        n = s.template gather<true>(fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY), [&](float l, int) { return s.weight(l) >= low; });
+      if (n <= kList) {
+        s.sort(n);
+        const int kept = s.kept_of_list(n, k, p, low);
+        token = s.choose_of_list(kept, share, &prob);
+      } else {
+        Border b{-INFINITY, 0x7FFFFFFF};
+        // logits whose weights are not 0: from hi down to -31 t, or to the smallest there is
+        const float range = fminf(31.f * t, hi - lo);
+#pragma unroll 1
+        for (int by_weight = ranked ? 0 : 1; by_weight <= (shared_out ? 1 : 0); ++by_weight)
+          s.cut(&b, by_weight ? 0 : (uint64_t)k, p, range);
+        token = s.choose_of_row(b, low, share, &prob);
+      }
     }
-    return;
   }
-  const Weigher weigher{(double)key_logit(top_key), 1.0 / (double)t, key_logit(top_key)};
-  Border b{0u, 0x7FFFFFFF};
-  if (k >= 1 && k < a.V) s.cut(&b, weigher, (uint64_t)k, 0.0);
-  if (p < 1.f) {
-    const uint64_t all = s.chunk_sums([&](uint32_t key, int i) -> uint64_t { return b.keeps(key, i) ? fixed(weigher(key)) : 0; });
-    __syncthreads();
-    s.cut(&b, weigher, 0, (double)p * (double)all);
-  }
-  const double low = m > 0.f ? (double)m : 0.0;
-  auto amount = [&](uint32_t key, int i) -> uint64_t {
-    if (!b.keeps(key, i)) return 0;
-    const double w = weigher(key);
-    return w >= low || i == first ? fixed(w) : 0;
-  };
-  const uint64_t total = s.chunk_sums(amount);
-  const double at = (u > 0.f ? (double)u : 0.0) * (double)total;
-  const uint64_t target = at < (double)total ? (uint64_t)at : total - 1;
-  uint32_t key;
-  const int token = s.locate(target < total ? target : total - 1, amount, &key);
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     a.tokens[r] = token;
-    if (a.probs) a.probs[r] = (float)(weigher(key) * kWeightOne / (double)total);
+    if (a.probs) a.probs[r] = prob;
   }
 }
 
 size_t sample_workspace(int64_t, int64_t, int) { return 0; }
 
+template <typename T>
+static void sample_launch(const SampleArgs& a, int64_t B, hipStream_t st) {
+  const int64_t pieces = (a.V + 2 * (16 / sizeof(T)) - 2) / (16 / sizeof(T));  // with any lead
+  const dim3 grid((unsigned)B);
+  if (pieces <= 256) sample_kernel<T, 256, 1><<<grid, dim3(256), 0, st>>>(a);
+  else if (pieces <= 1024) sample_kernel<T, 256, 4><<<grid, dim3(256), 0, st>>>(a);
+  else if (pieces <= 4096) sample_kernel<T, 1024, 4><<<grid, dim3(1024), 0, st>>>(a);
+  else if (pieces <= 8192) sample_kernel<T, 1024, 8><<<grid, dim3(1024), 0, st>>>(a);
+  else sample_kernel<T, 1024, 16><<<grid, dim3(1024), 0, st>>>(a);
+}
+
 hipError_t launch_sample(const SampleArgs& a, int logit_bytes, int64_t B, hipStream_t st) {
-  const int per = 64 * 16 / logit_bytes;  // elements of a chunk
-  const size_t lds = (size_t)((a.V + 16 + per - 1) / per) * sizeof(uint64_t);
-  const dim3 grid((unsigned)B), block(kSampleThreads);
-  if (logit_bytes == 2) sample_kernel<f16><<<grid, block, lds, st>>>(a);
-  else sample_kernel<float><<<grid, block, lds, st>>>(a);
+  if (logit_bytes == 2) sample_launch<f16>(a, B, st);
+  else sample_launch<float>(a, B, st);
   return hipGetLastError();
 }
 
