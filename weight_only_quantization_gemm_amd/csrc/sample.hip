@@ -1,13 +1,13 @@
 // The next token of each row of logits: temperature, top-k, top-p and min-p, and
 // the choice by a given random number, without sorting the row.
 //
-// One block takes one row and keeps it in registers (16-byte pieces, up to 16 a
-// thread; what is beyond is read again from the caches).  What is kept is always a
-// first part of the tokens in order (logit descending, then index), so all that
-// has to be found is its border:
+// One block takes one row.  A first pass finds the largest logit and leaves each
+// thread the largest of its 16-byte pieces, so later steps read again only what
+// they need.  What is kept is always a first part of the tokens in order (logit
+// descending, then index), so all that has to be found is its border:
 //   few tokens kept (top-k up to kListK, or min-p alone): a logit that at least k
-//   tokens reach, from the threads' own maxima, leaves a list short enough to sort;
-//   otherwise: a histogram of the weights (and counts) over equal steps of the
+//   threads' own maxima reach leaves a list short enough to sort;
+//   otherwise: a histogram of the weights (or counts) over equal steps of the
 //   logit finds the border's bin, whose tokens are then sorted.  A bin with more
 //   tokens than the list holds (ties) is searched digit by digit instead.
 // The choice walks sums in index order: over the list where it holds all that is
@@ -22,8 +22,22 @@
 namespace awq {
 
 constexpr double kWeightOne = 8796093022208.0;  // 2^43
-constexpr int kBins = 2048, kList = 2048, kExpTable = 512;
+constexpr int kBins = 2048, kList = 2048, kExpTable = 512, kSlots = 16;
 constexpr double kExpRate = 738.6598609351493;  // kExpTable log2(e)
+
+// 2^(43 + j / kExpTable), by the series of the exponential
+struct ExpTable {
+  double at[kExpTable];
+  constexpr ExpTable() : at() {
+    for (int j = 0; j < kExpTable; ++j) {
+      const double x = 0.69314718055994530942 * j / kExpTable;
+      double sum = 1.0, term = 1.0;
+      for (int i = 1; i < 24; ++i) sum += term *= x / i;
+      at[j] = kWeightOne * sum;
+    }
+  }
+};
+__device__ constexpr ExpTable kExp;
 
 // Order-preserving image of a logit (never 0 for one that can be chosen: not -inf, not NaN).
 __device__ __forceinline__ uint32_t logit_key(float v) {
@@ -56,10 +70,9 @@ __device__ __forceinline__ uint64_t lane64(uint64_t v, int lane) {
 
 template <int THREADS>
 struct SampleShared {
-  uint64_t list[kList];      // entries, or the bins' weights
-  uint32_t counts[kBins];    // the bins' counts
-  double table[kExpTable];   // 2^(j / kExpTable)
-  uint32_t maxima[THREADS];  // images of the threads' largest logits
+  uint64_t list[kList];     // entries, or the bins' weights
+  uint32_t counts[kBins];   // the bins' counts, or candidates
+  double table[kExpTable];  // kExp
   uint64_t part[2][THREADS / 64];
   uint64_t found[4];
   float most[2][THREADS / 64];
@@ -73,24 +86,25 @@ struct Border {
   __device__ __forceinline__ bool keeps(float x, int i) const { return x > value || (x == value && i <= last); }
 };
 
-// A row, without the pieces its threads hold.
 template <typename T, int THREADS>
-struct SampleShape {
+struct SampleRow {
   static constexpr int E = 16 / sizeof(T), WAVES = THREADS / 64;
   typedef T vec __attribute__((ext_vector_type(E)));
   SampleShared<THREADS>& sh;
   const T* base;  // 16-byte aligned, lead elements before the row
-  int lead, V, cw;  // cw: chunks (64 pieces) of a wave; wave w has chunks w cw .. w cw + cw - 1
-  bool infinite;    // some logit is +inf: those weigh 1 and all others nothing
-  double top, rate; // largest logit, kExpTable log2(e) / temperature
+  int lead, V, cw;   // cw: chunks (64 pieces) of a wave; wave w has chunks w cw .. w cw + cw - 1
+  bool infinite;     // some logit is +inf: those weigh 1 and all others nothing
+  double top, rate;  // largest logit, kExpTable log2(e) / temperature
 
   // Piece j: elements j E - lead .. + E - 1, NaN outside the row.
+  __device__ __forceinline__ bool whole(int j) const { return j * E >= lead && (j + 1) * E - lead <= V; }
+  __device__ __forceinline__ vec load_whole(int j) const { return *reinterpret_cast<const vec*>(base + (int64_t)j * E); }
   __device__ __forceinline__ vec load(int j) const {
-    const int first = j * E - lead;
     vec x;
-    if (first >= 0 && first + E <= V) {
-      x = *reinterpret_cast<const vec*>(base + (int64_t)j * E);
+    if (whole(j)) {
+      x = load_whole(j);
     } else {
+      const int first = j * E - lead;
 #pragma unroll
       for (int e = 0; e < E; ++e)
         x[e] = first + e >= 0 && first + e < V ? base[(int64_t)j * E + e] : (T)__builtin_nanf("");
@@ -110,28 +124,50 @@ struct SampleShape {
       return fmaxf(fmaxf((float)x[0], (float)x[1]), fmaxf((float)x[2], (float)x[3]));
     }
   }
+  // f(piece, its number) for this thread's pieces, four read at a time and the next four under way
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    vec next[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < cw) next[q] = load(piece(q));
+#pragma unroll 1
+    for (int u = 0; u < cw; u += 4) {
+      vec x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] = next[q];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (u + 4 + q < cw) next[q] = load(piece(u + 4 + q));
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (u + q < cw) f(x[q], piece(u + q));
+    }
+  }
 
-  // The weight times 2^43, rounded to a whole number: exp(z) = 2^(i / 512) (1 + g), g = exp(f ln2 / 512)
-  // - 1 to the third power of f, |f| <= 1/2 (the fourth is below 2^-46).  Below z = -31 it is none.
+  // The weight times 2^43, rounded to a whole number: with y = z 512 / ln 2 = i + f, i whole,
+  //   exp(z) = 2^(i / 512) (1 + g),  g = exp(f ln2 / 512) - 1 to the third power of f, |f| <= 1/2
+  // (the fourth is below 2^-46).  Below z = -31 it is none, and for a NaN.  Whole parts are split off
+  // by adding and subtracting 1.5 2^52 and 2^52.
+  __device__ __forceinline__ double unrounded(float x, double c3 = 4.1353783506767136e-10) const {
+    constexpr double c1 = 0.0013538030870311431, c2 = 9.163913992275265e-07;  // (ln2/512)^n / n!
+    constexpr double kWhole = 6755399441055744.0;
+    const double y = fmax(((double)x - top) * rate, -31.0 * kExpRate);
+    const double shifted = y + kWhole, f = y - (shifted - kWhole);
+    const int i = (int)(uint32_t)__double_as_longlong(shifted);
+    const uint64_t t = (uint64_t)__double_as_longlong(sh.table[i & (kExpTable - 1)]);
+    const double two = __longlong_as_double((int64_t)(t + ((uint64_t)(uint32_t)((i & -kExpTable) << (20 - 9)) << 32)));
+    return fma(two, f * fma(f, fma(f, c3, c2), c1), two);
+  }
   __device__ __forceinline__ double weight(float x) const {
-    constexpr double c1 = 0.0013538030870311431, c2 = 9.163913992275265e-07, c3 = 4.1353783506767136e-10;  // (ln2/512)^n / n!
-    constexpr double least = -31.0 * kExpRate;
-    const double y = fmax(((double)x - top) * rate, least);  // `least` for a NaN too
-    const double n = rint(y), f = y - n;
-    const int i = (int)n;
-    const double t = sh.table[i & (kExpTable - 1)];
-    const double g = f * fma(f, fma(f, c3, c2), c1);
-    return rint(ldexp(fma(t, g, t), (i >> 9) + 43));
+    constexpr double kHalfUnit = 4503599627370496.0;  // 2^52, where a double's spacing is 1
+    return (unrounded(x) + kHalfUnit) - kHalfUnit;
   }
 
   __device__ __forceinline__ uint64_t target_of(float share, uint64_t total) const {
     const double at = (share > 0.f ? (double)share : 0.0) * (double)total;
     const uint64_t target = at < (double)total ? (uint64_t)at : total - 1;
     return target < total ? target : total - 1;
-  }
-  // the weight times 2^43 before its rounding
-  __device__ __forceinline__ double exact_weight(float x) const {
-    return (double)x == top ? kWeightOne : kWeightOne * exp(fmax(((double)x - top) * rate, -31.0 * kExpRate) / kExpRate);
   }
 
   // Sum over the block; inclusive sums up to this thread in *upto where asked for.
@@ -149,8 +185,11 @@ struct SampleShape {
     return all;
   }
 
+  static __device__ __forceinline__ uint64_t entry(float x, int i) { return (uint64_t)logit_key(x) << 32 | (uint32_t)~i; }
+  static __device__ __forceinline__ float entry_logit(uint64_t e) { return key_logit((uint32_t)(e >> 32)); }
+
   // Sorts list[0 .. n) descending (n <= kList; entries up to the next power of two become 0).
-  __device__ __forceinline__ void sort(int n) {
+  __device__ void sort(int n) const {
     int size = 2;
     while (size < n) size *= 2;
     for (int i = n + threadIdx.x; i < size; i += THREADS) sh.list[i] = 0;
@@ -173,14 +212,241 @@ struct SampleShape {
     }
     lds_barrier();
   }
-  static __device__ __forceinline__ uint64_t entry(float x, int i) { return (uint64_t)logit_key(x) << 32 | (uint32_t)~i; }
-  static __device__ __forceinline__ float entry_logit(uint64_t e) { return key_logit((uint32_t)(e >> 32)); }
 
-  // SampleRow::cut digit by digit over the logits' images, for many tokens of nearly one logit.
-  static __device__ __noinline__ Border cut_by_digits(const SampleShape s, const Border old, uint64_t rank_at, double least) {
-    return s.digits(old, rank_at, least);
+  // list = the tokens that reach `least` and pass `also`, in any order, and returns their number (more
+  // than kList: only some are in the list).  most: the largest logits of this thread's slots (slot q:
+  // pieces q, q + kSlots, .. of it), and of its edge piece.
+  template <typename F>
+  __device__ __forceinline__ int gather(const float (&most)[kSlots], float edge, int edge_piece, float least, F also) const {
+    uint32_t slots = edge >= least && edge > -INFINITY ? 1u << kSlots : 0u;
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) slots |= most[q] >= least && most[q] > -INFINITY ? 1u << q : 0u;
+    if (threadIdx.x == 0) {
+      sh.n = 0;
+      sh.found[0] = 0;
+    }
+    lds_barrier();
+    while (slots != 0) {
+      const int q = __builtin_ctz(slots);
+      slots &= slots - 1;
+      const int at = atomicAdd(reinterpret_cast<int*>(&sh.found[0]), 1);
+      if (at < kBins) sh.counts[at] = q == kSlots ? ~(uint32_t)edge_piece : (uint32_t)piece(q);
+    }
+    lds_barrier();
+    const int slots_found = (int)(uint32_t)sh.found[0];
+    if (slots_found > kBins) {
+      lds_barrier();
+      return kList + 1;
+    }
+    for (int s = threadIdx.x; s < slots_found; s += THREADS) {
+      const uint32_t c = sh.counts[s];
+      const bool is_edge = (int32_t)c < 0;
+      // pieces of a slot are kSlots chunks apart, within its wave's chunks
+      const int j0 = is_edge ? (int)~c : (int)c, end = is_edge ? j0 + 1 : ((j0 / 64) / cw + 1) * cw * 64;
+      for (int j = j0; j < end; j += kSlots * 64) {
+        if (!is_edge && !whole(j)) continue;  // an edge piece is its own slot
+        const vec x = load(j);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float l = (float)x[e];
+          const int i = j * E - lead + e;
+          if (l >= least && l > -INFINITY && also(l, i)) {
+            const int at = atomicAdd(&sh.n, 1);
+            if (at < kList) sh.list[at] = entry(l, i);
+          }
+        }
+      }
+    }
+    lds_barrier();
+    const int n = __builtin_amdgcn_readfirstlane(sh.n);
+    lds_barrier();
+    return n;
   }
-  __device__ __forceinline__ Border digits(const Border old, uint64_t rank_at, double least) const {
+
+  // A logit that at least k tokens reach (-inf: all of them): the threads' largest logits counted over
+  // equal steps from hi down by `range`, the smallest of them in the steps that hold the first k.
+  __device__ __forceinline__ float reached_by(int k, float mine, float hi, float range) const {
+    constexpr int STEPS = 256;
+    const float step = fminf((float)STEPS / range, 1e30f);
+    const int bin = (int)fminf((hi - mine) * step, (float)(STEPS - 1));
+    if (threadIdx.x < STEPS) sh.counts[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sh.found[0] = STEPS;
+    lds_barrier();
+    if (mine > -INFINITY) atomicAdd(&sh.counts[bin], 1u);
+    lds_barrier();
+    if (threadIdx.x < 64) {
+      int count[4], sum = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum += count[q] = (int)sh.counts[4 * threadIdx.x + q];
+      int before = wave_scan(sum) - sum;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (before < k && before + count[q] >= k) sh.found[0] = 4 * threadIdx.x + q;
+        before += count[q];
+      }
+    }
+    lds_barrier();
+    const int last = (int)sh.found[0];
+    float least = mine > -INFINITY && bin <= last ? mine : INFINITY;
+#pragma unroll
+    for (int d = 32; d >= 1; d /= 2) least = fminf(least, __shfl_xor(least, d, kWave));
+    if ((threadIdx.x & 63) == 0) sh.most[0][threadIdx.x >> 6] = least;
+    lds_barrier();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) least = fminf(least, sh.most[0][w]);
+    return last == STEPS ? -INFINITY : least;
+  }
+
+  // The token at `share` of the up to 64 entries of the list, by the first wave alone.
+  __device__ __forceinline__ int choose_of_few(int n, int k, float p, double low, float share, float* prob) const {
+    if (threadIdx.x < 64) {
+      const int lane = threadIdx.x;
+      uint64_t e = lane < n ? sh.list[lane] : 0;
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += lane64(e, j) > e ? 1 : 0;
+      if (lane < n) sh.list[rank] = e;  // distinct: their indices are
+      __asm__ volatile("" ::: "memory");
+      e = lane < n ? sh.list[lane] : 0;
+      if (k >= 1 && k < n) n = k;
+      const double exact = lane < n ? unrounded(entry_logit(e)) : 0.0;
+      const uint64_t w = lane < n ? (uint64_t)weight(entry_logit(e)) : 0;
+      const uint64_t upto = scan64(w);
+      const double least = (double)p * (double)lane64(upto, 63);
+      const bool in = lane < n && (lane == 0 || ((p >= 1.f || (double)(upto - w) < least) && (double)w >= low));
+      const int kept = __popcll(__ballot(in));
+      const uint64_t total = lane64(upto, kept - 1), target = target_of(share, total);
+      uint64_t sum = 0;  // of the kept tokens up to this one, by index
+      for (int j = 0; j < kept; ++j) {
+        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e, j);
+        sum += other >= (uint32_t)e ? lane64(w, j) : 0;  // complements of the indices
+      }
+      if (lane < kept && sum > target && sum - w <= target) {
+        sh.found[0] = (uint32_t)e;
+        sh.found[1] = (uint64_t)__double_as_longlong(exact / (double)total);
+      }
+    }
+    lds_barrier();
+    *prob = (float)__longlong_as_double((int64_t)sh.found[1]);
+    return (int)~(uint32_t)sh.found[0];
+  }
+
+  // Of the sorted list's first n entries, how many are kept.
+  __device__ __forceinline__ int kept_of_list(int n, int k, float p, double low) const {
+    constexpr int Q = kList / THREADS;
+    if (k >= 1 && k < n) n = k;
+    double w[Q];
+    uint64_t upto[Q], carry = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = q * THREADS + threadIdx.x;
+      w[q] = 0.0;
+      upto[q] = 0;
+      if (q * THREADS < n) {
+        w[q] = i < n ? weight(entry_logit(sh.list[i])) : 0.0;
+        const uint64_t all = block_sum((uint64_t)w[q], q & 1, &upto[q]);
+        upto[q] += carry;
+        carry += all;
+      }
+    }
+    const double least = (double)p * (double)carry;
+    uint64_t kept = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = q * THREADS + threadIdx.x;
+      const bool in = i < n && (p >= 1.f || (double)(upto[q] - (uint64_t)w[q]) < least) && w[q] >= low;
+      kept += i == 0 || in ? 1 : 0;
+    }
+    lds_barrier();
+    return (int)block_sum(kept, 0);
+  }
+
+  // The token at `share` of the first n entries of the list.
+  __device__ __forceinline__ int choose_of_list(int n, float share, float* prob) const {
+    constexpr int Q = kList / THREADS;
+    lds_barrier();
+    for (int i = threadIdx.x; i < n; i += THREADS) sh.list[i] = sh.list[i] << 32 | sh.list[i] >> 32;  // by index
+    lds_barrier();
+    sort(n);
+    uint64_t w[Q], upto[Q], total = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = q * THREADS + threadIdx.x;
+      w[q] = upto[q] = 0;
+      if (q * THREADS < n) {
+        w[q] = i < n ? (uint64_t)weight(key_logit((uint32_t)sh.list[i])) : 0;
+        const uint64_t all = block_sum(w[q], q & 1, &upto[q]);
+        upto[q] += total;
+        total += all;
+      }
+    }
+    const uint64_t target = target_of(share, total);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (upto[q] > target && upto[q] - w[q] <= target) sh.found[0] = sh.list[q * THREADS + threadIdx.x];
+    lds_barrier();
+    const uint64_t e = sh.found[0];
+    *prob = (float)(unrounded(key_logit((uint32_t)e)) / (double)total);
+    return (int)~(uint32_t)(e >> 32);
+  }
+
+  // The token at `share` of all that b keeps with weights from low on.
+  __device__ __forceinline__ int choose_of_row(const Border& b, double low, float share, float* prob) const {
+    auto amount = [&](vec x, int j) {
+      double s = 0.0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float l = (float)x[e];
+        const double w = weight(l);
+        s += b.keeps(l, j * E - lead + e) && w >= low ? w : 0.0;
+      }
+      return s;
+    };
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double mine = 0.0;
+    each([&](vec x, int j) { mine += amount(x, j); });
+    lds_barrier();
+    const uint64_t total = block_sum((uint64_t)mine, 0);
+    uint64_t target = target_of(share, total);
+    // the wave, then its chunk, then the lane and its element
+    int w = 0;
+    while (w < WAVES - 1 && sh.part[0][w] <= target) target -= sh.part[0][w++];
+    for (int u = wave; u < cw; u += WAVES) {
+      const int j = (w * cw + u) * 64 + lane;
+      const uint64_t s = scan64((uint64_t)amount(load(j), j));
+      if (lane == 63) sh.list[u] = s;
+    }
+    lds_barrier();
+    if (wave == 0) {
+      int u = 0;
+      while (u < cw - 1 && sh.list[u] <= target) target -= sh.list[u++];
+      const int j = (w * cw + u) * 64 + lane;
+      const vec x = load(j);
+      const uint64_t own = (uint64_t)amount(x, j), upto = scan64(own);
+      const uint64_t over = __ballot(upto > target);
+      if (lane == __builtin_ctzll(over)) {
+        uint64_t sum = upto - own;
+        bool done = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float l = (float)x[e];
+          const int i = j * E - lead + e;
+          const double we = weight(l);
+          sum += b.keeps(l, i) && we >= low ? (uint64_t)we : 0;
+          if (!done && sum > target) {
+            done = true;
+            sh.found[0] = entry(l, i);
+          }
+        }
+      }
+    }
+    lds_barrier();
+    const uint64_t e = sh.found[0];
+    *prob = (float)(unrounded(entry_logit(e)) / (double)total);
+    return (int)~(uint32_t)e;
+  }
+
+  // cut() digit by digit over the logits' images, for many tokens of nearly one logit.
+  __device__ __noinline__ Border digits(const Border old, uint64_t rank_at, double least) const {
     Border b = old;
     const bool by_count = rank_at > 0;
     uint32_t prefix = 0;
@@ -279,227 +545,10 @@ struct SampleShape {
     lds_barrier();
     return b;
   }
-};
-
-template <typename T, int THREADS, int NV>
-struct SampleRow : SampleShape<T, THREADS> {
-  typedef SampleShape<T, THREADS> Shape;
-  using typename Shape::vec;
-  using Shape::E, Shape::WAVES, Shape::sh, Shape::lead, Shape::cw, Shape::top;
-  using Shape::load, Shape::piece, Shape::weight, Shape::block_sum, Shape::sort, Shape::largest, Shape::entry,
-      Shape::entry_logit, Shape::target_of, Shape::exact_weight;
-  vec v[NV];  // this thread's pieces of the first NV chunks of its wave
-  __device__ explicit SampleRow(const Shape& shape) : Shape(shape) {}
-
-  // f(piece, its number) for this thread's pieces, of those held and those that are not.  Only for what
-  // takes few registers beside them.  The empty asm hides that every pass sees the same values and
-  // indices: what one pass makes of them would otherwise be kept in registers for the next.
-  template <typename F>
-  __device__ __forceinline__ void each(F f) {
-#pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (u < cw) {
-        int j = piece(u);
-        __asm__ volatile("" : "+v"(v[u]), "+v"(j));
-        f(v[u], j);
-      }
-    for (int u = NV; u < cw; ++u) f(load(piece(u)), piece(u));
-  }
-  // The same with all pieces read again (from the caches), the next one under way.
-  template <typename F>
-  __device__ __forceinline__ void each_again(F f) const {
-    vec next = load(piece(0));
-#pragma unroll 1
-    for (int u = 0; u < cw; ++u) {
-      const vec x = next;
-      if (u + 1 < cw) next = load(piece(u + 1));
-      f(x, piece(u));
-    }
-  }
-
-  // list = the tokens that reach `least` and pass `also`, in any order; their number (more than
-  // kList: only some are in the list).
-  template <bool HELD, typename F>
-  __device__ __forceinline__ int gather(float least, F also) {
-    if (threadIdx.x == 0) sh.n = 0;
-    lds_barrier();
-    auto put = [&](vec x, int j) {
-      if (largest(x) >= least)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float l = (float)x[e];
-          const int i = j * E - lead + e;
-          if (l >= least && l > -INFINITY && also(l, i)) {
-            const int at = atomicAdd(&sh.n, 1);
-            if (at < kList) sh.list[at] = entry(l, i);
-          }
-        }
-    };
-    if constexpr (HELD) each(put);
-    else each_again(put);
-    lds_barrier();
-    const int n = sh.n;
-    lds_barrier();
-    return n;
-  }
-
-  // A logit that at least k tokens reach (k <= THREADS), the smallest live one if the threads with a
-  // live logit are fewer: by halving the range of the threads' maxima until few more than k remain.
-  __device__ __forceinline__ float reached_by(int k) {
-    if (threadIdx.x < 64) {
-      uint32_t key[WAVES], lo = ~0u, hi = 0u;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) {
-        key[w] = sh.maxima[w * 64 + threadIdx.x];
-        lo = key[w] < lo ? key[w] : lo;
-        hi = key[w] > hi ? key[w] : hi;
-      }
-#pragma unroll
-      for (int d = 32; d >= 1; d /= 2) {
-        const uint32_t l = (uint32_t)__shfl_xor((int)lo, d, kWave), h = (uint32_t)__shfl_xor((int)hi, d, kWave);
-        lo = l < lo ? l : lo;
-        hi = h > hi ? h : hi;
-      }
-      lo = lo > 0 ? lo : 1u;
-      // at least k maxima reach lo, unless lo is 1
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo + 1) / 2;
-        int count = 0;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) count += __popcll(__ballot(key[w] >= mid));
-        if (count >= k) {
-          lo = mid;
-          if (count <= k + k / 8 + 4) break;
-        } else {
-          hi = mid - 1;
-        }
-      }
-      if (threadIdx.x == 0) sh.found[0] = lo;
-    }
-    lds_barrier();
-    const uint32_t lo = (uint32_t)sh.found[0];
-    lds_barrier();
-    return lo <= 1u ? -INFINITY : key_logit(lo);
-  }
-
-  // Of the sorted list's first n entries, how many are kept.
-  __device__ __forceinline__ int kept_of_list(int n, int k, float p, double low) {
-    constexpr int Q = kList / THREADS;
-    if (k >= 1 && k < n) n = k;
-    double w[Q];
-    uint64_t upto[Q], carry = 0;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int i = q * THREADS + threadIdx.x;
-      w[q] = 0.0;
-      upto[q] = 0;
-      if (q * THREADS < n) {
-        w[q] = i < n ? weight(entry_logit(sh.list[i])) : 0.0;
-        const uint64_t all = block_sum((uint64_t)w[q], q & 1, &upto[q]);
-        upto[q] += carry;
-        carry += all;
-      }
-    }
-    const double least = (double)p * (double)carry;
-    uint64_t kept = 0;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int i = q * THREADS + threadIdx.x;
-      const bool in = i < n && (p >= 1.f || (double)(upto[q] - (uint64_t)w[q]) < least) && w[q] >= low;
-      kept += i == 0 || in ? 1 : 0;
-    }
-    lds_barrier();
-    return (int)block_sum(kept, 0);
-  }
-
-  // The token at `share` of the first n entries of the list; its probability.
-  __device__ __forceinline__ int choose_of_list(int n, float share, float* prob) {
-    constexpr int Q = kList / THREADS;
-    lds_barrier();
-    for (int i = threadIdx.x; i < n; i += THREADS) sh.list[i] = sh.list[i] << 32 | sh.list[i] >> 32;  // by index
-    lds_barrier();
-    sort(n);
-    uint64_t w[Q], upto[Q], total = 0;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int i = q * THREADS + threadIdx.x;
-      w[q] = upto[q] = 0;
-      if (q * THREADS < n) {
-        w[q] = i < n ? (uint64_t)weight(key_logit((uint32_t)sh.list[i])) : 0;
-        const uint64_t all = block_sum(w[q], q & 1, &upto[q]);
-        upto[q] += total;
-        total += all;
-      }
-    }
-    const uint64_t target = target_of(share, total);
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if (upto[q] > target && upto[q] - w[q] <= target) sh.found[0] = sh.list[q * THREADS + threadIdx.x];
-    lds_barrier();
-    const uint64_t e = sh.found[0];
-    *prob = (float)(exact_weight(key_logit((uint32_t)e)) / (double)total);
-    return (int)~(uint32_t)(e >> 32);
-  }
-  // The token at `share` of all that b keeps with weights from low on.
-  __device__ __forceinline__ int choose_of_row(const Border& b, double low, float share, float* prob) {
-    auto amount = [&](vec x, int j) {
-      double s = 0.0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float l = (float)x[e];
-        const double w = weight(l);
-        s += b.keeps(l, j * E - lead + e) && w >= low ? w : 0.0;
-      }
-      return s;
-    };
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double mine = 0.0;
-    each_again([&](vec x, int j) { mine += amount(x, j); });
-    lds_barrier();
-    const uint64_t total = block_sum((uint64_t)mine, 0);
-    uint64_t target = target_of(share, total);
-    // the wave, then its chunk, then the lane and its element
-    int w = 0;
-    while (w < WAVES - 1 && sh.part[0][w] <= target) target -= sh.part[0][w++];
-    lds_barrier();
-    for (int u = wave; u < cw; u += WAVES) {
-      const int j = (w * cw + u) * 64 + lane;
-      const uint64_t s = scan64((uint64_t)amount(load(j), j));
-      if (lane == 63) sh.list[u] = s;
-    }
-    lds_barrier();
-    if (wave == 0) {
-      int u = 0;
-      while (u < cw - 1 && sh.list[u] <= target) target -= sh.list[u++];
-      const int j = (w * cw + u) * 64 + lane;
-      const vec x = load(j);
-      const uint64_t own = (uint64_t)amount(x, j), upto = scan64(own);
-      const uint64_t over = __ballot(upto > target);
-      if (lane == __builtin_ctzll(over)) {
-        uint64_t sum = upto - own;
-        bool done = false;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float l = (float)x[e];
-          const int i = j * E - lead + e;
-          const double we = weight(l);
-          sum += b.keeps(l, i) && we >= low ? (uint64_t)we : 0;
-          if (!done && sum > target) {
-            done = true;
-            sh.found[0] = entry(l, i);
-          }
-        }
-      }
-    }
-    lds_barrier();
-    const uint64_t e = sh.found[0];
-    *prob = (float)(exact_weight(entry_logit(e)) / (double)total);
-    return (int)~(uint32_t)e;
-  }
 
   // Narrows b to the tokens up to the rank_at-th in order (rank_at > 0), or up to the first at which the
   // weights reach the share p of all of b's; everything stays where that is not reached.
-  __device__ __forceinline__ void cut(Border* b, uint64_t rank_at, float p, float range) {
+  __device__ __forceinline__ void cut(Border* b, uint64_t rank_at, float p, float range) const {
     constexpr int PER = kBins / THREADS;
     const bool by_count = rank_at > 0;
     const float step = fminf((float)kBins / range, 1e30f);
@@ -509,7 +558,7 @@ struct SampleRow : SampleShape<T, THREADS> {
       sh.counts[i] = 0;
     }
     lds_barrier();
-    each_again([&](vec x, int j) {
+    each([&](vec x, int j) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float l = (float)x[e];
@@ -549,9 +598,24 @@ struct SampleRow : SampleShape<T, THREADS> {
     lds_barrier();
     if (bin == kBins) return;
     const Border old = *b;
-    const int n = gather<false>(-INFINITY, [&](float l, int i) { return bin_of(l) == bin && old.keeps(l, i) && weight(l) > 0.0; });
+    if (threadIdx.x == 0) sh.n = 0;
+    lds_barrier();
+    each([&](vec x, int j) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float l = (float)x[e];
+        const int i = j * E - lead + e;
+        if (bin_of(l) == bin && old.keeps(l, i) && weight(l) > 0.0) {
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < kList) sh.list[at] = entry(l, i);
+        }
+      }
+    });
+    lds_barrier();
+    const int n = __builtin_amdgcn_readfirstlane(sh.n);
     if (n > kList) {
-      *b = Shape::cut_by_digits(*this, old, rank_at, least);  // by value: the pieces stay in registers
+      lds_barrier();
+      *b = digits(old, rank_at, least);
       return;
     }
     sort(n);
@@ -582,30 +646,55 @@ constexpr int kListK = THREADS * 600 / 1024;
 
 template <typename T, int THREADS, int NV>
 __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
-  typedef SampleRow<T, THREADS, NV> Row;
+  typedef SampleRow<T, THREADS> Row;
+  typedef typename Row::vec vec;
   constexpr int E = Row::E, WAVES = THREADS / 64;
+  static_assert(kSlots % NV == 0, "slots");
   __shared__ SampleShared<THREADS> sh;
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, wave = tid >> 6;
   const T* start = reinterpret_cast<const T*>(a.logits) + r * a.stride;
   const int lead = (int)((reinterpret_cast<uintptr_t>(start) & 15) / sizeof(T));
-  const int cw = ((lead + (int)a.V + E - 1) / E + THREADS - 1) / THREADS;
-  Row s(typename Row::Shape{sh, start - lead, lead, (int)a.V, cw, false, 0.0, 0.0});
+  const int pieces = (lead + (int)a.V + E - 1) / E, cw = (pieces + THREADS - 1) / THREADS;
+  Row s{sh, start - lead, lead, (int)a.V, cw, false, 0.0, 0.0};
+
+  // the largest logit of each slot, and the smallest of all (NaN aside); NV pieces under way
+  float slot[kSlots], lo = INFINITY;
 #pragma unroll
-  for (int u = 0; u < NV; ++u)
-    if (u < s.cw) s.v[u] = s.load(s.piece(u));
+  for (int q = 0; q < kSlots; ++q) slot[q] = -INFINITY;
+  for (int u0 = 0; u0 < cw; u0 += kSlots) {
+#pragma unroll
+    for (int h = 0; h < kSlots; h += NV) {
+      vec x[NV];
+#pragma unroll
+      for (int q = 0; q < NV; ++q) {
+        const int j = s.piece(u0 + h + q);
+        x[q] = vec{} + (T)__builtin_nanf("");
+        if (u0 + h + q < cw && s.whole(j)) x[q] = s.load_whole(j);
+      }
+#pragma unroll
+      for (int q = 0; q < NV; ++q) {
+        slot[h + q] = fmaxf(slot[h + q], Row::largest(x[q]));
+        lo = fminf(lo, -Row::largest(-x[q]));
+      }
+    }
+  }
+  // the pieces that reach out of the row, first and last, by the first two threads
+  float edge = -INFINITY;
+  const int edge_piece = tid == 0 ? 0 : pieces - 1;
+  if (tid < 2 && !s.whole(edge_piece) && (tid == 0 || pieces > 1)) {
+    const vec x = s.load(edge_piece);
+    edge = Row::largest(x);
+    lo = fminf(lo, -Row::largest(-x));
+    edge = edge > -INFINITY ? edge : -INFINITY;  // a NaN
+  }
   const float t = a.temperature ? a.temperature[r] : a.temperature_value;
   const int32_t k = a.top_k ? a.top_k[r] : a.top_k_value;
   const float p = a.top_p ? a.top_p[r] : a.top_p_value, m = a.min_p ? a.min_p[r] : a.min_p_value, share = a.u[r];
-
-  // the largest and smallest logit (NaN aside)
-  float most = -INFINITY, least = INFINITY;
-  s.each([&](typename Row::vec x, int) {
-    most = fmaxf(most, Row::largest(x));
-    least = fminf(least, -Row::largest(-x));
-  });
-  sh.maxima[tid] = most > -INFINITY ? logit_key(most) : 0u;
-  float hi = most, lo = least;
+  float mine = edge;
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) mine = fmaxf(mine, slot[q]);
+  float hi = mine;
 #pragma unroll
   for (int d = 32; d >= 1; d /= 2) {
     hi = fmaxf(hi, __shfl_xor(hi, d, kWave));
@@ -615,7 +704,8 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
     sh.most[0][wave] = hi;
     sh.most[1][wave] = lo;
   }
-  for (int i = tid; i < kExpTable; i += THREADS) sh.table[i] = exp2((double)i / kExpTable);
+  for (int i = tid; i < kExpTable; i += THREADS) sh.table[i] = kExp.at[i];
+  if (tid == 0) sh.n = 0x7FFFFFFF;
   lds_barrier();
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
@@ -625,51 +715,51 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
 
   int token = -1;
   float prob = 0.f;
-  if (hi > -INFINITY) {
-    if (!(t > 0.f) || k == 1 || p <= 0.f || m > 1.f) {  // the first in order alone
-      if (tid == 0) sh.n = 0x7FFFFFFF;
-      lds_barrier();
-      s.each([&](typename Row::vec x, int j) {
-        if (Row::largest(x) == hi)
+  if (hi == -INFINITY) {
+    // nothing to choose
+  } else if (!(t > 0.f) || k == 1 || p <= 0.f || m > 1.f) {  // the first in order alone
+    if (mine == hi) {
+      int first = 0x7FFFFFFF;
+      auto look = [&](int j) {
+        const vec x = s.load(j);
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if ((float)x[e] == hi) atomicMin(&sh.n, j * E - s.lead + e);
-      });
-      lds_barrier();
-      token = sh.n;
-      prob = 1.f;
+        for (int e = E - 1; e >= 0; --e)
+          if ((float)x[e] == hi) first = j * E - lead + e < first ? j * E - lead + e : first;
+      };
+      for (int u = 0; u < cw; ++u) look(s.piece(u));
+      if (edge == hi) look(edge_piece);
+      atomicMin(&sh.n, first);
+    }
+    lds_barrier();
+    token = sh.n;
+    prob = 1.f;
+  } else {
+    const double low = m > 0.f ? (double)m * kWeightOne : 0.0;
+    const bool ranked = k >= 1 && k < a.V, cut_by_share = p < 1.f;
+    s.infinite = hi == INFINITY;
+    s.top = s.infinite ? 0.0 : (double)hi;
+    s.rate = fmin(kExpRate / (double)t, 1e300);
+    // logits whose weights are not 0: from hi down to -31 t, or to the smallest there is
+    const float range = s.infinite ? 31.f * t : fminf(31.f * t, hi - lo);
+    int n = kList + 1;
+    if (!s.infinite) {
+      if (ranked && k <= kListK<THREADS>)
+        n = s.gather(slot, edge, edge_piece, s.reached_by(k, mine, hi, range), [](float, int) { return true; });
+      else if (!cut_by_share && low > 0.0)  // w >= m is l >= hi + t ln m, here a little less
+        n = s.gather(slot, edge, edge_piece, fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY),
+                     [&](float l, int) { return s.weight(l) >= low; });
+    }
+    if (n <= 64) {
+      token = s.choose_of_few(n, k, p, low, share, &prob);
+    } else if (n <= kList) {
+      s.sort(n);
+      token = s.choose_of_list(s.kept_of_list(n, k, p, low), share, &prob);
     } else {
-      if (hi == INFINITY) {
-        s.infinite = true;
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-          if (u < s.cw) s.v[u] = s.load(s.piece(u));
-        sh.maxima[tid] = most == INFINITY ? logit_key(0.f) : 0u;
-        lds_barrier();
-        hi = 0.f;
-        lo = -INFINITY;
-      }
-      s.top = (double)hi;
-      s.rate = fmin(kExpRate / (double)t, 1e300);
-      const double low = m > 0.f ? (double)m * kWeightOne : 0.0;
-      const bool ranked = k >= 1 && k < a.V, shared_out = p < 1.f;
-      int n = kList + 1;
-      if (ranked && k <= kListK<THREADS>) n = s.template gather<true>(s.reached_by(k), [](float, int) { return true; });
-      else if (!shared_out && low > 0.0)  // w >= m is l >= hi + t ln m, here a little less
-        n = s.template gather<true>(fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY), [&](float l, int) { return s.weight(l) >= low; });
-      if (n <= kList) {
-        s.sort(n);
-        const int kept = s.kept_of_list(n, k, p, low);
-        token = s.choose_of_list(kept, share, &prob);
-      } else {
-        Border b{-INFINITY, 0x7FFFFFFF};
-        // logits whose weights are not 0: from hi down to -31 t, or to the smallest there is
-        const float range = fminf(31.f * t, hi - lo);
+      Border b{-INFINITY, 0x7FFFFFFF};
 #pragma unroll 1
-        for (int by_weight = ranked ? 0 : 1; by_weight <= (shared_out ? 1 : 0); ++by_weight)
-          s.cut(&b, by_weight ? 0 : (uint64_t)k, p, range);
-        token = s.choose_of_row(b, low, share, &prob);
-      }
+      for (int by_weight = ranked ? 0 : 1; by_weight <= (cut_by_share ? 1 : 0); ++by_weight)
+        s.cut(&b, by_weight ? 0 : (uint64_t)k, p, range);
+      token = s.choose_of_row(b, low, share, &prob);
     }
   }
   if (tid == 0) {
@@ -684,11 +774,8 @@ template <typename T>
 static void sample_launch(const SampleArgs& a, int64_t B, hipStream_t st) {
   const int64_t pieces = (a.V + 2 * (16 / sizeof(T)) - 2) / (16 / sizeof(T));  // with any lead
   const dim3 grid((unsigned)B);
-  if (pieces <= 256) sample_kernel<T, 256, 1><<<grid, dim3(256), 0, st>>>(a);
-  else if (pieces <= 1024) sample_kernel<T, 256, 4><<<grid, dim3(256), 0, st>>>(a);
-  else if (pieces <= 4096) sample_kernel<T, 1024, 4><<<grid, dim3(1024), 0, st>>>(a);
-  else if (pieces <= 8192) sample_kernel<T, 1024, 8><<<grid, dim3(1024), 0, st>>>(a);
-  else sample_kernel<T, 1024, 16><<<grid, dim3(1024), 0, st>>>(a);
+  if (pieces <= 1024) sample_kernel<T, 256, 4><<<grid, dim3(256), 0, st>>>(a);
+  else sample_kernel<T, 1024, 8><<<grid, dim3(1024), 0, st>>>(a);
 }
 
 hipError_t launch_sample(const SampleArgs& a, int logit_bytes, int64_t B, hipStream_t st) {
