@@ -68,6 +68,22 @@ __device__ __forceinline__ uint64_t lane64(uint64_t v, int lane) {
          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32;
 }
 
+// A wave's largest (smallest) value, in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float shifted(float v, float none) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, shifted<0x111, 0xF>(v, -INFINITY));
+  v = fmaxf(v, shifted<0x112, 0xF>(v, -INFINITY));
+  v = fmaxf(v, shifted<0x114, 0xF>(v, -INFINITY));
+  v = fmaxf(v, shifted<0x118, 0xF>(v, -INFINITY));
+  v = fmaxf(v, shifted<0x142, 0xA>(v, -INFINITY));
+  v = fmaxf(v, shifted<0x143, 0xC>(v, -INFINITY));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float wave_min(float v) { return -wave_max(-v); }
+
 template <int THREADS>
 struct SampleShared {
   uint64_t list[kList];     // entries, or the bins' weights
@@ -75,7 +91,7 @@ struct SampleShared {
   double table[kExpTable];  // kExp
   uint64_t part[2][THREADS / 64];
   uint64_t found[4];
-  float most[2][THREADS / 64];
+  float most[THREADS / 64], least[THREADS / 64];
   int n;
 };
 
@@ -91,23 +107,20 @@ struct SampleRow {
   static constexpr int E = 16 / sizeof(T), WAVES = THREADS / 64;
   typedef T vec __attribute__((ext_vector_type(E)));
   SampleShared<THREADS>& sh;
-  const T* base;  // 16-byte aligned, lead elements before the row
+  __amdgpu_buffer_rsrc_t resource;  // from the 16-byte piece with the row's first element to the row's end
   int lead, V, cw;   // cw: chunks (64 pieces) of a wave; wave w has chunks w cw .. w cw + cw - 1
   bool infinite;     // some logit is +inf: those weigh 1 and all others nothing
   double top, rate;  // largest logit, kExpTable log2(e) / temperature
 
-  // Piece j: elements j E - lead .. + E - 1, NaN outside the row.
-  __device__ __forceinline__ bool whole(int j) const { return j * E >= lead && (j + 1) * E - lead <= V; }
-  __device__ __forceinline__ vec load_whole(int j) const { return *reinterpret_cast<const vec*>(base + (int64_t)j * E); }
+  // Piece j: elements j E - lead .. + E - 1, NaN outside the row.  Read with the hardware's bound at
+  // the row's end (a half's word there may hold the next half too); before the row's start there are
+  // only other rows, whose elements become NaN like those behind.
   __device__ __forceinline__ vec load(int j) const {
-    vec x;
-    if (whole(j)) {
-      x = load_whole(j);
-    } else {
-      const int first = j * E - lead;
+    vec x = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(resource, j * 16, 0, 0));
+    const int first = j * E - lead;
+    if (first < 0 || first + E > V) {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        x[e] = first + e >= 0 && first + e < V ? base[(int64_t)j * E + e] : (T)__builtin_nanf("");
+      for (int e = 0; e < E; ++e) x[e] = first + e >= 0 && first + e < V ? x[e] : (T)__builtin_nanf("");
     }
     if (infinite)
 #pragma unroll
@@ -124,24 +137,19 @@ struct SampleRow {
       return fmaxf(fmaxf((float)x[0], (float)x[1]), fmaxf((float)x[2], (float)x[3]));
     }
   }
-  // f(piece, its number) for this thread's pieces, four read at a time and the next four under way
+  // f(piece, its number) for this thread's pieces, 32 bytes read at a time and the next ones under way
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    vec next[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q < cw) next[q] = load(piece(q));
+    vec next[2] = {load(piece(0)), load(piece(1))};
 #pragma unroll 1
-    for (int u = 0; u < cw; u += 4) {
-      vec x[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] = next[q];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (u + 4 + q < cw) next[q] = load(piece(u + 4 + q));
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (u + q < cw) f(x[q], piece(u + q));
+    for (int u = 0; u < cw; u += 2) {
+      const vec x[2] = {next[0], next[1]};
+      if (u + 2 < cw) {
+        next[0] = load(piece(u + 2));
+        next[1] = load(piece(u + 3));
+      }
+      f(x[0], piece(u));
+      if (u + 1 < cw) f(x[1], piece(u + 1));
     }
   }
 
@@ -175,50 +183,62 @@ struct SampleRow {
     const uint64_t s = scan64(mine);
     if ((threadIdx.x & 63) == 63) sh.part[which][threadIdx.x >> 6] = s;
     lds_barrier();
-    uint64_t all = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      if (w == (int)(threadIdx.x >> 6)) before = all;
-      all += sh.part[which][w];
-    }
-    if (upto) *upto = before + s;
-    return all;
+    // the waves' sums, one a lane: a single access instead of one for each wave
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint64_t waves = scan64(lane < WAVES ? sh.part[which][lane] : 0);
+    if (upto) *upto = (wave > 0 ? lane64(waves, wave - 1) : 0) + s;
+    return lane64(waves, WAVES - 1);
   }
 
   static __device__ __forceinline__ uint64_t entry(float x, int i) { return (uint64_t)logit_key(x) << 32 | (uint32_t)~i; }
   static __device__ __forceinline__ float entry_logit(uint64_t e) { return key_logit((uint32_t)(e >> 32)); }
 
-  // Sorts list[0 .. n) descending (n <= kList; entries up to the next power of two become 0).
-  __device__ void sort(int n) const {
-    int size = 2;
-    while (size < n) size *= 2;
-    for (int i = n + threadIdx.x; i < size; i += THREADS) sh.list[i] = 0;
+  // Sorts list[0 .. n) descending; its entries differ.  Each wave ranks runs of 64 by comparing every pair,
+  // then every entry looks its place up in the other runs.
+  __device__ __forceinline__ void sort(int n) const {
+    constexpr int Q = kList / THREADS;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, runs = (n + 63) / 64;
+    uint64_t e[Q];
+    int rank[Q];
     lds_barrier();
-    const bool one_wave = size <= 128;
-    if (!one_wave || threadIdx.x < 64) {
-      for (int run = 2; run <= size; run *= 2)
-        for (int step = run / 2; step > 0; step /= 2) {
-          for (int i = threadIdx.x; i < size / 2; i += THREADS) {
-            const int a = 2 * i - (i & (step - 1)), b = a + step;
-            const uint64_t x = sh.list[a], y = sh.list[b];
-            if ((x < y) == ((a & run) == 0)) {
-              sh.list[a] = y;
-              sh.list[b] = x;
-            }
-          }
-          if (one_wave) __asm__ volatile("" ::: "memory");  // a wave's LDS accesses are done in order
-          else lds_barrier();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int run = q * WAVES + wave;
+      e[q] = 0;
+      rank[q] = 0;
+      if (run < runs) {
+        e[q] = run * 64 + lane < n ? sh.list[run * 64 + lane] : 0;
+        for (int j = 0; j < 64; ++j) rank[q] += lane64(e[q], j) > e[q] ? 1 : 0;
+        rank[q] = e[q] == 0 ? lane : rank[q];  // behind the last run's entries
+        sh.list[run * 64 + rank[q]] = e[q];
+      }
+    }
+    lds_barrier();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int run = q * WAVES + wave;
+      if (run < runs)
+        for (int other = 0; other < runs; ++other) {
+          if (other == run) continue;
+          int above = 0;  // of the other run
+#pragma unroll
+          for (int step = 32; step > 0; step /= 2) above += sh.list[other * 64 + above + step - 1] > e[q] ? step : 0;
+          rank[q] += above + (sh.list[other * 64 + above] > e[q] ? 1 : 0);
         }
     }
+    lds_barrier();
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (e[q] != 0) sh.list[rank[q]] = e[q];
     lds_barrier();
   }
 
   // list = the tokens that reach `least` and pass `also`, in any order, and returns their number (more
   // than kList: only some are in the list).  most: the largest logits of this thread's slots (slot q:
-  // pieces q, q + kSlots, .. of it), and of its edge piece.
+  // pieces q, q + kSlots, .. of it).
   template <typename F>
-  __device__ __forceinline__ int gather(const float (&most)[kSlots], float edge, int edge_piece, float least, F also) const {
-    uint32_t slots = edge >= least && edge > -INFINITY ? 1u << kSlots : 0u;
+  __device__ __forceinline__ int gather(const float (&most)[kSlots], float least, F also) const {
+    uint32_t slots = 0;
 #pragma unroll
     for (int q = 0; q < kSlots; ++q) slots |= most[q] >= least && most[q] > -INFINITY ? 1u << q : 0u;
     if (threadIdx.x == 0) {
@@ -230,7 +250,7 @@ struct SampleRow {
       const int q = __builtin_ctz(slots);
       slots &= slots - 1;
       const int at = atomicAdd(reinterpret_cast<int*>(&sh.found[0]), 1);
-      if (at < kBins) sh.counts[at] = q == kSlots ? ~(uint32_t)edge_piece : (uint32_t)piece(q);
+      if (at < kBins) sh.counts[at] = (uint32_t)piece(q);
     }
     lds_barrier();
     const int slots_found = (int)(uint32_t)sh.found[0];
@@ -239,12 +259,8 @@ struct SampleRow {
       return kList + 1;
     }
     for (int s = threadIdx.x; s < slots_found; s += THREADS) {
-      const uint32_t c = sh.counts[s];
-      const bool is_edge = (int32_t)c < 0;
-      // pieces of a slot are kSlots chunks apart, within its wave's chunks
-      const int j0 = is_edge ? (int)~c : (int)c, end = is_edge ? j0 + 1 : ((j0 / 64) / cw + 1) * cw * 64;
+      const int j0 = (int)sh.counts[s], end = ((j0 / 64) / cw + 1) * cw * 64;  // of its wave's chunks
       for (int j = j0; j < end; j += kSlots * 64) {
-        if (!is_edge && !whole(j)) continue;  // an edge piece is its own slot
         const vec x = load(j);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -288,46 +304,52 @@ struct SampleRow {
     lds_barrier();
     const int last = (int)sh.found[0];
     float least = mine > -INFINITY && bin <= last ? mine : INFINITY;
-#pragma unroll
-    for (int d = 32; d >= 1; d /= 2) least = fminf(least, __shfl_xor(least, d, kWave));
-    if ((threadIdx.x & 63) == 0) sh.most[0][threadIdx.x >> 6] = least;
+    least = wave_min(least);
+    if ((threadIdx.x & 63) == 0) sh.least[threadIdx.x >> 6] = least;
     lds_barrier();
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) least = fminf(least, sh.most[0][w]);
+    least = wave_min((threadIdx.x & 63) < WAVES ? sh.least[threadIdx.x & 63] : INFINITY);
     return last == STEPS ? -INFINITY : least;
   }
 
-  // The token at `share` of the up to 64 entries of the list, by the first wave alone.
+  // The token at `share` of the first n <= 64 entries of the sorted list, by the first wave: lane i has
+  // entry i (0 from n on).
+  __device__ __forceinline__ void choose_in_wave(uint64_t e, int n, float share) const {
+    const double exact = unrounded(entry_logit(e));
+    const uint64_t w = (int)threadIdx.x < n ? (uint64_t)weight(entry_logit(e)) : 0, total = lane64(scan64(w), 63);
+    const uint64_t target = target_of(share, total);
+    uint64_t sum = 0;  // of the tokens up to this one, by index
+    for (int j = 0; j < n; ++j) {
+      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e, j);
+      sum += other >= (uint32_t)e ? lane64(w, j) : 0;  // complements of the indices
+    }
+    if ((int)threadIdx.x < n && sum > target && sum - w <= target) {
+      sh.found[0] = (uint32_t)e;
+      sh.found[1] = (uint64_t)__double_as_longlong(exact / (double)total);
+    }
+  }
+  __device__ __forceinline__ int chosen_in_wave(float* prob) const {
+    lds_barrier();
+    *prob = (float)__longlong_as_double((int64_t)sh.found[1]);
+    return (int)~(uint32_t)sh.found[0];
+  }
+  // The token at `share` of the up to 64 entries of the list.
   __device__ __forceinline__ int choose_of_few(int n, int k, float p, double low, float share, float* prob) const {
     if (threadIdx.x < 64) {
       const int lane = threadIdx.x;
       uint64_t e = lane < n ? sh.list[lane] : 0;
       int rank = 0;
       for (int j = 0; j < n; ++j) rank += lane64(e, j) > e ? 1 : 0;
-      if (lane < n) sh.list[rank] = e;  // distinct: their indices are
+      if (lane < n) sh.list[rank] = e;  // a wave's accesses are done in order
       __asm__ volatile("" ::: "memory");
       e = lane < n ? sh.list[lane] : 0;
       if (k >= 1 && k < n) n = k;
-      const double exact = lane < n ? unrounded(entry_logit(e)) : 0.0;
       const uint64_t w = lane < n ? (uint64_t)weight(entry_logit(e)) : 0;
       const uint64_t upto = scan64(w);
       const double least = (double)p * (double)lane64(upto, 63);
       const bool in = lane < n && (lane == 0 || ((p >= 1.f || (double)(upto - w) < least) && (double)w >= low));
-      const int kept = __popcll(__ballot(in));
-      const uint64_t total = lane64(upto, kept - 1), target = target_of(share, total);
-      uint64_t sum = 0;  // of the kept tokens up to this one, by index
-      for (int j = 0; j < kept; ++j) {
-        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e, j);
-        sum += other >= (uint32_t)e ? lane64(w, j) : 0;  // complements of the indices
-      }
-      if (lane < kept && sum > target && sum - w <= target) {
-        sh.found[0] = (uint32_t)e;
-        sh.found[1] = (uint64_t)__double_as_longlong(exact / (double)total);
-      }
+      choose_in_wave(e, __popcll(__ballot(in)), share);
     }
-    lds_barrier();
-    *prob = (float)__longlong_as_double((int64_t)sh.found[1]);
-    return (int)~(uint32_t)sh.found[0];
+    return chosen_in_wave(prob);
   }
 
   // Of the sorted list's first n entries, how many are kept.
@@ -357,15 +379,18 @@ struct SampleRow {
       kept += i == 0 || in ? 1 : 0;
     }
     lds_barrier();
-    return (int)block_sum(kept, 0);
+    return __builtin_amdgcn_readfirstlane((int)block_sum(kept, 0));
   }
 
-  // The token at `share` of the first n entries of the list.
+  // The token at `share` of the first n entries of the list (in any order).
   __device__ __forceinline__ int choose_of_list(int n, float share, float* prob) const {
     constexpr int Q = kList / THREADS;
     lds_barrier();
+    if (n <= 64) {
+      if (threadIdx.x < 64) choose_in_wave((int)threadIdx.x < n ? sh.list[threadIdx.x] : 0, n, share);
+      return chosen_in_wave(prob);
+    }
     for (int i = threadIdx.x; i < n; i += THREADS) sh.list[i] = sh.list[i] << 32 | sh.list[i] >> 32;  // by index
-    lds_barrier();
     sort(n);
     uint64_t w[Q], upto[Q], total = 0;
 #pragma unroll
@@ -656,7 +681,8 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
   const T* start = reinterpret_cast<const T*>(a.logits) + r * a.stride;
   const int lead = (int)((reinterpret_cast<uintptr_t>(start) & 15) / sizeof(T));
   const int pieces = (lead + (int)a.V + E - 1) / E, cw = (pieces + THREADS - 1) / THREADS;
-  Row s{sh, start - lead, lead, (int)a.V, cw, false, 0.0, 0.0};
+  const int bytes = ((lead + (int)a.V) * (int)sizeof(T) + 3) & ~3;
+  Row s{sh, __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(start - lead), 0, bytes, 0x00020000), lead, (int)a.V, cw, false, 0.0, 0.0};
 
   // the largest logit of each slot, and the smallest of all (NaN aside); NV pieces under way
   float slot[kSlots], lo = INFINITY;
@@ -668,9 +694,8 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
       vec x[NV];
 #pragma unroll
       for (int q = 0; q < NV; ++q) {
-        const int j = s.piece(u0 + h + q);
         x[q] = vec{} + (T)__builtin_nanf("");
-        if (u0 + h + q < cw && s.whole(j)) x[q] = s.load_whole(j);
+        if (u0 + h + q < cw) x[q] = s.load(s.piece(u0 + h + q));
       }
 #pragma unroll
       for (int q = 0; q < NV; ++q) {
@@ -679,39 +704,23 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
       }
     }
   }
-  // the pieces that reach out of the row, first and last, by the first two threads
-  float edge = -INFINITY;
-  const int edge_piece = tid == 0 ? 0 : pieces - 1;
-  if (tid < 2 && !s.whole(edge_piece) && (tid == 0 || pieces > 1)) {
-    const vec x = s.load(edge_piece);
-    edge = Row::largest(x);
-    lo = fminf(lo, -Row::largest(-x));
-    edge = edge > -INFINITY ? edge : -INFINITY;  // a NaN
-  }
   const float t = a.temperature ? a.temperature[r] : a.temperature_value;
   const int32_t k = a.top_k ? a.top_k[r] : a.top_k_value;
   const float p = a.top_p ? a.top_p[r] : a.top_p_value, m = a.min_p ? a.min_p[r] : a.min_p_value, share = a.u[r];
-  float mine = edge;
+  float mine = slot[0];
 #pragma unroll
-  for (int q = 0; q < kSlots; ++q) mine = fmaxf(mine, slot[q]);
-  float hi = mine;
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) {
-    hi = fmaxf(hi, __shfl_xor(hi, d, kWave));
-    lo = fminf(lo, __shfl_xor(lo, d, kWave));
-  }
+  for (int q = 1; q < kSlots; ++q) mine = fmaxf(mine, slot[q]);
+  float hi = wave_max(mine);
+  lo = wave_min(lo);
   if ((tid & 63) == 0) {
-    sh.most[0][wave] = hi;
-    sh.most[1][wave] = lo;
+    sh.most[wave] = hi;
+    sh.least[wave] = lo;
   }
   for (int i = tid; i < kExpTable; i += THREADS) sh.table[i] = kExp.at[i];
   if (tid == 0) sh.n = 0x7FFFFFFF;
   lds_barrier();
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
-    hi = fmaxf(hi, sh.most[0][w]);
-    lo = fminf(lo, sh.most[1][w]);
-  }
+  hi = wave_max((tid & 63) < WAVES ? sh.most[tid & 63] : -INFINITY);
+  lo = wave_min((tid & 63) < WAVES ? sh.least[tid & 63] : INFINITY);
 
   int token = -1;
   float prob = 0.f;
@@ -727,7 +736,6 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
           if ((float)x[e] == hi) first = j * E - lead + e < first ? j * E - lead + e : first;
       };
       for (int u = 0; u < cw; ++u) look(s.piece(u));
-      if (edge == hi) look(edge_piece);
       atomicMin(&sh.n, first);
     }
     lds_barrier();
@@ -744,9 +752,9 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
     int n = kList + 1;
     if (!s.infinite) {
       if (ranked && k <= kListK<THREADS>)
-        n = s.gather(slot, edge, edge_piece, s.reached_by(k, mine, hi, range), [](float, int) { return true; });
+        n = s.gather(slot, s.reached_by(k, mine, hi, range), [](float, int) { return true; });
       else if (!cut_by_share && low > 0.0)  // w >= m is l >= hi + t ln m, here a little less
-        n = s.gather(slot, edge, edge_piece, fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY),
+        n = s.gather(slot, fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY),
                      [&](float l, int) { return s.weight(l) >= low; });
     }
     if (n <= 64) {
@@ -759,7 +767,10 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
 #pragma unroll 1
       for (int by_weight = ranked ? 0 : 1; by_weight <= (cut_by_share ? 1 : 0); ++by_weight)
         s.cut(&b, by_weight ? 0 : (uint64_t)k, p, range);
-      token = s.choose_of_row(b, low, share, &prob);
+      n = kList + 1;
+      if (!s.infinite && b.value > -INFINITY)  // what is kept may fit the list
+        n = s.gather(slot, b.value, [&](float l, int i) { return b.keeps(l, i) && s.weight(l) >= low; });
+      token = n <= kList ? s.choose_of_list(n, share, &prob) : s.choose_of_row(b, low, share, &prob);
     }
   }
   if (tid == 0) {
