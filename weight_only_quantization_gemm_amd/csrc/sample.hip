@@ -99,7 +99,9 @@ struct SampleShared {
 struct Border {
   float value;
   int last;
-  __device__ __forceinline__ bool keeps(float x, int i) const { return x > value || (x == value && i <= last); }
+  __device__ __forceinline__ bool keeps(float x, int i) const {
+    return (x > value) | ((x == value) & (i <= last));  // without branches
+  }
 };
 
 template <typename T, int THREADS>
@@ -170,6 +172,19 @@ struct SampleRow {
   __device__ __forceinline__ double weight(float x) const {
     constexpr double kHalfUnit = 4503599627370496.0;  // 2^52, where a double's spacing is 1
     return (unrounded(x) + kHalfUnit) - kHalfUnit;
+  }
+
+  // all of a piece, 0 where it is not kept or below low: side by side, so that the table's latency is paid once
+  __device__ __forceinline__ void weights(vec x, int j, const Border& b, double low, double (&w)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = unrounded((float)x[e]);
+    constexpr double kHalfUnit = 4503599627370496.0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      w[e] = (w[e] + kHalfUnit) - kHalfUnit;
+      const bool in = b.keeps((float)x[e], j * E - lead + e) & (w[e] >= low);
+      w[e] = in ? w[e] : 0.0;
+    }
   }
 
   __device__ __forceinline__ uint64_t target_of(float share, uint64_t total) const {
@@ -417,13 +432,10 @@ struct SampleRow {
   // The token at `share` of all that b keeps with weights from low on.
   __device__ __forceinline__ int choose_of_row(const Border& b, double low, float share, float* prob) const {
     auto amount = [&](vec x, int j) {
-      double s = 0.0;
+      double w[E], s = 0.0;
+      weights(x, j, b, low, w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float l = (float)x[e];
-        const double w = weight(l);
-        s += b.keeps(l, j * E - lead + e) && w >= low ? w : 0.0;
-      }
+      for (int e = 0; e < E; ++e) s += w[e];
       return s;
     };
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -451,15 +463,14 @@ struct SampleRow {
       if (lane == __builtin_ctzll(over)) {
         uint64_t sum = upto - own;
         bool done = false;
+        double we[E];
+        weights(x, j, b, low, we);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float l = (float)x[e];
-          const int i = j * E - lead + e;
-          const double we = weight(l);
-          sum += b.keeps(l, i) && we >= low ? (uint64_t)we : 0;
+          sum += (uint64_t)we[e];
           if (!done && sum > target) {
             done = true;
-            sh.found[0] = entry(l, i);
+            sh.found[0] = entry((float)x[e], j * E - lead + e);
           }
         }
       }
@@ -584,15 +595,14 @@ struct SampleRow {
     }
     lds_barrier();
     each([&](vec x, int j) {
+      double w[E];
+      weights(x, j, *b, 1.0, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float l = (float)x[e];
-        if (!b->keeps(l, j * E - lead + e)) continue;
-        const uint64_t w = (uint64_t)weight(l);
-        if (w == 0) continue;  // cannot be chosen, kept or not
-        const int bin = bin_of(l);
+        if (w[e] == 0.0) continue;  // cannot be chosen, kept or not
+        const int bin = bin_of((float)x[e]);
         if (by_count) atomicAdd(&sh.counts[bin], 1u);
-        else atomicAdd(reinterpret_cast<unsigned long long*>(&sh.list[bin]), (unsigned long long)w);
+        else atomicAdd(reinterpret_cast<unsigned long long*>(&sh.list[bin]), (unsigned long long)w[e]);
       }
     });
     lds_barrier();
@@ -626,6 +636,10 @@ struct SampleRow {
     if (threadIdx.x == 0) sh.n = 0;
     lds_barrier();
     each([&](vec x, int j) {
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < E; ++e) any |= bin_of((float)x[e]) == bin;
+      if (!any) return;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float l = (float)x[e];
