@@ -14,8 +14,7 @@
 // kept, over the row otherwise.
 //
 // Weights are whole multiples of 2^-43, so their sums are exact in any order and
-// the result does not depend on timing; as a double a thread's sum stays below
-// 2^53 (2^10 tokens of at most 2^43), a row's below 2^63 as a 64-bit number.
+// the result does not depend on timing; a row's sum stays below 2^63.
 #include "awq_internal.h"
 #include "row_common.h"
 
@@ -174,16 +173,22 @@ struct SampleRow {
     return (unrounded(x) + kHalfUnit) - kHalfUnit;
   }
 
-  // all of a piece, 0 where it is not kept or below low: side by side, so that the table's latency is paid once
-  __device__ __forceinline__ void weights(vec x, int j, const Border& b, double low, double (&w)[E]) const {
-#pragma unroll
-    for (int e = 0; e < E; ++e) w[e] = unrounded((float)x[e]);
+  // The same as a whole number: adding 2^52 leaves it in the double's low bits.
+  static __device__ __forceinline__ uint64_t whole(double unrounded) {
     constexpr double kHalfUnit = 4503599627370496.0;
+    return (uint64_t)__double_as_longlong(unrounded + kHalfUnit) - (uint64_t)__double_as_longlong(kHalfUnit);
+  }
+  // Those of a piece, with ALL of every token, otherwise of what b keeps from low on (0 for others); side
+  // by side, so that the table's latency is paid once.
+  template <bool ALL>
+  __device__ __forceinline__ void weights(vec x, int j, const Border& b, double low, uint64_t (&w)[E]) const {
+    double v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = unrounded((float)x[e]);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      w[e] = (w[e] + kHalfUnit) - kHalfUnit;
-      const bool in = b.keeps((float)x[e], j * E - lead + e) & (w[e] >= low);
-      w[e] = in ? w[e] : 0.0;
+      if constexpr (!ALL) v[e] = b.keeps((float)x[e], j * E - lead + e) & (v[e] >= low) ? v[e] : 0.0;
+      w[e] = whole(v[e]);
     }
   }
 
@@ -429,27 +434,28 @@ struct SampleRow {
     return (int)~(uint32_t)(e >> 32);
   }
 
-  // The token at `share` of all that b keeps with weights from low on.
+  // The token at `share` of all that b keeps with weights from low on; with ALL of the whole row.
+  template <bool ALL>
   __device__ __forceinline__ int choose_of_row(const Border& b, double low, float share, float* prob) const {
     auto amount = [&](vec x, int j) {
-      double w[E], s = 0.0;
-      weights(x, j, b, low, w);
+      uint64_t w[E], s = 0;
+      weights<ALL>(x, j, b, low, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) s += w[e];
       return s;
     };
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double mine = 0.0;
+    uint64_t mine = 0;
     each([&](vec x, int j) { mine += amount(x, j); });
     lds_barrier();
-    const uint64_t total = block_sum((uint64_t)mine, 0);
+    const uint64_t total = block_sum(mine, 0);
     uint64_t target = target_of(share, total);
     // the wave, then its chunk, then the lane and its element
     int w = 0;
     while (w < WAVES - 1 && sh.part[0][w] <= target) target -= sh.part[0][w++];
     for (int u = wave; u < cw; u += WAVES) {
       const int j = (w * cw + u) * 64 + lane;
-      const uint64_t s = scan64((uint64_t)amount(load(j), j));
+      const uint64_t s = scan64(amount(load(j), j));
       if (lane == 63) sh.list[u] = s;
     }
     lds_barrier();
@@ -458,16 +464,16 @@ struct SampleRow {
       while (u < cw - 1 && sh.list[u] <= target) target -= sh.list[u++];
       const int j = (w * cw + u) * 64 + lane;
       const vec x = load(j);
-      const uint64_t own = (uint64_t)amount(x, j), upto = scan64(own);
+      const uint64_t own = amount(x, j), upto = scan64(own);
       const uint64_t over = __ballot(upto > target);
       if (lane == __builtin_ctzll(over)) {
         uint64_t sum = upto - own;
         bool done = false;
-        double we[E];
-        weights(x, j, b, low, we);
+        uint64_t we[E];
+        weights<ALL>(x, j, b, low, we);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          sum += (uint64_t)we[e];
+          sum += we[e];
           if (!done && sum > target) {
             done = true;
             sh.found[0] = entry((float)x[e], j * E - lead + e);
@@ -588,6 +594,7 @@ struct SampleRow {
     constexpr int PER = kBins / THREADS;
     const bool by_count = rank_at > 0;
     const float step = fminf((float)kBins / range, 1e30f);
+    // NaN, behind the row's ends: the last bin, without weight
     auto bin_of = [&](float x) { return (int)fminf(((float)top - x) * step, (float)(kBins - 1)); };
     for (int i = threadIdx.x; i < kBins; i += THREADS) {
       sh.list[i] = 0;
@@ -595,14 +602,15 @@ struct SampleRow {
     }
     lds_barrier();
     each([&](vec x, int j) {
-      double w[E];
-      weights(x, j, *b, 1.0, w);
+      uint64_t w[E];
+      weights<false>(x, j, *b, 0.0, w);
+      int bin[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (w[e] == 0.0) continue;  // cannot be chosen, kept or not
-        const int bin = bin_of((float)x[e]);
-        if (by_count) atomicAdd(&sh.counts[bin], 1u);
-        else atomicAdd(reinterpret_cast<unsigned long long*>(&sh.list[bin]), (unsigned long long)w[e]);
+      for (int e = 0; e < E; ++e) bin[e] = bin_of((float)x[e]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {  // one of no weight cannot be chosen, kept or not
+        if (by_count) atomicAdd(&sh.counts[bin[e]], w[e] != 0 ? 1u : 0u);
+        else atomicAdd(reinterpret_cast<unsigned long long*>(&sh.list[bin[e]]), (unsigned long long)w[e]);
       }
     });
     lds_barrier();
@@ -784,7 +792,9 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
       n = kList + 1;
       if (!s.infinite && b.value > -INFINITY)  // what is kept may fit the list
         n = s.gather(slot, b.value, [&](float l, int i) { return b.keeps(l, i) && s.weight(l) >= low; });
-      token = n <= kList ? s.choose_of_list(n, share, &prob) : s.choose_of_row(b, low, share, &prob);
+      if (n <= kList) token = s.choose_of_list(n, share, &prob);
+      else if (b.value == -INFINITY && low == 0.0) token = s.template choose_of_row<true>(b, low, share, &prob);
+      else token = s.template choose_of_row<false>(b, low, share, &prob);
     }
   }
   if (tid == 0) {
