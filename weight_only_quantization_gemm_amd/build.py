@@ -40,6 +40,7 @@ FLAGS = [
 FILE_FLAGS = {"gemm_pipe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
               "grouped.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
               "kv_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+              "gemm_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
               "gemv.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"],
               "skinny.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"]}
 
