@@ -12,6 +12,7 @@
 // whole rows.
 #include "awq_internal.h"
 #include "mfma_pipe.h"
+#include "row_common.h"
 
 namespace awq {
 
@@ -26,6 +27,7 @@ struct I8Args {
   void* y;
   int64_t M, N, K;
   int mtiles, ntiles;
+  const float* s;  // input scales, where x is fp16
 };
 
 // Block b's tile.  Blocks are dispatched to the 8 XCDs in turn; each XCD takes a run of
@@ -157,10 +159,158 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
   }
 }
 
+// Few tokens: a block takes 16 channels at a time (gridDim.x groups apart), its NW waves every NW-th
+// 128 bytes of K, and their sums are joined through LDS.  A lane of v_mfma_i32_16x16x64_i8 holds 16 bytes
+// of one of 16 rows: lane l reads row l % 16, bytes 32 (l / 16) on of a chunk, 16 + 16, so four lanes share
+// a 128-byte line and both operands agree on the order of K.  Bound by the weights' one read: DEPTH chunks
+// of a wave are under way while DEPTH are multiplied, across the groups' ends; TT tiles of 16 tokens come
+// from the caches again for every group.
+// FUSED: x is fp16 [M][K], and each block quantises its rows to LDS itself (one launch instead of two),
+// while its first weights are under way.
+template <int TT, int NW, int DEPTH, bool FUSED, typename Y>
+__global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
+  extern __shared__ __align__(16) unsigned char rows[];  // FUSED: [M][K] codes
+  __shared__ i32x4 sums[2][NW][TT][64];
+  __shared__ float top[FUSED ? 16 * TT : 1][NW];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int chunks = (int)(a.K / 128), groups = (int)((a.N + 15) / 16), M = (int)a.M;
+  const int row = lane & 15, off = (lane >> 4) * 32;
+  const int batches = (chunks + NW * DEPTH - 1) / (NW * DEPTH);
+  struct Batch {
+    i32x4 w[DEPTH][2], x[FUSED ? 1 : TT][FUSED ? 1 : DEPTH][2];
+  };
+  int token[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) token[t] = t * 16 + row < M ? t * 16 + row : M - 1;  // the others' sums are not stored
+  // chunks past the end of a row: the last one, whose product is not taken
+  auto chunk = [&](int b, int d) { return wave + (b * DEPTH + d) * NW; };
+  auto fetch = [&](int g, int b, Batch& to) {
+    const int64_t n = (int64_t)g * 16 + row;
+    const int8_t* w = a.w + (n < a.N ? n : a.N - 1) * a.K + off;
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int c = chunk(b, d) < chunks ? chunk(b, d) : chunks - 1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        to.w[d][h] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(w + (int64_t)c * 128) + h);
+      if constexpr (!FUSED)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            to.x[t][d][h] = reinterpret_cast<const i32x4*>(a.x + (int64_t)token[t] * a.K + (int64_t)c * 128 + off)[h];
+    }
+  };
+  Batch cur, next;
+  int g = blockIdx.x, b = 0, buffer = 0;
+  fetch(g, 0, cur);
+  if constexpr (FUSED) {
+    // rows in slices of 512 channels, a wave at a time
+    const f16* x = reinterpret_cast<const f16*>(a.x);
+    auto values = [&](int m, int k) {
+      f32x8 v = widen(*reinterpret_cast<const f16x8*>(x + (int64_t)m * a.K + k));
+      return a.s ? v / *reinterpret_cast<const f32x8*>(a.s + k) : v;
+    };
+    for (int m = 0; m < M; ++m) {
+      float most = 0.f;
+      for (int k = threadIdx.x * 8; k < (int)a.K; k += 512 * NW) {
+        const f32x8 v = values(m, k);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) most = fmaxf(most, fabsf(v[u]));
+      }
+      most = wave_join(most, MaxOp());
+      if (lane == 0) top[m][wave] = most;
+    }
+    lds_barrier();
+    for (int m = 0; m < M; ++m) {
+      float most = top[m][0];
+#pragma unroll
+      for (int i = 1; i < NW; ++i) most = fmaxf(most, top[m][i]);
+      const float by = 127.f / most;
+      for (int k = threadIdx.x * 8; k < (int)a.K; k += 512 * NW) {
+        const f32x8 v = values(m, k);
+        float c[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) c[u] = code_of(v[u], by, most);
+        *reinterpret_cast<u32x2*>(rows + (int64_t)m * a.K + k) =
+            u32x2{code_word(c[0], c[1], c[2], c[3]), code_word(c[4], c[5], c[6], c[7])};
+      }
+    }
+    lds_barrier();
+  }
+  i32x4 acc[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) acc[t] = i32x4{};
+  while (g < groups) {
+    const bool last = b + 1 == batches;
+    const int g2 = last ? g + (int)gridDim.x : g, b2 = last ? 0 : b + 1;
+    if (g2 < groups) fetch(g2, b2, next);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (chunk(b, d) < chunks) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            i32x4 xv;
+            if constexpr (FUSED)
+              xv = reinterpret_cast<const i32x4*>(rows + (int64_t)token[t] * a.K + chunk(b, d) * 128 + off)[h];
+            else xv = cur.x[t][d][h];
+            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur.w[d][h], xv, acc[t], 0, 0, 0);
+          }
+      }
+    if (last) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        sums[buffer][wave][t][lane] = acc[t];
+        acc[t] = i32x4{};
+      }
+      lds_barrier();
+      // tile t's sums by wave t, four channels of a token a lane; the buffers are taken in turn, and the next
+      // group's barrier comes after these reads
+      if (wave < TT) {
+        i32x4 v = sums[buffer][0][wave][lane];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) v += sums[buffer][i][wave][lane];
+        const int m = wave * 16 + row;
+        const int64_t n = (int64_t)g * 16 + 4 * (lane >> 4);
+        if (m < M) {
+          float sm;
+          if constexpr (FUSED) {
+            sm = top[m][0];
+#pragma unroll
+            for (int i = 1; i < NW; ++i) sm = fmaxf(sm, top[m][i]);
+            sm = sm / 127.f;
+          } else {
+            sm = a.xs[m];
+          }
+          typedef Y yx4 __attribute__((ext_vector_type(4)));
+          Y* y = reinterpret_cast<Y*>(a.y) + (int64_t)m * a.N + n;
+          yx4 o;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[u] = (Y)((float)v[u] * sm * a.ws[n + u < a.N ? n + u : a.N - 1]);
+          if (n + 4 <= a.N && a.N % 4 == 0) *reinterpret_cast<yx4*>(y) = o;
+          else
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (n + u < a.N) y[u] = o[u];
+        }
+      }
+      buffer ^= 1;
+    }
+    cur = next;
+    g = g2;
+    b = b2;
+  }
+}
+
+// fp16 rows are quantised by the product itself up to this many codes
+static bool i8_fused(int64_t M, int64_t K, bool quantized) { return !quantized && M <= 4 && M * K <= 32768; }
+
 static size_t rows_bytes(int64_t M, int64_t K) { return ((size_t)M * (size_t)K + 255) / 256 * 256; }
 
 size_t gemm_i8_workspace(int64_t M, int64_t N, int64_t K, bool quantized) {
-  return quantized ? 0 : rows_bytes(M, K) + ((size_t)M * 4 + 255) / 256 * 256;
+  return quantized || i8_fused(M, K, quantized) ? 0 : rows_bytes(M, K) + ((size_t)M * 4 + 255) / 256 * 256;
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES>
@@ -175,9 +325,30 @@ static hipError_t tile_launch(I8Args a, int y_bytes, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <int TT, int NW, int DEPTH, bool FUSED>
+static hipError_t skinny_launch(const I8Args& a, int y_bytes, int per_cu, hipStream_t st) {
+  const int64_t groups = (a.N + 15) / 16, most = 256 * per_cu;
+  const dim3 grid((unsigned)(groups < most ? groups : most)), block(64 * NW);
+  const size_t lds = FUSED ? (size_t)(a.M * a.K) : 0;
+  if (KernelPlan* p = active_plan())
+    return plan_record(p, "gemm_i8_skinny_kernel<%d,%d,%d,%d> block=%u grid=%u", TT, NW, DEPTH, (int)FUSED, block.x, grid.x);
+  if (y_bytes == 2) gemm_i8_skinny_kernel<TT, NW, DEPTH, FUSED, f16><<<grid, block, lds, st>>>(a);
+  else gemm_i8_skinny_kernel<TT, NW, DEPTH, FUSED, float><<<grid, block, lds, st>>>(a);
+  return hipGetLastError();
+}
+
+static hipError_t skinny_dispatch(const I8Args& a, bool fused, int y_bytes, hipStream_t st) {
+  const bool wide = a.N <= 16 * 512;  // few groups: more waves on each
+  if (fused) return wide ? skinny_launch<1, 8, 4, true>(a, y_bytes, 2, st) : skinny_launch<1, 4, 4, true>(a, y_bytes, 4, st);
+  if (a.M <= 16) return wide ? skinny_launch<1, 8, 4, false>(a, y_bytes, 2, st) : skinny_launch<1, 4, 4, false>(a, y_bytes, 4, st);
+  if (a.M <= 32) return wide ? skinny_launch<2, 8, 2, false>(a, y_bytes, 2, st) : skinny_launch<2, 4, 2, false>(a, y_bytes, 4, st);
+  return wide ? skinny_launch<4, 8, 2, false>(a, y_bytes, 2, st) : skinny_launch<4, 4, 2, false>(a, y_bytes, 4, st);
+}
+
 hipError_t launch_gemm_i8(const void* x, const float* x_scales, const float* s, const void* codes, const float* scales,
                           void* y, int y_bytes, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t st) {
-  if (x_scales == nullptr && active_plan() == nullptr) {
+  const bool fused = i8_fused(M, K, x_scales != nullptr);
+  if (x_scales == nullptr && !fused && active_plan() == nullptr) {
     int8_t* xc = reinterpret_cast<int8_t*>(ws);
     float* sc = reinterpret_cast<float*>(xc + rows_bytes(M, K));
     const hipError_t e = launch_rows_i8(x, K, s, true, M, K, xc, sc, st);
@@ -185,7 +356,8 @@ hipError_t launch_gemm_i8(const void* x, const float* x_scales, const float* s, 
     x = xc;
     x_scales = sc;
   }
-  const I8Args a{reinterpret_cast<const int8_t*>(x), x_scales, reinterpret_cast<const int8_t*>(codes), scales, y, M, N, K, 0, 0};
+  const I8Args a{reinterpret_cast<const int8_t*>(x), x_scales, reinterpret_cast<const int8_t*>(codes), scales, y, M, N, K, 0, 0, s};
+  if (M <= 64) return skinny_dispatch(a, fused, y_bytes, st);
   if (M > 128) return tile_launch<256, 256, 4, 2, 4>(a, y_bytes, st);
   return tile_launch<128, 128, 2, 2, 4>(a, y_bytes, st);
 }
