@@ -19,6 +19,15 @@ namespace awq {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
+// A sum with its scales, rounded at each step.  The empty asm keeps the last product a number of its own:
+// joined with the rounding to fp16 into one instruction it would be rounded once less, in some kernels.
+template <typename Y>
+__device__ __forceinline__ Y scaled(int32_t sum, float token, float channel) {
+  float v = (float)sum * token * channel;
+  __asm__("" : "+v"(v));
+  return (Y)v;
+}
+
 struct I8Args {
   const int8_t* x;
   const float* xs;
@@ -26,9 +35,11 @@ struct I8Args {
   const float* ws;
   void* y;
   int64_t M, N, K;
-  int mtiles, ntiles;
-  const float* s;  // input scales, where x is fp16
+  const float* s;     // input scales, where x is fp16
+  int mtiles, ntiles, splits;
+  int32_t* partial;   // [splits][M][partial_pitch(N)] sums of each share of K, where splits > 1
 };
+static __host__ __device__ constexpr int64_t partial_pitch(int64_t N) { return (N + 3) / 4 * 4; }
 
 // Block b's tile.  Blocks are dispatched to the 8 XCDs in turn; each XCD takes a run of
 // tiles, in groups of up to 8 token tiles by all channel tiles, so that the blocks of an XCD
@@ -63,17 +74,19 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
   __shared__ __align__(16) unsigned char lds[S::LDS];
   f16* ring = reinterpret_cast<f16*>(lds);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const TileAt at = tile_at(blockIdx.x, a.mtiles, a.ntiles);
+  const int tiles = a.mtiles * a.ntiles, share = blockIdx.x / tiles;
+  const TileAt at = tile_at(blockIdx.x - share * tiles, a.mtiles, a.ntiles);
   const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
   const int wm = (wave % WM) * S::TM, wn = (wave / WM) * S::TN;
   TilePlan<BM, S::NW, 32> px;
   TilePlan<BN, S::NW, 32> pw;
   px.init(reinterpret_cast<const f16*>(a.x), a.K / 2, m0, a.M, wave, lane);
   pw.init(reinterpret_cast<const f16*>(a.w), a.K / 2, n0, a.N, wave, lane);
-  const int steps = (int)(a.K / 64);  // even
+  const int all = (int)(a.K / 64), first = (int)((int64_t)all * share / a.splits);
+  const int steps = (int)((int64_t)all * (share + 1) / a.splits) - first;  // splits <= all
   auto issue = [&](int s) {
     f16* stage = ring + (s % STAGES) * S::STAGE;
-    const int64_t k = (int64_t)(s < steps ? s : steps - 1) * 32;  // past the end: counted, never used
+    const int64_t k = (int64_t)(first + (s < steps ? s : steps - 1)) * 32;  // past the end: counted, never used
     px.issue(stage, k);
     pw.issue(stage + BM * 32, k);
   };
@@ -122,12 +135,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
   Y* turn_y = reinterpret_cast<Y*>(turn);
   constexpr int PITCH = sizeof(Y) == 4 ? S::PITCH : 2 * S::PITCH;  // elements
   constexpr int PER = 16 / sizeof(Y), LANES = S::TN / PER, ROWS = 64 / LANES;
-  Y* y = reinterpret_cast<Y*>(a.y);
-  const bool whole = a.N % PER == 0 && n0 + wn + S::TN <= a.N;
+  constexpr bool kPartial = __is_same(Y, int32_t);
+  const int64_t pitch = kPartial ? partial_pitch(a.N) : a.N;
+  Y* y = kPartial ? reinterpret_cast<Y*>(a.partial) + share * a.M * pitch : reinterpret_cast<Y*>(a.y);
+  const bool whole = pitch % PER == 0 && n0 + wn + S::TN <= a.N;
 #pragma unroll
   for (int j = 0; j < AM; ++j) {
     const int64_t mj = m0 + wm + j * 32, m = mj + (lane & 31);
-    const float sm = a.xs[m < a.M ? m : a.M - 1];
+    float sm = 0.f;
+    if constexpr (!kPartial) sm = a.xs[m < a.M ? m : a.M - 1];
 #pragma unroll
     for (int i = 0; i < AN; ++i)
 #pragma unroll
@@ -138,7 +154,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int64_t ng = n0 + wn + n + u;
-          v[u] = (Y)((float)acc[i][j][4 * q + u] * sm * a.ws[ng < a.N ? ng : a.N - 1]);
+          if constexpr (kPartial) v[u] = acc[i][j][4 * q + u];
+          else v[u] = scaled<Y>(acc[i][j][4 * q + u], sm, a.ws[ng < a.N ? ng : a.N - 1]);
         }
         *reinterpret_cast<yx4*>(turn_y + (lane & 31) * PITCH + n) = v;
       }
@@ -148,15 +165,36 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
       for (int r = 0; r < 32; r += ROWS) {
         const int row = r + lane / LANES, n = (lane % LANES) * PER;
         const u32x4 v = *reinterpret_cast<const u32x4*>(turn_y + row * PITCH + n);
-        if (mj + row < a.M) *reinterpret_cast<u32x4*>(y + (mj + row) * a.N + n0 + wn + n) = v;
+        if (mj + row < a.M) *reinterpret_cast<u32x4*>(y + (mj + row) * pitch + n0 + wn + n) = v;
       }
     } else {
       for (int r = 0; r < 32; ++r)
         for (int n = lane; n < S::TN; n += 64)
-          if (mj + r < a.M && n0 + wn + n < a.N) y[(mj + r) * a.N + n0 + wn + n] = turn_y[r * PITCH + n];
+          if (mj + r < a.M && n0 + wn + n < a.N) y[(mj + r) * pitch + n0 + wn + n] = turn_y[r * PITCH + n];
     }
     __asm__ volatile("" ::: "memory");
   }
+}
+
+// The shares' sums joined, scaled and rounded: four channels of a token a thread.
+template <typename Y>
+__global__ __launch_bounds__(256) void gemm_i8_join_kernel(I8Args a) {
+  const int64_t pitch = partial_pitch(a.N), per = pitch / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.M * per) return;
+  const int64_t m = i / per, n = (i - m * per) * 4;
+  i32x4 v = {};
+  for (int s = 0; s < a.splits; ++s) v += *reinterpret_cast<const i32x4*>(a.partial + (s * a.M + m) * pitch + n);
+  const float sm = a.xs[m];
+  typedef Y yx4 __attribute__((ext_vector_type(4)));
+  Y* y = reinterpret_cast<Y*>(a.y) + m * a.N + n;
+  yx4 o;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) o[u] = scaled<Y>(v[u], sm, a.ws[n + u < a.N ? n + u : a.N - 1]);
+  if (a.N % 4 == 0) *reinterpret_cast<yx4*>(y) = o;
+  else
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (n + u < a.N) y[u] = o[u];
 }
 
 // Few tokens: a block takes 16 channels at a time (gridDim.x groups apart), its NW waves every NW-th
@@ -165,13 +203,13 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
 // a 128-byte line and both operands agree on the order of K.  Bound by the weights' one read: DEPTH chunks
 // of a wave are under way while DEPTH are multiplied, across the groups' ends; TT tiles of 16 tokens come
 // from the caches again for every group.
-// FUSED: x is fp16 [M][K], and each block quantises its rows to LDS itself (one launch instead of two),
-// while its first weights are under way.
+// FUSED: x is one fp16 row, which each block quantises to LDS itself (one launch instead of two), while its
+// first weights are under way.
 template <int TT, int NW, int DEPTH, bool FUSED, typename Y>
 __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
-  extern __shared__ __align__(16) unsigned char rows[];  // FUSED: [M][K] codes
+  extern __shared__ __align__(16) unsigned char rows[];  // FUSED: the row's codes
   __shared__ i32x4 sums[2][NW][TT][64];
-  __shared__ float top[FUSED ? 16 * TT : 1][NW];
+  __shared__ float part[NW];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int chunks = (int)(a.K / 128), groups = (int)((a.N + 15) / 16), M = (int)a.M;
   const int row = lane & 15, off = (lane >> 4) * 32;
@@ -204,37 +242,28 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
   Batch cur, next;
   int g = blockIdx.x, b = 0, buffer = 0;
   fetch(g, 0, cur);
+  float top = 0.f;
   if constexpr (FUSED) {
-    // rows in slices of 512 channels, a wave at a time
     const f16* x = reinterpret_cast<const f16*>(a.x);
-    auto values = [&](int m, int k) {
-      f32x8 v = widen(*reinterpret_cast<const f16x8*>(x + (int64_t)m * a.K + k));
+    auto values = [&](int k) {
+      const f32x8 v = widen(*reinterpret_cast<const f16x8*>(x + k));
       return a.s ? v / *reinterpret_cast<const f32x8*>(a.s + k) : v;
     };
-    for (int m = 0; m < M; ++m) {
-      float most = 0.f;
-      for (int k = threadIdx.x * 8; k < (int)a.K; k += 512 * NW) {
-        const f32x8 v = values(m, k);
+    float most = 0.f;
+    for (int k = threadIdx.x * 8; k < (int)a.K; k += 512 * NW) {
+      const f32x8 v = values(k);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) most = fmaxf(most, fabsf(v[u]));
-      }
-      most = wave_join(most, MaxOp());
-      if (lane == 0) top[m][wave] = most;
+      for (int u = 0; u < 8; ++u) most = fmaxf(most, fabsf(v[u]));
     }
-    lds_barrier();
-    for (int m = 0; m < M; ++m) {
-      float most = top[m][0];
+    most = row_join<64 * NW>(most, part, MaxOp());
+    top = most;
+    const float by = 127.f / most;
+    for (int k = threadIdx.x * 8; k < (int)a.K; k += 512 * NW) {
+      const f32x8 v = values(k);
+      float c[8];
 #pragma unroll
-      for (int i = 1; i < NW; ++i) most = fmaxf(most, top[m][i]);
-      const float by = 127.f / most;
-      for (int k = threadIdx.x * 8; k < (int)a.K; k += 512 * NW) {
-        const f32x8 v = values(m, k);
-        float c[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) c[u] = code_of(v[u], by, most);
-        *reinterpret_cast<u32x2*>(rows + (int64_t)m * a.K + k) =
-            u32x2{code_word(c[0], c[1], c[2], c[3]), code_word(c[4], c[5], c[6], c[7])};
-      }
+      for (int u = 0; u < 8; ++u) c[u] = code_of(v[u], by, most);
+      *reinterpret_cast<u32x2*>(rows + k) = u32x2{code_word(c[0], c[1], c[2], c[3]), code_word(c[4], c[5], c[6], c[7])};
     }
     lds_barrier();
   }
@@ -254,7 +283,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
           for (int h = 0; h < 2; ++h) {
             i32x4 xv;
             if constexpr (FUSED)
-              xv = reinterpret_cast<const i32x4*>(rows + (int64_t)token[t] * a.K + chunk(b, d) * 128 + off)[h];
+              xv = reinterpret_cast<const i32x4*>(rows + chunk(b, d) * 128 + off)[h];
             else xv = cur.x[t][d][h];
             acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur.w[d][h], xv, acc[t], 0, 0, 0);
           }
@@ -275,20 +304,12 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
         const int m = wave * 16 + row;
         const int64_t n = (int64_t)g * 16 + 4 * (lane >> 4);
         if (m < M) {
-          float sm;
-          if constexpr (FUSED) {
-            sm = top[m][0];
-#pragma unroll
-            for (int i = 1; i < NW; ++i) sm = fmaxf(sm, top[m][i]);
-            sm = sm / 127.f;
-          } else {
-            sm = a.xs[m];
-          }
+          const float sm = FUSED ? top / 127.f : a.xs[m];
           typedef Y yx4 __attribute__((ext_vector_type(4)));
           Y* y = reinterpret_cast<Y*>(a.y) + (int64_t)m * a.N + n;
           yx4 o;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) o[u] = (Y)((float)v[u] * sm * a.ws[n + u < a.N ? n + u : a.N - 1]);
+          for (int u = 0; u < 4; ++u) o[u] = scaled<Y>(v[u], sm, a.ws[n + u < a.N ? n + u : a.N - 1]);
           if (n + 4 <= a.N && a.N % 4 == 0) *reinterpret_cast<yx4*>(y) = o;
           else
 #pragma unroll
@@ -304,24 +325,73 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
   }
 }
 
-// fp16 rows are quantised by the product itself up to this many codes
-static bool i8_fused(int64_t M, int64_t K, bool quantized) { return !quantized && M <= 4 && M * K <= 32768; }
-
 static size_t rows_bytes(int64_t M, int64_t K) { return ((size_t)M * (size_t)K + 255) / 256 * 256; }
 
+// One fp16 row is quantised by the product itself, up to this many codes (its LDS).
+static bool i8_fused(int64_t M, int64_t K, bool quantized) { return !quantized && M == 1 && K <= 32768; }
+
+// The kernel for these sizes: the one of least estimated time, in us, by what was measured on an MI355X
+// over N x K = 4096 x 4096 .. 28672 x 8192 and 1408 x 2048, M = 1 .. 1024 (estimates within 15 %):
+//   few tokens: the weights at 4.5 TB/s up to 8 tokens, 3.8 to 16, 2.75 to 32, 1.65 to 64 (the rows' codes
+//     come from the L2 once for each 16 channels);
+//   tiles of BM x 128 (256 x 256): the weights at 6 TB/s, and a block's step of 64 bytes of K in 0.19, 0.21,
+//     0.32, 0.93 us at BM = 32, 64, 128, 256, a compute unit's blocks one after the other;
+//   shares of K: 2.5 us for the join and its traffic at 4 TB/s.
+// E.g. 77 x 4096 x 11008: BM = 64, 4 shares: 17.3 us (1 share 38, BM = 128 with 6 shares 18.2); 32 x 50021 x
+// 4096: BM = 32: 35.9 us (few tokens' kernel 82); 8 x 4096 x 4096: few tokens' kernel 6.4 us (BM = 32: 9.1).
+struct I8Plan {
+  int tile;    // tokens of a tile; 0: the kernel for few tokens
+  int splits;  // shares of K
+};
+static I8Plan i8_plan(int64_t M, int64_t N, int64_t K, bool quantized) {
+  const double launch = 3.0, weights = (double)N * (double)K * 1e-6;  // MB
+  I8Plan best{0, 1};
+  double least = 1e30;
+  if (M <= 64) least = launch + weights / (M <= 8 ? 4.5 : M <= 16 ? 3.8 : M <= 32 ? 2.75 : 1.65);
+  const double rows = i8_fused(M, K, quantized) ? launch : 0.0;  // the rows' own launch, which that kernel saves
+  const int64_t steps = K / 64;
+  for (const int tile : {32, 64, 128, 256}) {
+    const int64_t tiles = ((M + tile - 1) / tile) * ((N + (tile == 256 ? 255 : 127)) / (tile == 256 ? 256 : 128));
+    const double step = tile == 32 ? 0.19 : tile == 64 ? 0.21 : tile == 128 ? 0.32 : 0.93;
+    for (int splits = 1; splits == 1 || (splits <= 16 && splits * 4 <= steps && tiles * splits <= 1024); ++splits) {
+      const int64_t rounds = (tiles * splits + 255) / 256, share = (steps + splits - 1) / splits;
+      double us = launch + rows + fmax(weights / 6.0, (double)rounds * (double)share * step);
+      if (splits > 1) us += 2.5 + (double)splits * (double)M * (double)N * 8e-6 / 4.0;
+      if (us < least) {
+        least = us;
+        best = {tile, splits};
+      }
+    }
+  }
+  return best;
+}
+
 size_t gemm_i8_workspace(int64_t M, int64_t N, int64_t K, bool quantized) {
-  return quantized || i8_fused(M, K, quantized) ? 0 : rows_bytes(M, K) + ((size_t)M * 4 + 255) / 256 * 256;
+  const I8Plan plan = i8_plan(M, N, K, quantized);
+  size_t bytes = plan.splits > 1 ? (size_t)plan.splits * (size_t)M * (size_t)partial_pitch(N) * 4 : 0;
+  if (!quantized && !(plan.tile == 0 && i8_fused(M, K, quantized)))
+    bytes += rows_bytes(M, K) + ((size_t)M * 4 + 255) / 256 * 256;
+  return (bytes + 255) / 256 * 256;
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES>
 static hipError_t tile_launch(I8Args a, int y_bytes, hipStream_t st) {
   a.mtiles = (int)((a.M + BM - 1) / BM);
   a.ntiles = (int)((a.N + BN - 1) / BN);
-  const dim3 grid((unsigned)(a.mtiles * a.ntiles)), block(64 * WM * WN);
+  const dim3 grid((unsigned)(a.mtiles * a.ntiles * a.splits)), block(64 * WM * WN);
   if (KernelPlan* p = active_plan())
-    return plan_record(p, "gemm_i8_kernel<%d,%d,%d,%d,%d> block=%u grid=%u", BM, BN, WM, WN, STAGES, block.x, grid.x);
-  if (y_bytes == 2) gemm_i8_kernel<BM, BN, WM, WN, STAGES, f16><<<grid, block, 0, st>>>(a);
-  else gemm_i8_kernel<BM, BN, WM, WN, STAGES, float><<<grid, block, 0, st>>>(a);
+    return plan_record(p, "gemm_i8_kernel<%d,%d,%d,%d,%d> block=%u grid=%u shares=%d", BM, BN, WM, WN, STAGES, block.x,
+                       grid.x, a.splits);
+  if (a.splits > 1) {
+    gemm_i8_kernel<BM, BN, WM, WN, STAGES, int32_t><<<grid, block, 0, st>>>(a);
+    const dim3 join((unsigned)((a.M * (partial_pitch(a.N) / 4) + 255) / 256));
+    if (y_bytes == 2) gemm_i8_join_kernel<f16><<<join, dim3(256), 0, st>>>(a);
+    else gemm_i8_join_kernel<float><<<join, dim3(256), 0, st>>>(a);
+  } else if (y_bytes == 2) {
+    gemm_i8_kernel<BM, BN, WM, WN, STAGES, f16><<<grid, block, 0, st>>>(a);
+  } else {
+    gemm_i8_kernel<BM, BN, WM, WN, STAGES, float><<<grid, block, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 
@@ -329,7 +399,7 @@ template <int TT, int NW, int DEPTH, bool FUSED>
 static hipError_t skinny_launch(const I8Args& a, int y_bytes, int per_cu, hipStream_t st) {
   const int64_t groups = (a.N + 15) / 16, most = 256 * per_cu;
   const dim3 grid((unsigned)(groups < most ? groups : most)), block(64 * NW);
-  const size_t lds = FUSED ? (size_t)(a.M * a.K) : 0;
+  const size_t lds = FUSED ? (size_t)a.K : 0;
   if (KernelPlan* p = active_plan())
     return plan_record(p, "gemm_i8_skinny_kernel<%d,%d,%d,%d> block=%u grid=%u", TT, NW, DEPTH, (int)FUSED, block.x, grid.x);
   if (y_bytes == 2) gemm_i8_skinny_kernel<TT, NW, DEPTH, FUSED, f16><<<grid, block, lds, st>>>(a);
@@ -338,28 +408,35 @@ static hipError_t skinny_launch(const I8Args& a, int y_bytes, int per_cu, hipStr
 }
 
 static hipError_t skinny_dispatch(const I8Args& a, bool fused, int y_bytes, hipStream_t st) {
-  const bool wide = a.N <= 16 * 512;  // few groups: more waves on each
-  if (fused) return wide ? skinny_launch<1, 8, 4, true>(a, y_bytes, 2, st) : skinny_launch<1, 4, 4, true>(a, y_bytes, 4, st);
-  if (a.M <= 16) return wide ? skinny_launch<1, 8, 4, false>(a, y_bytes, 2, st) : skinny_launch<1, 4, 4, false>(a, y_bytes, 4, st);
-  if (a.M <= 32) return wide ? skinny_launch<2, 8, 2, false>(a, y_bytes, 2, st) : skinny_launch<2, 4, 2, false>(a, y_bytes, 4, st);
-  return wide ? skinny_launch<4, 8, 2, false>(a, y_bytes, 2, st) : skinny_launch<4, 4, 2, false>(a, y_bytes, 4, st);
+  const bool narrow = a.N <= 16 * 512;  // few groups: more waves on each
+  if (fused) return narrow ? skinny_launch<1, 8, 4, true>(a, y_bytes, 2, st) : skinny_launch<1, 4, 4, true>(a, y_bytes, 4, st);
+  if (a.M <= 16) return narrow ? skinny_launch<1, 8, 4, false>(a, y_bytes, 2, st) : skinny_launch<1, 4, 4, false>(a, y_bytes, 4, st);
+  if (a.M <= 32) return narrow ? skinny_launch<2, 8, 2, false>(a, y_bytes, 2, st) : skinny_launch<2, 4, 2, false>(a, y_bytes, 4, st);
+  return narrow ? skinny_launch<4, 8, 2, false>(a, y_bytes, 2, st) : skinny_launch<4, 4, 2, false>(a, y_bytes, 4, st);
 }
 
 hipError_t launch_gemm_i8(const void* x, const float* x_scales, const float* s, const void* codes, const float* scales,
                           void* y, int y_bytes, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t st) {
-  const bool fused = i8_fused(M, K, x_scales != nullptr);
+  const I8Plan plan = i8_plan(M, N, K, x_scales != nullptr);
+  const bool fused = plan.tile == 0 && i8_fused(M, K, x_scales != nullptr);
+  int8_t* scratch = reinterpret_cast<int8_t*>(ws);
   if (x_scales == nullptr && !fused && active_plan() == nullptr) {
-    int8_t* xc = reinterpret_cast<int8_t*>(ws);
-    float* sc = reinterpret_cast<float*>(xc + rows_bytes(M, K));
-    const hipError_t e = launch_rows_i8(x, K, s, true, M, K, xc, sc, st);
+    float* sc = reinterpret_cast<float*>(scratch + rows_bytes(M, K));
+    const hipError_t e = launch_rows_i8(x, K, s, true, M, K, scratch, sc, st);
     if (e != hipSuccess) return e;
-    x = xc;
+    x = scratch;
     x_scales = sc;
+    scratch += rows_bytes(M, K) + ((size_t)M * 4 + 255) / 256 * 256;
   }
-  const I8Args a{reinterpret_cast<const int8_t*>(x), x_scales, reinterpret_cast<const int8_t*>(codes), scales, y, M, N, K, 0, 0, s};
-  if (M <= 64) return skinny_dispatch(a, fused, y_bytes, st);
-  if (M > 128) return tile_launch<256, 256, 4, 2, 4>(a, y_bytes, st);
-  return tile_launch<128, 128, 2, 2, 4>(a, y_bytes, st);
+  const I8Args a{reinterpret_cast<const int8_t*>(x), x_scales, reinterpret_cast<const int8_t*>(codes), scales, y, M, N, K, s,
+                 0, 0, plan.splits, reinterpret_cast<int32_t*>(scratch)};
+  switch (plan.tile) {
+    case 0: return skinny_dispatch(a, fused, y_bytes, st);
+    case 32: return tile_launch<32, 128, 1, 2, 8>(a, y_bytes, st);
+    case 64: return tile_launch<64, 128, 1, 4, 6>(a, y_bytes, st);
+    case 128: return tile_launch<128, 128, 2, 2, 4>(a, y_bytes, st);
+    default: return tile_launch<256, 256, 4, 2, 4>(a, y_bytes, st);
+  }
 }
 
 }  // namespace awq
