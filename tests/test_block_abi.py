@@ -107,14 +107,17 @@ def test_wrappers_refuse_cpu_tensors_and_wrong_types():
 
 @pytest.mark.parametrize("M,N,K,quantized,kernel", [
     (1, 11008, 4096, False, "gemm_i8_skinny_kernel<1,4,4,1> block=256 grid=688"),   # quantises its own row
-    (1, 4096, 65536, False, "gemm_i8_kernel<32,128,1,2,8> block=128 grid=160 shares=5"),  # too long a row for that
+    (1, 4096, 65536, False, "gemm_i8_kernel<32,128,1,4,4,64> block=256 grid=160 shares=5"),  # too long a row for that
     (1, 4096, 4096, True, "gemm_i8_skinny_kernel<1,8,4,0> block=512 grid=256"),
     (32, 4096, 4096, True, "gemm_i8_skinny_kernel<2,8,2,0> block=512 grid=256"),
     (64, 1408, 2048, True, "gemm_i8_skinny_kernel<4,8,2,0> block=512 grid=88"),
-    (16, 50021, 4096, True, "gemm_i8_kernel<32,128,1,2,8> block=128 grid=391 shares=1"),  # a wide layer
-    (77, 4096, 11008, True, "gemm_i8_kernel<64,128,1,4,6> block=256 grid=256 shares=4"),
-    (128, 28672, 8192, True, "gemm_i8_kernel<128,128,2,2,4> block=256 grid=224 shares=1"),
-    (8192, 28672, 8192, True, "gemm_i8_kernel<256,256,4,2,4> block=512 grid=3584 shares=1"),
+    (16, 11008, 4096, True, "gemm_i8_kernel<32,64,1,2,6,64> block=128 grid=172 shares=1"),
+    (16, 50021, 4096, True, "gemm_i8_kernel<32,128,1,4,4,64> block=256 grid=391 shares=1"),  # a wide layer
+    (64, 28672, 8192, True, "gemm_i8_kernel<64,64,1,2,5,64> block=128 grid=448 shares=1"),
+    (77, 4096, 11008, True, "gemm_i8_kernel<128,128,2,4,4,64> block=512 grid=224 shares=7"),
+    (500, 4096, 1024, True, "gemm_i8_kernel<64,128,1,4,3,64> block=256 grid=256 shares=1"),
+    (128, 28672, 8192, True, "gemm_i8_kernel<128,128,2,4,4,64> block=512 grid=224 shares=1"),
+    (8192, 28672, 8192, True, "gemm_i8_kernel<256,256,4,2,4,32> block=512 grid=3584 shares=1"),
 ])
 def test_product_dispatch(M, N, K, quantized, kernel):
     assert awq.awq_gemm_i8_kernel(M, N, K, quantized) == kernel
@@ -124,5 +127,5 @@ def test_product_workspaces():
     """None for a quantised x without shares of K, nor for the one row a kernel quantises itself."""
     assert awq.awq_gemm_i8_workspace_bytes(8192, 28672, 8192, True) == 0
     assert awq.awq_gemm_i8_workspace_bytes(1, 11008, 4096, False) == 0
-    assert awq.awq_gemm_i8_workspace_bytes(77, 4096, 11008, True) == 4 * 77 * 4096 * 4
+    assert awq.awq_gemm_i8_workspace_bytes(77, 4096, 11008, True) == 7 * 77 * 4096 * 4
     assert awq.awq_gemm_i8_workspace_bytes(8192, 28672, 8192, False) == 8192 * 8192 + 8192 * 4

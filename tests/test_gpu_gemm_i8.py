@@ -88,7 +88,7 @@ SHAPES = [(M, N, K) for M in (1, 2, 5, 8, 16, 17, 31, 32, 33, 64, 65, 96, 128, 1
 SHAPES += [(M, N, K) for M in (1, 3, 16, 48, 64, 200) for N, K in ((257, 4096), (96, 11008), (4097, 512), (16, 32768))]
 SHAPES += [(513, 515, 640), (700, 300, 128), (1025, 768, 1408), (2048, 100, 256), (40, 20000, 256), (600, 6000, 256)]
 SHAPES += [(77, 1001, 4096), (33, 515, 11008), (100, 259, 8192), (256, 1030, 4096), (8, 26001, 512), (50, 30000, 256),
-           (300, 2050, 11008)]  # shares of K with odd channels, and wide layers of few tokens
+           (300, 2050, 11008), (497, 4090, 1024), (3999, 4093, 512)]  # shares of K with odd channels, and wide layers of few tokens
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

@@ -1,15 +1,18 @@
 // The product in 8-bit integers: y = (x codes) (w codes)^T in exact 32-bit sums,
 // times a scale for each token and each channel.
 //
-// Tile kernel: BM tokens x BN channels a block, K in stages of 64 bytes.  Stages go
-// from global memory straight into a ring of LDS buffers (the 64-byte-row layout
-// of mfma_pipe.h, a pair of codes in the place of a half) and feed
-// v_mfma_i32_32x32x32_i8.  A stage's first fragments are read before the barrier
+// Tile kernel: BM tokens x BN channels a block, K in stages of 2 W bytes (128, a whole
+// line, where the weights come from memory: 32 x 50021 x 4096 49.6 us, 56.0 with 64;
+// 64 for the largest tiles, whose stages would not fit).  Stages go from global memory
+// straight into a ring of LDS buffers (the layouts of mfma_pipe.h, a pair of codes in
+// the place of a half) and feed v_mfma_i32_32x32x32_i8.  A stage's first fragments are read before the barrier
 // that opens it, so the matrix cores do not wait for the barrier or the LDS: the
 // barrier of stage s only says that stage s + 1 has landed and stage s - 1 is free.
 // The weights are the A operand, so a lane's accumulators hold four consecutive
 // channels of one token; the results are turned over through LDS and stored as
 // whole rows.
+#include <cmath>
+
 #include "awq_internal.h"
 #include "mfma_pipe.h"
 #include "row_common.h"
@@ -55,21 +58,21 @@ __device__ __forceinline__ TileAt tile_at(int b, int mtiles, int ntiles) {
   return {group * 8 + in % rows, in / rows};
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES>
+template <int BM, int BN, int WM, int WN, int STAGES, int W>
 struct I8Shape {
   static constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, AM = TM / 32, AN = TN / 32;
-  static constexpr int STAGE = (BM + BN) * 32;  // halfs
-  static constexpr int LOADS = (BM + BN) / 16 / NW;
+  static constexpr int SUB = W / 16;            // matrix instructions along K of a stage
+  static constexpr int STAGE = (BM + BN) * W;   // halfs
+  static constexpr int LOADS = (BM + BN) * W / 512 / NW;
   static constexpr int PITCH = TN + 4;          // words of a row of the turned-over tile (fp32; fp16 uses half)
   static constexpr int RING = STAGES * STAGE * 2, TURN = NW * 32 * PITCH * 4;
   static constexpr int LDS = RING > TURN ? RING : TURN;
-  static_assert((BM / 16) % NW == 0 && (BN / 16) % NW == 0, "whole loads a wave");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-template <int BM, int BN, int WM, int WN, int STAGES, typename Y>
+template <int BM, int BN, int WM, int WN, int STAGES, int W, typename Y>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
-  typedef I8Shape<BM, BN, WM, WN, STAGES> S;
+  typedef I8Shape<BM, BN, WM, WN, STAGES, W> S;
   constexpr int AM = S::AM, AN = S::AN;
   __shared__ __align__(16) unsigned char lds[S::LDS];
   f16* ring = reinterpret_cast<f16*>(lds);
@@ -78,17 +81,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
   const TileAt at = tile_at(blockIdx.x - share * tiles, a.mtiles, a.ntiles);
   const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
   const int wm = (wave % WM) * S::TM, wn = (wave / WM) * S::TN;
-  TilePlan<BM, S::NW, 32> px;
-  TilePlan<BN, S::NW, 32> pw;
+  TilePlan<BM, S::NW, W> px;
+  TilePlan<BN, S::NW, W> pw;
   px.init(reinterpret_cast<const f16*>(a.x), a.K / 2, m0, a.M, wave, lane);
   pw.init(reinterpret_cast<const f16*>(a.w), a.K / 2, n0, a.N, wave, lane);
-  const int all = (int)(a.K / 64), first = (int)((int64_t)all * share / a.splits);
+  const int all = (int)(a.K / (2 * W)), first = (int)((int64_t)all * share / a.splits);
   const int steps = (int)((int64_t)all * (share + 1) / a.splits) - first;  // splits <= all
   auto issue = [&](int s) {
     f16* stage = ring + (s % STAGES) * S::STAGE;
-    const int64_t k = (int64_t)(first + (s < steps ? s : steps - 1)) * 32;  // past the end: counted, never used
+    const int64_t k = (int64_t)(first + (s < steps ? s : steps - 1)) * W;  // past the end: counted, never used
     px.issue(stage, k);
-    pw.issue(stage + BM * 32, k);
+    pw.issue(stage + BM * W, k);
   };
   i32x16 acc[AN][AM];
 #pragma unroll
@@ -96,15 +99,18 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
 #pragma unroll
     for (int j = 0; j < AM; ++j) acc[i][j] = i32x16{};
   i32x4 fa[2][AN], fb[2][AM];
+  auto piece = [](const f16* tile, int r, int c) {
+    return __builtin_bit_cast(i32x4, W == 32 ? frag32(tile, r, c) : frag(tile, r, c));
+  };
   auto read = [&](int s, int c, int into) {
     const f16* tx = ring + (s % STAGES) * S::STAGE;
-    const f16* tw = tx + BM * 32;
+    const f16* tw = tx + BM * W;
 #pragma unroll
     for (int i = 0; i < AN; ++i)
-      fa[into][i] = __builtin_bit_cast(i32x4, frag32(tw, wn + i * 32 + (lane & 31), 2 * c + (lane >> 5)));
+      fa[into][i] = piece(tw, wn + i * 32 + (lane & 31), 2 * c + (lane >> 5));
 #pragma unroll
     for (int j = 0; j < AM; ++j)
-      fb[into][j] = __builtin_bit_cast(i32x4, frag32(tx, wm + j * 32 + (lane & 31), 2 * c + (lane >> 5)));
+      fb[into][j] = piece(tx, wm + j * 32 + (lane & 31), 2 * c + (lane >> 5));
   };
   auto multiply = [&](int from) {
 #pragma unroll
@@ -122,10 +128,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Args a) {
     wait_vmcnt<(STAGES - 3) * S::LOADS>();  // stage s + 1
     lds_barrier();
     issue(s + STAGES - 1);  // into stage s - 1
-    read(s, 1, 1);
-    multiply(0);
-    read(s + 1, 0, 0);
-    multiply(1);
+#pragma unroll
+    for (int c = 0; c < S::SUB; ++c) {
+      if (c + 1 < S::SUB) read(s, c + 1, (c + 1) & 1);
+      else read(s + 1, 0, 0);
+      multiply(c & 1);
+    }
   }
   wait_vmcnt<0>();  // the loads past the end
   lds_barrier();
@@ -220,14 +228,14 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
   int token[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) token[t] = t * 16 + row < M ? t * 16 + row : M - 1;  // the others' sums are not stored
-  // chunks past the end of a row: the last one, whose product is not taken
   auto chunk = [&](int b, int d) { return wave + (b * DEPTH + d) * NW; };
   auto fetch = [&](int g, int b, Batch& to) {
     const int64_t n = (int64_t)g * 16 + row;
     const int8_t* w = a.w + (n < a.N ? n : a.N - 1) * a.K + off;
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      const int c = chunk(b, d) < chunks ? chunk(b, d) : chunks - 1;
+      const int c = chunk(b, d);
+      if (c >= chunks) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         to.w[d][h] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(w + (int64_t)c * 128) + h);
@@ -330,36 +338,44 @@ static size_t rows_bytes(int64_t M, int64_t K) { return ((size_t)M * (size_t)K +
 // One fp16 row is quantised by the product itself, up to this many codes (its LDS).
 static bool i8_fused(int64_t M, int64_t K, bool quantized) { return !quantized && M == 1 && K <= 32768; }
 
-// The kernel for these sizes: the one of least estimated time, in us, by what was measured on an MI355X
-// over N x K = 4096 x 4096 .. 28672 x 8192 and 1408 x 2048, M = 1 .. 1024 (estimates within 15 %):
-//   few tokens: the weights at 4.5 TB/s up to 8 tokens, 3.8 to 16, 2.75 to 32, 1.65 to 64 (the rows' codes
-//     come from the L2 once for each 16 channels);
-//   tiles of BM x 128 (256 x 256): the weights at 6 TB/s, and a block's step of 64 bytes of K in 0.19, 0.21,
-//     0.32, 0.93 us at BM = 32, 64, 128, 256, a compute unit's blocks one after the other;
-//   shares of K: 2.5 us for the join and its traffic at 4 TB/s.
-// E.g. 77 x 4096 x 11008: BM = 64, 4 shares: 17.3 us (1 share 38, BM = 128 with 6 shares 18.2); 32 x 50021 x
-// 4096: BM = 32: 35.9 us (few tokens' kernel 82); 8 x 4096 x 4096: few tokens' kernel 6.4 us (BM = 32: 9.1).
+// The kernel for these sizes: the one of least estimated time, in us.  The numbers are fitted to 1300
+// times measured on an MI355X with the weights out of the caches, over N x K = 700 x 512 .. 50021 x 4096
+// and 28672 x 8192, M = 1 .. 5000; the kernel picked is on average 2 % slower than the best.  E.g.
+//   8 x 4096 x 4096:   few tokens' kernel 6.1, 32 x 64 tiles with 4 shares 10.0
+//   32 x 50021 x 4096: few tokens' kernel 82, 32 x 128 tiles 49.6, 64 x 128 52.7
+//   77 x 4096 x 11008: 64 x 64 tiles with 4 shares 20.5, 128 x 128 with 8 19.4, with 1 share 38
+//   512 x 28672 x 8192: 256 x 256 tiles 135, 128 x 128 168
 struct I8Plan {
-  int tile;    // tokens of a tile; 0: the kernel for few tokens
+  int tile;    // index of kI8Tiles; -1: the kernel for few tokens
   int splits;  // shares of K
 };
+struct I8Tile {
+  int tokens, channels;
+  double start, step;  // before the first and after the last stage; 128 bytes of K
+};
+constexpr I8Tile kI8Tiles[] = {{32, 64, 5.0, 0.28},   {32, 128, 4.6, 0.48},  {64, 64, 5.7, 0.32},
+                               {64, 128, 6.4, 0.60}, {128, 128, 6.4, 0.68}, {256, 256, 9.0, 1.85}};
 static I8Plan i8_plan(int64_t M, int64_t N, int64_t K, bool quantized) {
-  const double launch = 3.0, weights = (double)N * (double)K * 1e-6;  // MB
-  I8Plan best{0, 1};
+  const double weights = (double)N * (double)K * 1e-6;  // MB, streamed at TB/s
+  I8Plan best{-1, 1};
   double least = 1e30;
-  if (M <= 64) least = launch + weights / (M <= 8 ? 4.5 : M <= 16 ? 3.8 : M <= 32 ? 2.75 : 1.65);
-  const double rows = i8_fused(M, K, quantized) ? launch : 0.0;  // the rows' own launch, which that kernel saves
-  const int64_t steps = K / 64;
-  for (const int tile : {32, 64, 128, 256}) {
-    const int64_t tiles = ((M + tile - 1) / tile) * ((N + (tile == 256 ? 255 : 127)) / (tile == 256 ? 256 : 128));
-    const double step = tile == 32 ? 0.19 : tile == 64 ? 0.21 : tile == 128 ? 0.32 : 0.93;
-    for (int splits = 1; splits == 1 || (splits <= 16 && splits * 4 <= steps && tiles * splits <= 1024); ++splits) {
-      const int64_t rounds = (tiles * splits + 255) / 256, share = (steps + splits - 1) / splits;
-      double us = launch + rows + fmax(weights / 6.0, (double)rounds * (double)share * step);
-      if (splits > 1) us += 2.5 + (double)splits * (double)M * (double)N * 8e-6 / 4.0;
+  if (M <= 64)  // the rows' codes come from the L2 once for each 16 channels
+    least = 4.3 + fmax(weights / (M <= 8 ? 4.5 : M <= 16 ? 3.9 : M <= 32 ? 3.2 : 1.85),
+                       (double)K / 1024 * 0.44 * (M <= 16 ? 1 : M <= 32 ? 2 : 4));
+  const double rows = i8_fused(M, K, quantized) ? 3.0 : 0.0;  // the rows' own launch, which that kernel saves
+  const int64_t steps = K / 128;
+  for (int i = 0; i < (int)(sizeof(kI8Tiles) / sizeof(kI8Tiles[0])); ++i) {
+    const I8Tile& t = kI8Tiles[i];
+    const int64_t tiles = ((M + t.tokens - 1) / t.tokens) * ((N + t.channels - 1) / t.channels);
+    for (int splits = 1; splits == 1 || (splits <= 8 && splits * 2 <= steps && tiles * splits <= 1024); ++splits) {
+      // blocks of a compute unit one after the other; small ones share it more evenly
+      const double blocks = (double)(tiles * splits) / 256.0;
+      const double rounds = t.tokens == 256 ? ceil(blocks) : blocks <= 1.0 ? 1.0 : blocks + 0.3;
+      double us = rows + t.start + fmax(weights / 4.7, rounds * (double)((steps + splits - 1) / splits) * t.step);
+      if (splits > 1) us += 1.6 + 0.21 * (double)splits * (double)M * (double)N * 8e-6;  // the join
       if (us < least) {
         least = us;
-        best = {tile, splits};
+        best = {i, splits};
       }
     }
   }
@@ -369,28 +385,29 @@ static I8Plan i8_plan(int64_t M, int64_t N, int64_t K, bool quantized) {
 size_t gemm_i8_workspace(int64_t M, int64_t N, int64_t K, bool quantized) {
   const I8Plan plan = i8_plan(M, N, K, quantized);
   size_t bytes = plan.splits > 1 ? (size_t)plan.splits * (size_t)M * (size_t)partial_pitch(N) * 4 : 0;
-  if (!quantized && !(plan.tile == 0 && i8_fused(M, K, quantized)))
+  if (!quantized && !(plan.tile < 0 && i8_fused(M, K, quantized)))
     bytes += rows_bytes(M, K) + ((size_t)M * 4 + 255) / 256 * 256;
   return (bytes + 255) / 256 * 256;
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES>
+template <int BM, int BN, int WM, int WN, int STAGES, int W>
 static hipError_t tile_launch(I8Args a, int y_bytes, hipStream_t st) {
+  if (a.splits < 1 || a.splits > a.K / (2 * W)) return hipErrorInvalidValue;  // a share has a stage at least
   a.mtiles = (int)((a.M + BM - 1) / BM);
   a.ntiles = (int)((a.N + BN - 1) / BN);
   const dim3 grid((unsigned)(a.mtiles * a.ntiles * a.splits)), block(64 * WM * WN);
   if (KernelPlan* p = active_plan())
-    return plan_record(p, "gemm_i8_kernel<%d,%d,%d,%d,%d> block=%u grid=%u shares=%d", BM, BN, WM, WN, STAGES, block.x,
+    return plan_record(p, "gemm_i8_kernel<%d,%d,%d,%d,%d,%d> block=%u grid=%u shares=%d", BM, BN, WM, WN, STAGES, W, block.x,
                        grid.x, a.splits);
   if (a.splits > 1) {
-    gemm_i8_kernel<BM, BN, WM, WN, STAGES, int32_t><<<grid, block, 0, st>>>(a);
+    gemm_i8_kernel<BM, BN, WM, WN, STAGES, W, int32_t><<<grid, block, 0, st>>>(a);
     const dim3 join((unsigned)((a.M * (partial_pitch(a.N) / 4) + 255) / 256));
     if (y_bytes == 2) gemm_i8_join_kernel<f16><<<join, dim3(256), 0, st>>>(a);
     else gemm_i8_join_kernel<float><<<join, dim3(256), 0, st>>>(a);
   } else if (y_bytes == 2) {
-    gemm_i8_kernel<BM, BN, WM, WN, STAGES, f16><<<grid, block, 0, st>>>(a);
+    gemm_i8_kernel<BM, BN, WM, WN, STAGES, W, f16><<<grid, block, 0, st>>>(a);
   } else {
-    gemm_i8_kernel<BM, BN, WM, WN, STAGES, float><<<grid, block, 0, st>>>(a);
+    gemm_i8_kernel<BM, BN, WM, WN, STAGES, W, float><<<grid, block, 0, st>>>(a);
   }
   return hipGetLastError();
 }
@@ -418,7 +435,7 @@ static hipError_t skinny_dispatch(const I8Args& a, bool fused, int y_bytes, hipS
 hipError_t launch_gemm_i8(const void* x, const float* x_scales, const float* s, const void* codes, const float* scales,
                           void* y, int y_bytes, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t st) {
   const I8Plan plan = i8_plan(M, N, K, x_scales != nullptr);
-  const bool fused = plan.tile == 0 && i8_fused(M, K, x_scales != nullptr);
+  const bool fused = plan.tile < 0 && i8_fused(M, K, x_scales != nullptr);
   int8_t* scratch = reinterpret_cast<int8_t*>(ws);
   if (x_scales == nullptr && !fused && active_plan() == nullptr) {
     float* sc = reinterpret_cast<float*>(scratch + rows_bytes(M, K));
@@ -431,11 +448,13 @@ hipError_t launch_gemm_i8(const void* x, const float* x_scales, const float* s, 
   const I8Args a{reinterpret_cast<const int8_t*>(x), x_scales, reinterpret_cast<const int8_t*>(codes), scales, y, M, N, K, s,
                  0, 0, plan.splits, reinterpret_cast<int32_t*>(scratch)};
   switch (plan.tile) {
-    case 0: return skinny_dispatch(a, fused, y_bytes, st);
-    case 32: return tile_launch<32, 128, 1, 2, 8>(a, y_bytes, st);
-    case 64: return tile_launch<64, 128, 1, 4, 6>(a, y_bytes, st);
-    case 128: return tile_launch<128, 128, 2, 2, 4>(a, y_bytes, st);
-    default: return tile_launch<256, 256, 4, 2, 4>(a, y_bytes, st);
+    case -1: return skinny_dispatch(a, fused, y_bytes, st);
+    case 0: return tile_launch<32, 64, 1, 2, 6, 64>(a, y_bytes, st);
+    case 1: return tile_launch<32, 128, 1, 4, 4, 64>(a, y_bytes, st);
+    case 2: return tile_launch<64, 64, 1, 2, 5, 64>(a, y_bytes, st);
+    case 3: return tile_launch<64, 128, 1, 4, 3, 64>(a, y_bytes, st);
+    case 4: return tile_launch<128, 128, 2, 4, 4, 64>(a, y_bytes, st);
+    default: return tile_launch<256, 256, 4, 2, 4, 32>(a, y_bytes, st);
   }
 }
 
