@@ -61,9 +61,21 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
   const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * ROWS + threadIdx.x / L;
   if (t >= a.T) return;  // a whole wave of its own row (L = 64) or the whole block
   const bool layer = a.kind == AWQ_NORM_LAYER;
+  // With one eight a thread and wide rows everything is under way before the first join: 16384 x 8192 with
+  // post-norm and gate 232 us, 247 with each vector read where it is used (x 4096: 106 and 111).  Otherwise
+  // the registers cost more than the wait (16000 x 1024: 28.0 and 25.9; 4000 x 16384: 146 and 131).
+  constexpr bool EARLY = PER == 1 && L >= 512;
   bool live[PER];
   int64_t at[PER];
   f32x8 h[PER];
+  f16x8 w_early[PER], pw_early[PER], g_early[PER];
+  auto part_of = [&](const f16* v, int p) {
+    return v != nullptr && live[p] ? *reinterpret_cast<const f16x8*>(v + at[p]) : f16x8{};
+  };
+  int64_t row = a.gates > 1 ? t : 0;
+  if (a.gate_rows != nullptr) row = a.gate_rows[t];
+  const bool adds = a.gate == nullptr || (row >= 0 && row < a.gates);
+  const f16* gate = adds && a.gate != nullptr ? a.gate + row * a.N : nullptr;
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     at[p] = (int64_t)(p * L + lane) * 8;
@@ -79,44 +91,46 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
       y[p] = f32x8{};
       if (live[p]) y[p] = widen(*reinterpret_cast<const f16x8*>(a.y + t * a.y_stride + at[p]));
     }
+    if constexpr (EARLY)
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        pw_early[p] = part_of(a.post_weight, p);
+        g_early[p] = part_of(gate, p);
+        w_early[p] = part_of(a.weight, p);
+      }
     if (a.post_weight != nullptr) {
       statistics<L>(y, live, a.N, layer, a.eps, part, &mean, &r);
 #pragma unroll
-      for (int p = 0; p < PER; ++p)
-        if (live[p]) {
-          const f32x8 w = widen(*reinterpret_cast<const f16x8*>(a.post_weight + at[p]));
-          y[p] = (y[p] - mean) * r * w;
-          if (a.post_bias != nullptr) y[p] += widen(*reinterpret_cast<const f16x8*>(a.post_bias + at[p]));
-        }
+      for (int p = 0; p < PER; ++p) {
+        y[p] = (y[p] - mean) * r * widen(EARLY ? pw_early[p] : part_of(a.post_weight, p));
+        if (a.post_bias != nullptr) y[p] += widen(part_of(a.post_bias, p));
+      }
     }
-    int64_t row = a.gates > 1 ? t : 0;
-    if (a.gate_rows != nullptr) row = a.gate_rows[t];
-    const bool adds = a.gate == nullptr || (row >= 0 && row < a.gates);
 #pragma unroll
     for (int p = 0; p < PER; ++p)
       if (live[p]) {
         f32x8 g = f32x8{} + a.scale;
-        if (a.gate != nullptr && adds) g = widen(*reinterpret_cast<const f16x8*>(a.gate + row * a.N + at[p])) * a.scale;
+        if (gate != nullptr) g *= widen(EARLY ? g_early[p] : part_of(gate, p));
         if (adds) h[p] += y[p] * g;
         const HV kept = __builtin_convertvector(h[p], HV);
         h[p] = as_f32(kept);
         *reinterpret_cast<HV*>(reinterpret_cast<H*>(a.h_out) + t * a.N + at[p]) = kept;
       }
+  } else if constexpr (EARLY) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p) w_early[p] = part_of(a.weight, p);
   }
   if (a.weight == nullptr) return;
   statistics<L>(h, live, a.N, layer, a.eps, part + 2 * W, &mean, &r);
   f32x8 w[PER];
 #pragma unroll
-  for (int p = 0; p < PER; ++p) {
-    w[p] = f32x8{};
-    if (live[p]) w[p] = widen(*reinterpret_cast<const f16x8*>(a.weight + at[p]));
-  }
+  for (int p = 0; p < PER; ++p) w[p] = widen(EARLY ? w_early[p] : part_of(a.weight, p));
   if (a.x_scales == nullptr) {
 #pragma unroll
     for (int p = 0; p < PER; ++p)
       if (live[p]) {
         f32x8 x = (h[p] - mean) * r * w[p];
-        if (a.bias != nullptr) x += widen(*reinterpret_cast<const f16x8*>(a.bias + at[p]));
+        if (a.bias != nullptr) x += widen(part_of(a.bias, p));
         *reinterpret_cast<f16x8*>(reinterpret_cast<f16*>(a.x) + t * a.N + at[p]) = __builtin_convertvector(x, f16x8);
       }
     return;

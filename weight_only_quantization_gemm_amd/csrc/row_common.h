@@ -39,9 +39,14 @@ __device__ __forceinline__ float row_join(float v, float* part, Op op) {
   if constexpr (L > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     lds_barrier();
-    v = part[0];
+    if constexpr (L <= 256) {
+      v = part[0];
 #pragma unroll
-    for (int w = 1; w < L / 64; ++w) v = op(v, part[w]);
+      for (int w = 1; w < L / 64; ++w) v = op(v, part[w]);
+    } else {  // a lane for each wave's: one access and six steps instead of an access for each
+      const int lane = threadIdx.x & 63;
+      v = wave_join(lane < L / 64 ? part[lane] : 0.f, op);
+    }
   }
   return v;
 }
