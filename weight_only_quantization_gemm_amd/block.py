@@ -15,22 +15,36 @@ import torch
 
 from ._lib import check, load
 from .api import _need
-from .serve import _like, _run, _scratch
+from .serve import _like, _raw_stream, _scratch
 
 NORM_KINDS = ("rms", "layer")
 
-_FLOATS = (torch.float16, torch.float32)
+_F16, _F32, _I32, _I8 = torch.float16, torch.float32, torch.int32, torch.int8
+_FLOATS = (_F16, _F32)
+
+_current_device = torch._C._cuda_getDevice  # of the calling thread
 
 
-def _matrix(t: torch.Tensor, name: str, dtypes, index: Optional[int]):
-    """(rows, columns, elements from one row to the next) of a GPU matrix of one of the dtypes whose
-    rows are contiguous; any stride between rows (a single row has no next)."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda or t.dim() != 2:
+def _run(index: int, fn, *args) -> None:
+    """fn(*args, stream) with the device current and its current stream; raises on a status."""
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        check(status)
+
+
+def _matrix(t: torch.Tensor, name: str, dtypes, index: int):
+    """(rows, columns, elements from one row to the next) of a matrix of one of the dtypes on the given device
+    (-1: any GPU) whose rows are contiguous; any stride between rows (a single row has no next)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda:
         if isinstance(t, torch.Tensor) and t.dtype not in dtypes:
             raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
         _need(t, name, dtypes[0], 2)
         raise ValueError(f"{name} must be a GPU matrix")
-    if index is not None and t.get_device() != index:
+    if index >= 0 and t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     T, N = t.shape
     row, column = t.stride()
@@ -39,19 +53,15 @@ def _matrix(t: torch.Tensor, name: str, dtypes, index: Optional[int]):
     return T, N, row if T > 1 else N
 
 
-def _vector(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int, index: int):
-    """The pointer of a vector of n, or None."""
-    if t is None:
-        return None
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, index: int) -> int:
+    """The pointer of a vector of n."""
     _like(t, name, dtype, 1, index)
     if t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
     return t.data_ptr()
 
 
-def _output(out: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype: torch.dtype, index: int):
-    if out is None:
-        return like.new_empty(shape, dtype=dtype)
+def _output(out: torch.Tensor, name: str, shape, dtype: torch.dtype, index: int) -> torch.Tensor:
     _like(out, name, dtype, len(shape), index)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
@@ -73,45 +83,59 @@ def awq_norm(h: torch.Tensor, weight: Optional[torch.Tensor] = None, y: Optional
     Returns a dict: "h", the new residual stream (with y; in h_out where given, which may be h itself);
     "x" (with weight), fp16, or with quantize (rms, no bias) the rows in 8 bits that awq_gemm_i8
     takes as x and x_scales: int8 "x" and fp32 "scales"."""
-    T, N, h_stride = _matrix(h, "h", _FLOATS, None)
+    T, N, h_stride = _matrix(h, "h", _FLOATS, -1)
     index = h.get_device()
-    if kind not in NORM_KINDS:
-        raise ValueError(f"kind must be one of {NORM_KINDS}, got {kind!r}")
-    y_stride, gates, out = 0, 0, {}
-    h_ptr = y_ptr = x_ptr = scales_ptr = gate_ptr = rows_ptr = None
+    y_stride = gates = 0
+    h_ptr = y_ptr = x_ptr = scales_ptr = gate_ptr = rows_ptr = w_ptr = b_ptr = pw_ptr = pb_ptr = None
+    out = {}
     if y is not None:
-        Ty, Ny, y_stride = _matrix(y, "y", (torch.float16,), index)
+        Ty, Ny, y_stride = _matrix(y, "y", (_F16,), index)
         if Ty != T or Ny != N:
             raise ValueError(f"y must be [{T}][{N}], got {tuple(y.shape)}")
         y_ptr = y.data_ptr()
-        new = out["h"] = _output(h_out, "h_out", h, (T, N), h.dtype, index)
-        h_ptr = new.data_ptr()
-    elif h_out is not None:
-        raise ValueError("h_out is only for a call with y")
+        if h_out is None:
+            h_out = torch.empty_like(h) if h_stride == N else h.new_empty((T, N))
+        else:
+            _output(h_out, "h_out", (T, N), h.dtype, index)
+        out["h"] = h_out
+        h_ptr = h_out.data_ptr()
+        if post_weight is not None:
+            pw_ptr = _vector(post_weight, "post_weight", _F16, N, index)
+    elif h_out is not None or post_weight is not None:
+        raise ValueError("h_out and post_weight are only for a call with y")
+    if post_bias is not None:
+        pb_ptr = _vector(post_bias, "post_bias", _F16, N, index)
     if gate is not None:
         if isinstance(gate, torch.Tensor) and gate.dim() == 1:
-            gate_ptr, gates = _vector(gate, "gate", torch.float16, N, index), 1
+            gate_ptr, gates = _vector(gate, "gate", _F16, N, index), 1
         else:
-            _like(gate, "gate", torch.float16, 2, index)
+            _like(gate, "gate", _F16, 2, index)
             gates = gate.shape[0]
             if gate.shape[1] != N:
                 raise ValueError(f"gate must have {N} columns, got {gate.shape[1]}")
             gate_ptr = gate.data_ptr()
     if gate_rows is not None:
-        rows_ptr = _vector(gate_rows, "gate_rows", torch.int32, T, index)
+        rows_ptr = _vector(gate_rows, "gate_rows", _I32, T, index)
     if weight is not None:
-        x = out["x"] = h.new_empty((T, N), dtype=torch.int8 if quantize else torch.float16)
+        w_ptr = _vector(weight, "weight", _F16, N, index)
+        x = out["x"] = (torch.empty_like(y) if y_stride == N and not quantize else
+                        h.new_empty((T, N), dtype=_I8 if quantize else _F16))
         x_ptr = x.data_ptr()
         if quantize:
-            scales = out["scales"] = h.new_empty(T, dtype=torch.float32)
+            scales = out["scales"] = h.new_empty(T, dtype=_F32)
             scales_ptr = scales.data_ptr()
     elif quantize:
         raise ValueError("quantize needs weight")
-    half = torch.float16
-    _run(index, load().awq_norm, h.data_ptr(), h.element_size(), h_stride, y_ptr, y_stride,
-         _vector(post_weight, "post_weight", half, N, index), _vector(post_bias, "post_bias", half, N, index),
-         gate_ptr, rows_ptr, gates, scale, _vector(weight, "weight", half, N, index), _vector(bias, "bias", half, N, index),
-         NORM_KINDS.index(kind), eps, h_ptr, x_ptr, scales_ptr, T, N)
+    if bias is not None:
+        b_ptr = _vector(bias, "bias", _F16, N, index)
+    if kind == "rms":
+        layer = 0
+    elif kind in NORM_KINDS:
+        layer = 1
+    else:
+        raise ValueError(f"kind must be one of {NORM_KINDS}, got {kind!r}")
+    _run(index, load().awq_norm, h.data_ptr(), h.element_size(), h_stride, y_ptr, y_stride, pw_ptr, pb_ptr, gate_ptr, rows_ptr,
+         gates, scale, w_ptr, b_ptr, layer, eps, h_ptr, x_ptr, scales_ptr, T, N)
     return out
 
 
@@ -119,10 +143,10 @@ def awq_norm(h: torch.Tensor, weight: Optional[torch.Tensor] = None, y: Optional
 def awq_quantize_rows(x: torch.Tensor, s: Optional[torch.Tensor] = None):
     """The rows of x (fp16 [M][K], strided rows allowed), or of x / s (fp32 [K]), in 8 bits: int8 codes
     [M][K] and fp32 scales [M], a row standing for code * scale."""
-    M, K, stride = _matrix(x, "x", (torch.float16,), None)
+    M, K, stride = _matrix(x, "x", (_F16,), -1)
     index = x.get_device()
-    codes, scales = x.new_empty((M, K), dtype=torch.int8), x.new_empty(M, dtype=torch.float32)
-    _run(index, load().awq_quantize_rows, x.data_ptr(), stride, _vector(s, "s", torch.float32, K, index), M, K,
+    codes, scales = x.new_empty((M, K), dtype=_I8), x.new_empty(M, dtype=_F32)
+    _run(index, load().awq_quantize_rows, x.data_ptr(), stride, None if s is None else _vector(s, "s", _F32, K, index), M, K,
          codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
@@ -132,8 +156,8 @@ def awq_pack_i8(W: torch.Tensor, s: Optional[torch.Tensor] = None):
     _need(W, "W", torch.float16, 2)
     index = W.get_device()
     N, K = W.shape
-    codes, scales = W.new_empty((N, K), dtype=torch.int8), W.new_empty(N, dtype=torch.float32)
-    _run(index, load().awq_pack_i8, W.data_ptr(), _vector(s, "s", torch.float32, K, index), N, K, codes.data_ptr(),
+    codes, scales = W.new_empty((N, K), dtype=_I8), W.new_empty(N, dtype=_F32)
+    _run(index, load().awq_pack_i8, W.data_ptr(), None if s is None else _vector(s, "s", _F32, K, index), N, K, codes.data_ptr(),
          scales.data_ptr())
     return codes, scales
 
@@ -150,24 +174,26 @@ def awq_gemm_i8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, x_sc
     [M][K] with x_scales fp32 [M] (awq_quantize_rows, awq_norm), or fp16 [M][K], which is quantised on
     the way, divided by s (fp32 [K]) first where given."""
     quantized = x_scales is not None
-    _need(x, "x", torch.int8 if quantized else torch.float16, 2)
+    _need(x, "x", _I8 if quantized else _F16, 2)
     index = x.get_device()
-    _like(codes, "codes", torch.int8, 2, index)
+    _like(codes, "codes", _I8, 2, index)
     M, K = x.shape
-    N = codes.shape[0]
-    if codes.shape[1] != K:
-        raise ValueError(f"codes are of rows of {codes.shape[1]}, x of {K}")
-    if out is not None and isinstance(out, torch.Tensor):
-        dtype = out.dtype
-    if dtype not in _FLOATS:
-        raise TypeError(f"y must be float16 or float32, got {dtype}")
-    y = _output(out, "out", x, (M, N), dtype, index)
+    N, Kw = codes.shape
+    if Kw != K:
+        raise ValueError(f"codes are of rows of {Kw}, x of {K}")
+    if out is None:
+        if dtype not in _FLOATS:
+            raise TypeError(f"y must be float16 or float32, got {dtype}")
+        out = x.new_empty((M, N), dtype=dtype)
+    else:
+        dtype = out.dtype if isinstance(out, torch.Tensor) and out.dtype in _FLOATS else _F16
+        _output(out, "out", (M, N), dtype, index)
     lib = load()
     ws, ws_bytes, _keep = _scratch(workspace, lib.awq_gemm_i8_workspace_bytes(M, N, K, quantized), x.device)
-    _run(index, lib.awq_gemm_i8, x.data_ptr(), _vector(x_scales, "x_scales", torch.float32, M, index),
-         _vector(s, "s", torch.float32, K, index), codes.data_ptr(), _vector(scales, "scales", torch.float32, N, index),
-         y.data_ptr(), y.element_size(), M, N, K, ws, ws_bytes)
-    return y
+    _run(index, lib.awq_gemm_i8, x.data_ptr(), _vector(x_scales, "x_scales", _F32, M, index) if quantized else None,
+         None if s is None else _vector(s, "s", _F32, K, index), codes.data_ptr(), _vector(scales, "scales", _F32, N, index),
+         out.data_ptr(), out.element_size(), M, N, K, ws, ws_bytes)
+    return out
 
 
 def awq_gemm_i8_kernel(M: int, N: int, K: int, quantized: bool = True) -> str:
@@ -199,19 +225,18 @@ def awq_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, 
     share, in index order, first exceeds u.  Each setting is one number, or a tensor with one for each
     row (fp32; top_k int32).  Returns a dict: int32 "tokens" [B] (-1 where every logit is -inf or NaN)
     and fp32 "probs" [B], the token's share of the remaining weights."""
-    B, V, stride = _matrix(logits, "logits", _FLOATS, None)
+    B, V, stride = _matrix(logits, "logits", _FLOATS, -1)
     index = logits.get_device()
-    f32 = torch.float32
-    t_ptr, t = _setting(temperature, "temperature", f32, B, index)
-    k_ptr, k = _setting(top_k, "top_k", torch.int32, B, index)
-    p_ptr, p = _setting(top_p, "top_p", f32, B, index)
-    m_ptr, m = _setting(min_p, "min_p", f32, B, index)
-    tokens, probs = logits.new_empty(B, dtype=torch.int32), logits.new_empty(B, dtype=f32)
+    t_ptr, t = _setting(temperature, "temperature", _F32, B, index)
+    k_ptr, k = _setting(top_k, "top_k", _I32, B, index)
+    p_ptr, p = _setting(top_p, "top_p", _F32, B, index)
+    m_ptr, m = _setting(min_p, "min_p", _F32, B, index)
+    tokens, probs = logits.new_empty(B, dtype=_I32), logits.new_empty(B, dtype=_F32)
     lib = load()
     size = logits.element_size()
     ws, ws_bytes, _keep = _scratch(workspace, lib.awq_sample_workspace_bytes(B, V, size), logits.device)
     _run(index, lib.awq_sample, logits.data_ptr(), size, stride, B, V, t_ptr, t, k_ptr, k, p_ptr, p, m_ptr, m,
-         _vector(u, "u", f32, B, index), tokens.data_ptr(), probs.data_ptr(), ws, ws_bytes)
+         _vector(u, "u", _F32, B, index), tokens.data_ptr(), probs.data_ptr(), ws, ws_bytes)
     return dict(tokens=tokens, probs=probs)
 
 
