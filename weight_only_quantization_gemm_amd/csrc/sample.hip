@@ -21,22 +21,29 @@
 namespace awq {
 
 constexpr double kWeightOne = 8796093022208.0;  // 2^43
-constexpr int kBins = 2048, kList = 2048, kExpTable = 512, kSlots = 16;
+constexpr int kExpTable = 512, kSlots = 16;
 constexpr double kExpRate = 738.6598609351493;  // kExpTable log2(e)
 
-// 2^(43 + j / kExpTable), by the series of the exponential
-struct ExpTable {
-  double at[kExpTable];
-  constexpr ExpTable() : at() {
-    for (int j = 0; j < kExpTable; ++j) {
-      const double x = 0.69314718055994530942 * j / kExpTable;
-      double sum = 1.0, term = 1.0;
-      for (int i = 1; i < 24; ++i) sum += term *= x / i;
-      at[j] = kWeightOne * sum;
-    }
-  }
-};
-__device__ constexpr ExpTable kExp;
+// 2^(43 + j / kExpTable), 0 <= j < kExpTable: the series of the exponential about 0 to the 12th power, whose next
+// term is below 2^-52 for the nearer whole power of 2.
+__device__ __forceinline__ double exp_entry(int j) {
+  const bool upper = j >= kExpTable / 2;
+  const double x = (upper ? j - kExpTable : j) * (0.69314718055994530942 / kExpTable);
+  double sum = 1.0 / 479001600.0;  // 1 / 12!
+  sum = fma(sum, x, 1.0 / 39916800.0);
+  sum = fma(sum, x, 1.0 / 3628800.0);
+  sum = fma(sum, x, 1.0 / 362880.0);
+  sum = fma(sum, x, 1.0 / 40320.0);
+  sum = fma(sum, x, 1.0 / 5040.0);
+  sum = fma(sum, x, 1.0 / 720.0);
+  sum = fma(sum, x, 1.0 / 120.0);
+  sum = fma(sum, x, 1.0 / 24.0);
+  sum = fma(sum, x, 1.0 / 6.0);
+  sum = fma(sum, x, 0.5);
+  sum = fma(sum, x, 1.0);
+  sum = fma(sum, x, 1.0);
+  return sum * (upper ? 2.0 * kWeightOne : kWeightOne);
+}
 
 // Order-preserving image of a logit (never 0 for one that can be chosen: not -inf, not NaN).
 __device__ __forceinline__ uint32_t logit_key(float v) {
@@ -85,9 +92,10 @@ __device__ __forceinline__ float wave_min(float v) { return -wave_max(-v); }
 
 template <int THREADS>
 struct SampleShared {
+  static constexpr int kList = 2 * THREADS, kBins = 2 * THREADS;
   uint64_t list[kList];     // entries, or the bins' weights
   uint32_t counts[kBins];   // the bins' counts, or candidates
-  double table[kExpTable];  // kExp
+  double table[kExpTable];  // exp_entry
   uint64_t part[2][THREADS / 64];
   uint64_t found[4];
   float most[THREADS / 64], least[THREADS / 64];
@@ -106,6 +114,7 @@ struct Border {
 template <typename T, int THREADS>
 struct SampleRow {
   static constexpr int E = 16 / sizeof(T), WAVES = THREADS / 64;
+  static constexpr int kList = SampleShared<THREADS>::kList, kBins = SampleShared<THREADS>::kBins;
   typedef T vec __attribute__((ext_vector_type(E)));
   SampleShared<THREADS>& sh;
   __amdgpu_buffer_rsrc_t resource;  // from the 16-byte piece with the row's first element to the row's end
@@ -113,21 +122,24 @@ struct SampleRow {
   bool infinite;     // some logit is +inf: those weigh 1 and all others nothing
   double top, rate;  // largest logit, kExpTable log2(e) / temperature
 
-  // Piece j: elements j E - lead .. + E - 1, NaN outside the row.  Read with the hardware's bound at
-  // the row's end (a half's word there may hold the next half too); before the row's start there are
-  // only other rows, whose elements become NaN like those behind.
-  __device__ __forceinline__ vec load(int j) const {
-    vec x = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(resource, j * 16, 0, 0));
-    const int first = j * E - lead;
-    if (first < 0 || first + E > V) {
+  // Piece j: elements j E - lead .. + E - 1.  Read with the hardware's bound at the row's end (a half's word there
+  // may hold the next half too); before the row's start there are only other rows.
+  __device__ __forceinline__ vec read(int j) const {
+    return __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(resource, j * 16, 0, 0));
+  }
+  __device__ __forceinline__ bool whole(int j) const { return j * E >= lead && (j + 1) * E - lead <= V; }
+  // The elements outside the row become NaN.
+  __device__ __forceinline__ vec trim(vec x, int j) const {
+    if (!whole(j)) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = first + e >= 0 && first + e < V ? x[e] : (T)__builtin_nanf("");
+      for (int e = 0; e < E; ++e) x[e] = j * E + e >= lead && j * E + e - lead < V ? x[e] : (T)__builtin_nanf("");
     }
     if (infinite)
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] = (float)x[e] == INFINITY ? (T)0.f : (T)-INFINITY;
     return x;
   }
+  __device__ __forceinline__ vec load(int j) const { return trim(read(j), j); }
   __device__ __forceinline__ int piece(int u) const { return ((int)(threadIdx.x >> 6) * cw + u) * 64 + (threadIdx.x & 63); }
   static __device__ __forceinline__ float largest(vec x) {
     if constexpr (E == 8) {
@@ -138,19 +150,18 @@ struct SampleRow {
       return fmaxf(fmaxf((float)x[0], (float)x[1]), fmaxf((float)x[2], (float)x[3]));
     }
   }
-  // f(piece, its number) for this thread's pieces, 32 bytes read at a time and the next ones under way
+  // f(piece, its number) for this thread's pieces, two under way.  Loops like this one are not unrolled: a row is
+  // one pass through the kernel, whose code has to stay in the instruction cache from launch to launch (64 KB,
+  // shared by two compute units; the unrolled kernel of 92 KB took FIXED us more).
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    vec next[2] = {load(piece(0)), load(piece(1))};
+    vec next = read(piece(0)), after = read(piece(1));
 #pragma unroll 1
-    for (int u = 0; u < cw; u += 2) {
-      const vec x[2] = {next[0], next[1]};
-      if (u + 2 < cw) {
-        next[0] = load(piece(u + 2));
-        next[1] = load(piece(u + 3));
-      }
-      f(x[0], piece(u));
-      if (u + 1 < cw) f(x[1], piece(u + 1));
+    for (int u = 0; u < cw; ++u) {
+      const vec x = next;
+      next = after;
+      after = read(piece(u + 2));
+      f(trim(x, piece(u)), piece(u));
     }
   }
 
@@ -228,6 +239,7 @@ struct SampleRow {
       rank[q] = 0;
       if (run < runs) {
         e[q] = run * 64 + lane < n ? sh.list[run * 64 + lane] : 0;
+#pragma unroll 4
         for (int j = 0; j < 64; ++j) rank[q] += lane64(e[q], j) > e[q] ? 1 : 0;
         rank[q] = e[q] == 0 ? lane : rank[q];  // behind the last run's entries
         sh.list[run * 64 + rank[q]] = e[q];
@@ -238,6 +250,7 @@ struct SampleRow {
     for (int q = 0; q < Q; ++q) {
       const int run = q * WAVES + wave;
       if (run < runs)
+#pragma unroll 1
         for (int other = 0; other < runs; ++other) {
           if (other == run) continue;
           int above = 0;  // of the other run
@@ -253,19 +266,20 @@ struct SampleRow {
     lds_barrier();
   }
 
-  // list = the tokens that reach `least` and pass `also`, in any order, and returns their number (more
-  // than kList: only some are in the list).  most: the largest logits of this thread's slots (slot q:
-  // pieces q, q + kSlots, .. of it).
-  template <typename F>
-  __device__ __forceinline__ int gather(const float (&most)[kSlots], float least, F also) const {
+  // list = the tokens that reach `least`, of what b keeps with weights from low on, in any order, and returns their
+  // number (more than kList: only some are in the list).  most: the largest logits of this thread's slots
+  // (slot q: pieces q, q + kSlots, .. of it).
+  __device__ __forceinline__ int gather(const float (&most)[kSlots], float least, const Border& b, double low) const {
     uint32_t slots = 0;
+    const float finite = fmaxf(least, -3.4028235e38f);  // not -inf, a slot without a logit
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) slots |= most[q] >= least && most[q] > -INFINITY ? 1u << q : 0u;
+    for (int q = 0; q < kSlots; ++q) slots |= most[q] >= finite ? 1u << q : 0u;
     if (threadIdx.x == 0) {
       sh.n = 0;
       sh.found[0] = 0;
     }
     lds_barrier();
+#pragma unroll 1
     while (slots != 0) {
       const int q = __builtin_ctz(slots);
       slots &= slots - 1;
@@ -273,28 +287,40 @@ struct SampleRow {
       if (at < kBins) sh.counts[at] = (uint32_t)piece(q);
     }
     lds_barrier();
-    const int slots_found = (int)(uint32_t)sh.found[0];
-    if (slots_found > kBins) {
-      lds_barrier();
-      return kList + 1;
-    }
-    for (int s = threadIdx.x; s < slots_found; s += THREADS) {
-      const int j0 = (int)sh.counts[s], end = ((j0 / 64) / cw + 1) * cw * 64;  // of its wave's chunks
-      for (int j = j0; j < end; j += kSlots * 64) {
-        const vec x = load(j);
+    const int slots_found = __builtin_amdgcn_readfirstlane((int)(uint32_t)sh.found[0]);
+    if (slots_found <= kBins) {
+#pragma unroll 1
+      for (int s0 = threadIdx.x & ~63; s0 < slots_found; s0 += THREADS) {  // whole waves
+        const int s = s0 + (threadIdx.x & 63), j0 = s < slots_found ? (int)sh.counts[s] : 0;
+        const int end = s < slots_found ? ((j0 / 64) / cw + 1) * cw * 64 : 0;  // of its wave's chunks
+#pragma unroll 1
+        for (int j = j0; __any(j < end); j += kSlots * 64) {
+          const vec x = load(j < end ? j : 0);
+          uint32_t in = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float l = (float)x[e];
-          const int i = j * E - lead + e;
-          if (l >= least && l > -INFINITY && also(l, i)) {
-            const int at = atomicAdd(&sh.n, 1);
-            if (at < kList) sh.list[at] = entry(l, i);
+          for (int e = 0; e < E; ++e) {
+            const float l = (float)x[e];
+            in |= (j < end) & (l >= finite) & b.keeps(l, j * E - lead + e) ? 1u << e : 0u;
+          }
+          if (low > 0.0)
+#pragma unroll
+            for (int e = 0; e < E; ++e) in &= unrounded((float)x[e]) >= low ? ~0u : ~(1u << e);
+          // places for the wave's tokens by one access
+          const int count = __popc(in), upto = wave_scan(count), all = __builtin_amdgcn_readlane(upto, 63);
+          if (all == 0) continue;
+          int at = 0;
+          if ((threadIdx.x & 63) == 0) at = atomicAdd(&sh.n, all);
+          at = __builtin_amdgcn_readfirstlane(at) + upto - count;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if ((in >> e & 1) && at < kList) sh.list[at] = entry((float)x[e], j * E - lead + e);
+            at += in >> e & 1;
           }
         }
       }
     }
     lds_barrier();
-    const int n = __builtin_amdgcn_readfirstlane(sh.n);
+    const int n = slots_found <= kBins ? __builtin_amdgcn_readfirstlane(sh.n) : kList + 1;
     lds_barrier();
     return n;
   }
@@ -322,7 +348,7 @@ struct SampleRow {
       }
     }
     lds_barrier();
-    const int last = (int)sh.found[0];
+    const int last = __builtin_amdgcn_readfirstlane((int)sh.found[0]);
     float least = mine > -INFINITY && bin <= last ? mine : INFINITY;
     least = wave_min(least);
     if ((threadIdx.x & 63) == 0) sh.least[threadIdx.x >> 6] = least;
@@ -338,6 +364,7 @@ struct SampleRow {
     const uint64_t w = (int)threadIdx.x < n ? (uint64_t)weight(entry_logit(e)) : 0, total = lane64(scan64(w), 63);
     const uint64_t target = target_of(share, total);
     uint64_t sum = 0;  // of the tokens up to this one, by index
+#pragma unroll 2
     for (int j = 0; j < n; ++j) {
       const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e, j);
       sum += other >= (uint32_t)e ? lane64(w, j) : 0;  // complements of the indices
@@ -358,6 +385,7 @@ struct SampleRow {
       const int lane = threadIdx.x;
       uint64_t e = lane < n ? sh.list[lane] : 0;
       int rank = 0;
+#pragma unroll 2
       for (int j = 0; j < n; ++j) rank += lane64(e, j) > e ? 1 : 0;
       if (lane < n) sh.list[rank] = e;  // a wave's accesses are done in order
       __asm__ volatile("" ::: "memory");
@@ -406,10 +434,6 @@ struct SampleRow {
   __device__ __forceinline__ int choose_of_list(int n, float share, float* prob) const {
     constexpr int Q = kList / THREADS;
     lds_barrier();
-    if (n <= 64) {
-      if (threadIdx.x < 64) choose_in_wave((int)threadIdx.x < n ? sh.list[threadIdx.x] : 0, n, share);
-      return chosen_in_wave(prob);
-    }
     for (int i = threadIdx.x; i < n; i += THREADS) sh.list[i] = sh.list[i] << 32 | sh.list[i] >> 32;  // by index
     sort(n);
     uint64_t w[Q], upto[Q], total = 0;
@@ -434,25 +458,35 @@ struct SampleRow {
     return (int)~(uint32_t)(e >> 32);
   }
 
-  // The token at `share` of all that b keeps with weights from low on; with ALL of the whole row.
-  template <bool ALL>
+  // The token at `share` of all that b keeps with weights from low on.
   __device__ __forceinline__ int choose_of_row(const Border& b, double low, float share, float* prob) const {
     auto amount = [&](vec x, int j) {
       uint64_t w[E], s = 0;
-      weights<ALL>(x, j, b, low, w);
+      weights<false>(x, j, b, low, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) s += w[e];
       return s;
     };
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint64_t mine = 0;
-    each([&](vec x, int j) { mine += amount(x, j); });
+    if (b.value == -INFINITY && low == 0.0) {  // everything: without the comparisons
+      each([&](vec x, int j) {
+        uint64_t w[E];
+        weights<true>(x, j, b, low, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) mine += w[e];
+      });
+    } else {
+      each([&](vec x, int j) { mine += amount(x, j); });
+    }
     lds_barrier();
     const uint64_t total = block_sum(mine, 0);
     uint64_t target = target_of(share, total);
     // the wave, then its chunk, then the lane and its element
-    int w = 0;
-    while (w < WAVES - 1 && sh.part[0][w] <= target) target -= sh.part[0][w++];
+    const uint64_t waves = scan64(lane < WAVES ? sh.part[0][lane] : 0);
+    const int w = __builtin_ctzll(__ballot(waves > target));
+    target -= w > 0 ? lane64(waves, w - 1) : 0;
+#pragma unroll 1
     for (int u = wave; u < cw; u += WAVES) {
       const int j = (w * cw + u) * 64 + lane;
       const uint64_t s = scan64(amount(load(j), j));
@@ -461,16 +495,28 @@ struct SampleRow {
     lds_barrier();
     if (wave == 0) {
       int u = 0;
-      while (u < cw - 1 && sh.list[u] <= target) target -= sh.list[u++];
+#pragma unroll 1
+      for (;; u += 64) {
+        const uint64_t chunks = scan64(u + lane < cw ? sh.list[u + lane] : 0), over = __ballot(chunks > target);
+        if (over != 0) {
+          const int first = __builtin_ctzll(over);
+          u += first;
+          target -= first > 0 ? lane64(chunks, first - 1) : 0;
+          break;
+        }
+        target -= lane64(chunks, 63);
+        if (u + 64 >= cw) break;  // not reached: the target is below the wave's sum
+      }
       const int j = (w * cw + u) * 64 + lane;
       const vec x = load(j);
-      const uint64_t own = amount(x, j), upto = scan64(own);
-      const uint64_t over = __ballot(upto > target);
+      uint64_t we[E], own = 0;
+      weights<false>(x, j, b, low, we);
+#pragma unroll
+      for (int e = 0; e < E; ++e) own += we[e];
+      const uint64_t upto = scan64(own), over = __ballot(upto > target);
       if (lane == __builtin_ctzll(over)) {
         uint64_t sum = upto - own;
         bool done = false;
-        uint64_t we[E];
-        weights<ALL>(x, j, b, low, we);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           sum += we[e];
@@ -502,6 +548,7 @@ struct SampleRow {
       for (int u = 0; u < cw; ++u) {
         const vec x = load(piece(u));
         const int j = piece(u);
+#pragma unroll 1
         for (int e = 0; e < E; ++e) {
           const float l = (float)x[e];
           const uint32_t key = logit_key(l);
@@ -636,8 +683,8 @@ struct SampleRow {
       before += amount[q];
     }
     lds_barrier();
-    const int bin = (int)sh.found[0];
-    const uint64_t above = sh.found[1];
+    const int bin = __builtin_amdgcn_readfirstlane((int)sh.found[0]);
+    const uint64_t above = lane64(sh.found[1], 0);
     lds_barrier();
     if (bin == kBins) return;
     const Border old = *b;
@@ -680,8 +727,8 @@ struct SampleRow {
     lds_barrier();
     const uint64_t e = sh.found[0];
     lds_barrier();
-    b->value = entry_logit(e);
-    b->last = (int)~(uint32_t)e;
+    b->value = entry_logit(lane64(e, 0));
+    b->last = (int)~(uint32_t)lane64(e, 0);
   }
 
 };
@@ -706,29 +753,46 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
   const int bytes = ((lead + (int)a.V) * (int)sizeof(T) + 3) & ~3;
   Row s{sh, __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(start - lead), 0, bytes, 0x00020000), lead, (int)a.V, cw, false, 0.0, 0.0};
 
+  const float t = a.temperature ? a.temperature[r] : a.temperature_value;
+  const int32_t k = a.top_k ? a.top_k[r] : a.top_k_value;
+  const float p = a.top_p ? a.top_p[r] : a.top_p_value, m = a.min_p ? a.min_p[r] : a.min_p_value, share = a.u[r];
+
   // the largest logit of each slot, and the smallest of all (NaN aside); NV pieces under way
   float slot[kSlots], lo = INFINITY;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) slot[q] = -INFINITY;
+#pragma unroll 1
   for (int u0 = 0; u0 < cw; u0 += kSlots) {
 #pragma unroll
     for (int h = 0; h < kSlots; h += NV) {
+      if (u0 + h >= cw) break;
       vec x[NV];
 #pragma unroll
-      for (int q = 0; q < NV; ++q) {
-        x[q] = vec{} + (T)__builtin_nanf("");
-        if (u0 + h + q < cw) x[q] = s.load(s.piece(u0 + h + q));
-      }
+      for (int q = 0; q < NV; ++q) x[q] = s.read(s.piece(u0 + h + q));
 #pragma unroll
       for (int q = 0; q < NV; ++q) {
-        slot[h + q] = fmaxf(slot[h + q], Row::largest(x[q]));
-        lo = fminf(lo, -Row::largest(-x[q]));
+        const int u = u0 + h + q;
+        const bool in = u < cw && s.whole(s.piece(u));
+        const float most = Row::largest(x[q]), least = -Row::largest(-x[q]);
+        slot[h + q] = fmaxf(slot[h + q], in ? most : -INFINITY);
+        lo = fminf(lo, in ? least : INFINITY);
       }
     }
   }
-  const float t = a.temperature ? a.temperature[r] : a.temperature_value;
-  const int32_t k = a.top_k ? a.top_k[r] : a.top_k_value;
-  const float p = a.top_p ? a.top_p[r] : a.top_p_value, m = a.min_p ? a.min_p[r] : a.min_p_value, share = a.u[r];
+  // the two pieces that may reach out of the row
+#pragma unroll 1
+  for (int j = 0;; j = pieces - 1) {
+    const int chunk = j / 64;
+    if (!s.whole(j) && wave == chunk / cw && (tid & 63) == j % 64) {
+      const vec x = s.load(j);
+      const float most = Row::largest(x);
+      lo = fminf(lo, -Row::largest(-x));
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (q == (chunk % cw) % kSlots) slot[q] = fmaxf(slot[q], most);
+    }
+    if (j == pieces - 1) break;
+  }
   float mine = slot[0];
 #pragma unroll
   for (int q = 1; q < kSlots; ++q) mine = fmaxf(mine, slot[q]);
@@ -738,7 +802,7 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
     sh.most[wave] = hi;
     sh.least[wave] = lo;
   }
-  for (int i = tid; i < kExpTable; i += THREADS) sh.table[i] = kExp.at[i];
+  for (int i = tid; i < kExpTable; i += THREADS) sh.table[i] = exp_entry(i);
   if (tid == 0) sh.n = 0x7FFFFFFF;
   lds_barrier();
   hi = wave_max((tid & 63) < WAVES ? sh.most[tid & 63] : -INFINITY);
@@ -751,50 +815,69 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
   } else if (!(t > 0.f) || k == 1 || p <= 0.f || m > 1.f) {  // the first in order alone
     if (mine == hi) {
       int first = 0x7FFFFFFF;
-      auto look = [&](int j) {
+#pragma unroll 1
+      for (int u = 0; u < cw; ++u) {
+        const int j = s.piece(u);
         const vec x = s.load(j);
 #pragma unroll
         for (int e = E - 1; e >= 0; --e)
           if ((float)x[e] == hi) first = j * E - lead + e < first ? j * E - lead + e : first;
-      };
-      for (int u = 0; u < cw; ++u) look(s.piece(u));
+      }
       atomicMin(&sh.n, first);
     }
     lds_barrier();
     token = sh.n;
     prob = 1.f;
   } else {
-    const double low = m > 0.f ? (double)m * kWeightOne : 0.0;
     const bool ranked = k >= 1 && k < a.V, cut_by_share = p < 1.f;
     s.infinite = hi == INFINITY;
     s.top = s.infinite ? 0.0 : (double)hi;
     s.rate = fmin(kExpRate / (double)t, 1e300);
+    const double low = m > 0.f ? (double)m * kWeightOne : 0.0;
     // logits whose weights are not 0: from hi down to -31 t, or to the smallest there is
     const float range = s.infinite ? 31.f * t : fminf(31.f * t, hi - lo);
-    int n = kList + 1;
-    if (!s.infinite) {
-      if (ranked && k <= kListK<THREADS>)
-        n = s.gather(slot, s.reached_by(k, mine, hi, range), [](float, int) { return true; });
-      else if (!cut_by_share && low > 0.0)  // w >= m is l >= hi + t ln m, here a little less
-        n = s.gather(slot, fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY),
-                     [&](float l, int) { return s.weight(l) >= low; });
+    // first a list of all that can be kept, where that is likely to be short; then a list of what is found to be
+    // kept; otherwise the row
+    Border b{-INFINITY, 0x7FFFFFFF};
+    float least = NAN;  // no list
+    double low_here = 0.0;
+    if (s.infinite) {
+      // ties: no list
+    } else if (ranked && k <= kListK<THREADS>) {
+      least = s.reached_by(k, mine, hi, range);
+    } else if (!cut_by_share && low > 0.0) {  // w >= m is l >= hi + t ln m, here a little less
+      least = fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY);
+      low_here = low;
     }
-    if (n <= 64) {
-      token = s.choose_of_few(n, k, p, low, share, &prob);
-    } else if (n <= kList) {
-      s.sort(n);
-      token = s.choose_of_list(s.kept_of_list(n, k, p, low), share, &prob);
-    } else {
-      Border b{-INFINITY, 0x7FFFFFFF};
+    bool cut = false;
+#pragma unroll 1
+    for (;;) {
+      int n = Row::kList + 1;
+      if (least >= -INFINITY) n = s.gather(slot, least, b, low_here);
+      n = __builtin_amdgcn_readfirstlane(n);
+      if (n <= 64) {
+        token = s.choose_of_few(n, cut ? 0 : k, cut ? 1.f : p, cut ? 0.0 : low, share, &prob);
+        break;
+      }
+      // (960 tokens found by a cut take 10 us by list, a pass over a row of 50000 12, of 131072 23)
+      if (n <= (cut ? Row::kList / 2 : Row::kList)) {
+        if (!cut) {
+          s.sort(n);
+          n = s.kept_of_list(n, k, p, low);
+        }
+        token = s.choose_of_list(n, share, &prob);
+        break;
+      }
+      if (cut) {
+        token = s.choose_of_row(b, low, share, &prob);
+        break;
+      }
 #pragma unroll 1
       for (int by_weight = ranked ? 0 : 1; by_weight <= (cut_by_share ? 1 : 0); ++by_weight)
         s.cut(&b, by_weight ? 0 : (uint64_t)k, p, range);
-      n = kList + 1;
-      if (!s.infinite && b.value > -INFINITY)  // what is kept may fit the list
-        n = s.gather(slot, b.value, [&](float l, int i) { return b.keeps(l, i) && s.weight(l) >= low; });
-      if (n <= kList) token = s.choose_of_list(n, share, &prob);
-      else if (b.value == -INFINITY && low == 0.0) token = s.template choose_of_row<true>(b, low, share, &prob);
-      else token = s.template choose_of_row<false>(b, low, share, &prob);
+      cut = true;
+      least = !s.infinite && b.value > -INFINITY ? b.value : NAN;
+      low_here = low;
     }
   }
   if (tid == 0) {
