@@ -150,9 +150,7 @@ struct SampleRow {
       return fmaxf(fmaxf((float)x[0], (float)x[1]), fmaxf((float)x[2], (float)x[3]));
     }
   }
-  // f(piece, its number) for this thread's pieces, two under way.  Loops like this one are not unrolled: a row is
-  // one pass through the kernel, whose code has to stay in the instruction cache from launch to launch (64 KB,
-  // shared by two compute units; the unrolled kernel of 92 KB took FIXED us more).
+  // f(piece, its number) for this thread's pieces, two under way.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     vec next = read(piece(0)), after = read(piece(1));
@@ -892,7 +890,13 @@ template <typename T>
 static void sample_launch(const SampleArgs& a, int64_t B, hipStream_t st) {
   const int64_t pieces = (a.V + 2 * (16 / sizeof(T)) - 2) / (16 / sizeof(T));  // with any lead
   const dim3 grid((unsigned)B);
+  // Rows of few pieces need few threads.  Where every row is cut to a short list, 512 threads: two rows share a
+  // compute unit, and fewer waves meet at the barriers (top-k 50, top-p, min-p: 512 x 131072 42.7 us, 47.4 with
+  // 1024; 1 x 32000 10.2 and 12.3).  Where rows may need passes over all weights, 1024 (mixed settings: 512 x
+  // 131072 139 us, 173 with 512).
+  const bool lists = a.top_k == nullptr && a.top_k_value >= 1 && a.top_k_value <= kListK<512>;
   if (pieces <= 1024) sample_kernel<T, 256, 4><<<grid, dim3(256), 0, st>>>(a);
+  else if (lists) sample_kernel<T, 512, 8><<<grid, dim3(512), 0, st>>>(a);
   else sample_kernel<T, 1024, 8><<<grid, dim3(1024), 0, st>>>(a);
 }
 
