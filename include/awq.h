@@ -694,16 +694,13 @@ int awq_gemm_i8_kernel(int64_t M, int64_t N, int64_t K, int32_t quantized, char*
  *   tokens       device int32 [B]   out
  *   probs        device fp32 [B] or NULL   out: the token's share of the
  *                remaining weights
- *   workspace    device, >= awq_sample_workspace_bytes(B, V, logit_bytes) bytes (may
- *                be NULL where that is 0); it needs no clearing and keeps nothing
  * The values for every row must be numbers (not NaN).  Requires 1 <= B <= 2^20,
  * 1 <= V <= 2^20, B * stride < 2^40.
  */
-size_t awq_sample_workspace_bytes(int64_t B, int64_t V, int32_t logit_bytes);
 int awq_sample(const void* logits, int32_t logit_bytes, int64_t stride, int64_t B, int64_t V, const float* temperature,
                float temperature_value, const int32_t* top_k, int32_t top_k_value, const float* top_p,
                float top_p_value, const float* min_p, float min_p_value, const float* u, int32_t* tokens, float* probs,
-               void* workspace, size_t workspace_bytes, void* stream);
+               void* stream);
 
 /* Message for a status code; message for the calling thread's last failure. */
 const char* awq_status_string(int status);

@@ -21,11 +21,11 @@ CALLS = {
                         workspace=FAKE, workspace_bytes=1 << 20, stream=None),
     "awq_sample": dict(logits=FAKE, logit_bytes=2, stride=100, B=5, V=100, temperature=FAKE, temperature_value=1.0,
                        top_k=FAKE, top_k_value=0, top_p=FAKE, top_p_value=1.0, min_p=FAKE, min_p_value=0.0, u=FAKE,
-                       tokens=FAKE, probs=FAKE, workspace=FAKE, workspace_bytes=1 << 24, stream=None),
+                       tokens=FAKE, probs=FAKE, stream=None),
 }
 # pointers that may be left out by themselves
 OPTIONAL = {"awq_norm": {"post_bias", "gate_rows", "bias"}, "awq_quantize_rows": {"s"}, "awq_pack_i8": {"s"},
-            "awq_gemm_i8": {"s", "workspace"}, "awq_sample": {"temperature", "top_k", "top_p", "min_p", "probs", "workspace"}}
+            "awq_gemm_i8": {"s", "workspace"}, "awq_sample": {"temperature", "top_k", "top_p", "min_p", "probs"}}
 
 
 def call(entry, **changes):
@@ -83,10 +83,6 @@ def test_workspaces():
     assert call("awq_gemm_i8", M=500, workspace=None, workspace_bytes=need) == INVALID
     assert awq.awq_gemm_i8_workspace_bytes(0, 64, 256, False) == 0
     assert awq.awq_gemm_i8_workspace_bytes(5, 64, 100, False) == 0
-    assert awq.awq_sample_workspace_bytes(5, 0, 2) == 0 and awq.awq_sample_workspace_bytes(5, 100, 3) == 0
-    need = awq.awq_sample_workspace_bytes(1, 1 << 20, 4)
-    if need:
-        assert call("awq_sample", B=1, V=1 << 20, stride=1 << 20, logit_bytes=4, workspace_bytes=need - 1) == WS_SMALL
 
 
 def test_wrappers_refuse_cpu_tensors_and_wrong_types():

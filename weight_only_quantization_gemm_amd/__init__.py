@@ -41,7 +41,6 @@ from .block import (  # noqa: F401
     awq_pack_i8,
     awq_quantize_rows,
     awq_sample,
-    awq_sample_workspace_bytes,
 )
 from .serve import (  # noqa: F401
     KV_BITS,

@@ -72,9 +72,8 @@ SIGNATURES = {
     "awq_gemm_i8_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i32]),
     "awq_gemm_i8": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_size, c_vp]),
     "awq_gemm_i8_kernel": (ctypes.c_int, [c_i64, c_i64, c_i64, c_i32, ctypes.c_char_p, c_size]),
-    "awq_sample_workspace_bytes": (c_size, [c_i64, c_i64, c_i32]),
     "awq_sample": (ctypes.c_int, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_f32, c_vp, c_i32, c_vp, c_f32, c_vp, c_f32,
-                                  c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+                                  c_vp, c_vp, c_vp, c_vp]),
     "awq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "awq_last_error": (ctypes.c_char_p, []),
     "awq_version": (ctypes.c_int, []),

@@ -204,10 +204,6 @@ def awq_gemm_i8_kernel(M: int, N: int, K: int, quantized: bool = True) -> str:
 
 
 # ------------------------------------------------------------------- next token
-def awq_sample_workspace_bytes(B: int, V: int, logit_bytes: int) -> int:
-    return int(load().awq_sample_workspace_bytes(B, V, logit_bytes))
-
-
 def _setting(v, name: str, dtype: torch.dtype, n: int, index: int):
     """(pointer, value) of a setting: a vector with an entry for each row, or a number for all."""
     if isinstance(v, torch.Tensor):
@@ -217,7 +213,7 @@ def _setting(v, name: str, dtype: torch.dtype, n: int, index: int):
 
 def awq_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torch.Tensor] = 1.0,
                top_k: Union[int, torch.Tensor] = 0, top_p: Union[float, torch.Tensor] = 1.0,
-               min_p: Union[float, torch.Tensor] = 0.0, workspace: Optional[torch.Tensor] = None) -> dict:
+               min_p: Union[float, torch.Tensor] = 0.0) -> dict:
     """One token of each row of logits (fp16 or fp32 [B][V], strided rows allowed) from the random
     numbers u (fp32 [B], in [0, 1)): softmax at the temperature (0: the largest logit), cut to the top_k
     largest (0: all), of those to the fewest largest with top_p of the weight (1: all), of those to the ones
@@ -232,11 +228,8 @@ def awq_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, 
     p_ptr, p = _setting(top_p, "top_p", _F32, B, index)
     m_ptr, m = _setting(min_p, "min_p", _F32, B, index)
     tokens, probs = logits.new_empty(B, dtype=_I32), logits.new_empty(B, dtype=_F32)
-    lib = load()
-    size = logits.element_size()
-    ws, ws_bytes, _keep = _scratch(workspace, lib.awq_sample_workspace_bytes(B, V, size), logits.device)
-    _run(index, lib.awq_sample, logits.data_ptr(), size, stride, B, V, t_ptr, t, k_ptr, k, p_ptr, p, m_ptr, m,
-         _vector(u, "u", _F32, B, index), tokens.data_ptr(), probs.data_ptr(), ws, ws_bytes)
+    _run(index, load().awq_sample, logits.data_ptr(), logits.element_size(), stride, B, V, t_ptr, t, k_ptr, k, p_ptr, p, m_ptr, m,
+         _vector(u, "u", _F32, B, index), tokens.data_ptr(), probs.data_ptr())
     return dict(tokens=tokens, probs=probs)
 
 

@@ -156,15 +156,10 @@ int awq_gemm_i8_kernel(int64_t M, int64_t N, int64_t K, int32_t quantized, char*
   AWQ_GUARD_END
 }
 
-size_t awq_sample_workspace_bytes(int64_t B, int64_t V, int32_t logit_bytes) {
-  if (B < 1 || B > (1 << 20) || V < 1 || V > (1 << 20) || (logit_bytes != 2 && logit_bytes != 4)) return 0;
-  return awq::sample_workspace(B, V, logit_bytes);
-}
-
 int awq_sample(const void* logits, int32_t logit_bytes, int64_t stride, int64_t B, int64_t V, const float* temperature,
                float temperature_value, const int32_t* top_k, int32_t top_k_value, const float* top_p,
                float top_p_value, const float* min_p, float min_p_value, const float* u, int32_t* tokens, float* probs,
-               void* workspace, size_t workspace_bytes, void* stream) {
+               void* stream) {
   AWQ_GUARD_BEGIN
   AWQ_REQUIRE(logits && u && tokens, AWQ_ERROR_INVALID_VALUE, "logits, u and tokens must not be NULL");
   AWQ_REQUIRE(logit_bytes == 2 || logit_bytes == 4, AWQ_ERROR_INVALID_VALUE,
@@ -175,13 +170,9 @@ int awq_sample(const void* logits, int32_t logit_bytes, int64_t stride, int64_t 
               "stride=%lld must be at least V, and B * stride below 2^40", (long long)stride);
   AWQ_REQUIRE(!std::isnan(temperature_value) && !std::isnan(top_p_value) && !std::isnan(min_p_value),
               AWQ_ERROR_INVALID_VALUE, "temperature, top_p and min_p must be numbers");
-  const size_t need = awq::sample_workspace(B, V, logit_bytes);
-  AWQ_REQUIRE(workspace || need == 0, AWQ_ERROR_INVALID_VALUE, "workspace must not be NULL (%zu bytes needed)", need);
   if (int st = check_aligned({{logits, "logits"}, {temperature, "temperature"}, {top_k, "top_k"}, {top_p, "top_p"},
-                              {min_p, "min_p"}, {u, "u"}, {tokens, "tokens"}, {probs, "probs"}, {workspace, "workspace"}}))
+                              {min_p, "min_p"}, {u, "u"}, {tokens, "tokens"}, {probs, "probs"}}))
     return st;
-  AWQ_REQUIRE(workspace_bytes >= need, AWQ_ERROR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes,
-              need);
   const awq::SampleArgs a{logits, stride, V, temperature, top_k, top_p, min_p, u, tokens, probs, temperature_value,
                           top_p_value, min_p_value, top_k_value};
   return device_status(awq::launch_sample(a, logit_bytes, B, as_stream(stream)), "awq_sample");

@@ -166,7 +166,6 @@ struct SampleArgs {
   float temperature_value, top_p_value, min_p_value;
   int32_t top_k_value;
 };
-size_t sample_workspace(int64_t B, int64_t V, int logit_bytes);
 hipError_t launch_sample(const SampleArgs& a, int logit_bytes, int64_t B, hipStream_t st);
 
 // Dry runs of the product dispatch.  While a KernelPlan is installed on the

@@ -355,7 +355,7 @@ struct I8Tile {
 };
 constexpr I8Tile kI8Tiles[] = {{32, 64, 5.0, 0.28},   {32, 128, 4.6, 0.48},  {64, 64, 5.7, 0.32},
                                {64, 128, 6.4, 0.60}, {128, 128, 6.4, 0.68}, {256, 256, 9.0, 1.85}};
-static I8Plan i8_plan(int64_t M, int64_t N, int64_t K, bool quantized) {
+static I8Plan i8_estimate(int64_t M, int64_t N, int64_t K, bool quantized) {
   const double weights = (double)N * (double)K * 1e-6;  // MB, streamed at TB/s
   I8Plan best{-1, 1};
   double least = 1e30;
@@ -380,6 +380,19 @@ static I8Plan i8_plan(int64_t M, int64_t N, int64_t K, bool quantized) {
     }
   }
   return best;
+}
+
+// A call asks twice, for its workspace and for its launch.
+static I8Plan i8_plan(int64_t M, int64_t N, int64_t K, bool quantized) {
+  struct Last {
+    int64_t M, N, K;
+    bool quantized;
+    I8Plan plan;
+  };
+  static thread_local Last last{0, 0, 0, false, {-1, 1}};
+  if (last.M != M || last.N != N || last.K != K || last.quantized != quantized)
+    last = {M, N, K, quantized, i8_estimate(M, N, K, quantized)};
+  return last.plan;
 }
 
 size_t gemm_i8_workspace(int64_t M, int64_t N, int64_t K, bool quantized) {

@@ -884,8 +884,6 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
   }
 }
 
-size_t sample_workspace(int64_t, int64_t, int) { return 0; }
-
 template <typename T>
 static void sample_launch(const SampleArgs& a, int64_t B, hipStream_t st) {
   const int64_t pieces = (a.V + 2 * (16 / sizeof(T)) - 2) / (16 / sizeof(T));  // with any lead
