@@ -113,7 +113,7 @@ def test_wrappers_refuse_cpu_tensors_and_wrong_types():
     (77, 4096, 11008, True, "gemm_i8_kernel<128,128,2,4,4,64> block=512 grid=224 shares=7"),
     (500, 4096, 1024, True, "gemm_i8_kernel<64,128,1,4,3,64> block=256 grid=256 shares=1"),
     (128, 28672, 8192, True, "gemm_i8_kernel<128,128,2,4,4,64> block=512 grid=224 shares=1"),
-    (8192, 28672, 8192, True, "gemm_i8_kernel<256,256,4,2,4,32> block=512 grid=3584 shares=1"),
+    (8192, 28672, 8192, True, "gemm_i8_kernel<256,256,2,4,4,32> block=512 grid=3584 shares=1"),
 ])
 def test_product_dispatch(M, N, K, quantized, kernel):
     assert awq.awq_gemm_i8_kernel(M, N, K, quantized) == kernel

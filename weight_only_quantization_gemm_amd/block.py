@@ -39,26 +39,28 @@ def _run(index: int, fn, *args) -> None:
 def _matrix(t: torch.Tensor, name: str, dtypes, index: int):
     """(rows, columns, elements from one row to the next) of a matrix of one of the dtypes on the given device
     (-1: any GPU) whose rows are contiguous; any stride between rows (a single row has no next)."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda:
-        if isinstance(t, torch.Tensor) and t.dtype not in dtypes:
-            raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        _need(t, name, dtypes[0], 2)
-        raise ValueError(f"{name} must be a GPU matrix")
-    if index >= 0 and t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    T, N = t.shape
-    row, column = t.stride()
-    if column != 1 and N > 1:
-        raise ValueError(f"{name} must be contiguous within each row")
-    return T, N, row if T > 1 else N
+    if isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in dtypes:
+        device = t.get_device()
+        if device >= 0 and (device == index or index < 0):
+            T, N = t.shape
+            if t.is_contiguous():
+                return T, N, N
+            row, column = t.stride()
+            if column == 1 or N == 1:
+                return T, N, row if T > 1 else N
+            raise ValueError(f"{name} must be contiguous within each row")
+    if isinstance(t, torch.Tensor) and t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    _need(t, name, dtypes[0] if not isinstance(t, torch.Tensor) else t.dtype, 2)
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
 def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, index: int) -> int:
     """The pointer of a vector of n."""
-    _like(t, name, dtype, 1, index)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.shape == (n,) and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _like(t, name, dtype, 1, index)  # says what is wrong
+    raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
 
 
 def _output(out: torch.Tensor, name: str, shape, dtype: torch.dtype, index: int) -> torch.Tensor:

@@ -207,8 +207,8 @@ __global__ __launch_bounds__(256) void gemm_i8_join_kernel(I8Args a) {
 
 // Few tokens: a block takes 16 channels at a time (gridDim.x groups apart), its NW waves every NW-th
 // 128 bytes of K, and their sums are joined through LDS.  A lane of v_mfma_i32_16x16x64_i8 holds 16 bytes
-// of one of 16 rows: lane l reads row l % 16, bytes 32 (l / 16) on of a chunk, 16 + 16, so four lanes share
-// a 128-byte line and both operands agree on the order of K.  Bound by the weights' one read: DEPTH chunks
+// of one of 16 rows: lane l reads row l % 16, bytes 16 (l / 16) on of each half of a chunk, so four lanes read
+// 64 bytes side by side and both operands agree on the order of K.  Bound by the weights' one read: DEPTH chunks
 // of a wave are under way while DEPTH are multiplied, across the groups' ends; TT tiles of 16 tokens come
 // from the caches again for every group.
 // FUSED: x is one fp16 row, which each block quantises to LDS itself (one launch instead of two), while its
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
   __shared__ float part[NW];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int chunks = (int)(a.K / 128), groups = (int)((a.N + 15) / 16), M = (int)a.M;
-  const int row = lane & 15, off = (lane >> 4) * 32;
+  const int row = lane & 15, off = (lane >> 4) * 16;
   const int batches = (chunks + NW * DEPTH - 1) / (NW * DEPTH);
   struct Batch {
     i32x4 w[DEPTH][2], x[FUSED ? 1 : TT][FUSED ? 1 : DEPTH][2];
@@ -238,13 +238,13 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
       if (c >= chunks) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        to.w[d][h] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(w + (int64_t)c * 128) + h);
+        to.w[d][h] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(w + (int64_t)c * 128) + 4 * h);
       if constexpr (!FUSED)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            to.x[t][d][h] = reinterpret_cast<const i32x4*>(a.x + (int64_t)token[t] * a.K + (int64_t)c * 128 + off)[h];
+            to.x[t][d][h] = reinterpret_cast<const i32x4*>(a.x + (int64_t)token[t] * a.K + (int64_t)c * 128 + off)[4 * h];
     }
   };
   Batch cur, next;
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
           for (int h = 0; h < 2; ++h) {
             i32x4 xv;
             if constexpr (FUSED)
-              xv = reinterpret_cast<const i32x4*>(rows + chunk(b, d) * 128 + off)[h];
+              xv = reinterpret_cast<const i32x4*>(rows + chunk(b, d) * 128 + off)[4 * h];
             else xv = cur.x[t][d][h];
             acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur.w[d][h], xv, acc[t], 0, 0, 0);
           }
@@ -467,7 +467,7 @@ hipError_t launch_gemm_i8(const void* x, const float* x_scales, const float* s, 
     case 2: return tile_launch<64, 64, 1, 2, 5, 64>(a, y_bytes, st);
     case 3: return tile_launch<64, 128, 1, 4, 3, 64>(a, y_bytes, st);
     case 4: return tile_launch<128, 128, 2, 4, 4, 64>(a, y_bytes, st);
-    default: return tile_launch<256, 256, 4, 2, 4, 32>(a, y_bytes, st);
+    default: return tile_launch<256, 256, 2, 4, 4, 32>(a, y_bytes, st);
   }
 }
 
