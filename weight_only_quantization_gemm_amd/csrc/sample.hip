@@ -92,9 +92,13 @@ __device__ __forceinline__ float wave_min(float v) { return -wave_max(-v); }
 
 template <int THREADS>
 struct SampleShared {
-  static constexpr int kList = 2 * THREADS, kBins = 2 * THREADS;
-  uint64_t list[kList];     // entries, or the bins' weights
-  uint32_t counts[kBins];   // the bins' counts, or candidates
+  static constexpr int kList = 8 * THREADS, kSort = 2 * THREADS, kBins = 2 * THREADS, kFound = 5 * THREADS;
+  uint64_t list[kList];  // entries, or the bins' weights
+  union {
+    uint32_t counts[kBins];         // the bins' counts
+    uint32_t slots[kFound];         // slots with tokens for the list
+    uint64_t chunks[kFound / 2];    // sums of the list's tokens, for each 64 pieces
+  };
   double table[kExpTable];  // exp_entry
   uint64_t part[2][THREADS / 64];
   uint64_t found[4];
@@ -114,7 +118,8 @@ struct Border {
 template <typename T, int THREADS>
 struct SampleRow {
   static constexpr int E = 16 / sizeof(T), WAVES = THREADS / 64;
-  static constexpr int kList = SampleShared<THREADS>::kList, kBins = SampleShared<THREADS>::kBins;
+  typedef SampleShared<THREADS> Shared;
+  static constexpr int kList = Shared::kList, kSort = Shared::kSort, kBins = Shared::kBins, kFound = Shared::kFound;
   typedef T vec __attribute__((ext_vector_type(E)));
   SampleShared<THREADS>& sh;
   __amdgpu_buffer_rsrc_t resource;  // from the 16-byte piece with the row's first element to the row's end
@@ -222,10 +227,10 @@ struct SampleRow {
   static __device__ __forceinline__ uint64_t entry(float x, int i) { return (uint64_t)logit_key(x) << 32 | (uint32_t)~i; }
   static __device__ __forceinline__ float entry_logit(uint64_t e) { return key_logit((uint32_t)(e >> 32)); }
 
-  // Sorts list[0 .. n) descending; its entries differ.  Each wave ranks runs of 64 by comparing every pair,
+  // Sorts list[0 .. n) descending (n <= kSort); its entries differ.  Each wave ranks runs of 64 by comparing every pair,
   // then every entry looks its place up in the other runs.
   __device__ __forceinline__ void sort(int n) const {
-    constexpr int Q = kList / THREADS;
+    constexpr int Q = kSort / THREADS;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, runs = (n + 63) / 64;
     uint64_t e[Q];
     int rank[Q];
@@ -277,19 +282,19 @@ struct SampleRow {
       sh.found[0] = 0;
     }
     lds_barrier();
+    const int mine = __popc(slots), upto = wave_scan(mine), all = __builtin_amdgcn_readlane(upto, 63);
+    int place = 0;  // one access a wave: thousands to one address take their time
+    if ((threadIdx.x & 63) == 0 && all > 0) place = atomicAdd(reinterpret_cast<int*>(&sh.found[0]), all);
+    place = __builtin_amdgcn_readfirstlane(place) + upto - mine;
 #pragma unroll 1
-    while (slots != 0) {
-      const int q = __builtin_ctz(slots);
-      slots &= slots - 1;
-      const int at = atomicAdd(reinterpret_cast<int*>(&sh.found[0]), 1);
-      if (at < kBins) sh.counts[at] = (uint32_t)piece(q);
-    }
+    for (; slots != 0; slots &= slots - 1, ++place)
+      if (place < kFound) sh.slots[place] = (uint32_t)piece(__builtin_ctz(slots));
     lds_barrier();
     const int slots_found = __builtin_amdgcn_readfirstlane((int)(uint32_t)sh.found[0]);
-    if (slots_found <= kBins) {
+    if (slots_found <= kFound) {
 #pragma unroll 1
       for (int s0 = threadIdx.x & ~63; s0 < slots_found; s0 += THREADS) {  // whole waves
-        const int s = s0 + (threadIdx.x & 63), j0 = s < slots_found ? (int)sh.counts[s] : 0;
+        const int s = s0 + (threadIdx.x & 63), j0 = s < slots_found ? (int)sh.slots[s] : 0;
         const int end = s < slots_found ? ((j0 / 64) / cw + 1) * cw * 64 : 0;  // of its wave's chunks
 #pragma unroll 1
         for (int j = j0; __any(j < end); j += kSlots * 64) {
@@ -318,7 +323,7 @@ struct SampleRow {
       }
     }
     lds_barrier();
-    const int n = slots_found <= kBins ? __builtin_amdgcn_readfirstlane(sh.n) : kList + 1;
+    const int n = slots_found <= kFound ? __builtin_amdgcn_readfirstlane(sh.n) : kList + 1;
     lds_barrier();
     return n;
   }
@@ -398,9 +403,17 @@ struct SampleRow {
     return chosen_in_wave(prob);
   }
 
+  // The border with the list's entry i the last one kept.
+  __device__ __forceinline__ Border border_of(int i) const {
+    const uint64_t e = lane64(sh.list[i], 0);
+    return {entry_logit(e), (int)~(uint32_t)e};
+  }
+  // Whether the row's chunks have sums in choose_of_list.
+  __device__ __forceinline__ bool chunks_fit() const { return (lead + V + E - 1) / E <= 64 * (kFound / 2); }
+
   // Of the sorted list's first n entries, how many are kept.
   __device__ __forceinline__ int kept_of_list(int n, int k, float p, double low) const {
-    constexpr int Q = kList / THREADS;
+    constexpr int Q = kSort / THREADS;
     if (k >= 1 && k < n) n = k;
     double w[Q];
     uint64_t upto[Q], carry = 0;
@@ -428,32 +441,64 @@ struct SampleRow {
     return __builtin_amdgcn_readfirstlane((int)block_sum(kept, 0));
   }
 
-  // The token at `share` of the first n entries of the list (in any order).
-  __device__ __forceinline__ int choose_of_list(int n, float share, float* prob) const {
-    constexpr int Q = kList / THREADS;
-    lds_barrier();
-    for (int i = threadIdx.x; i < n; i += THREADS) sh.list[i] = sh.list[i] << 32 | sh.list[i] >> 32;  // by index
-    sort(n);
-    uint64_t w[Q], upto[Q], total = 0;
+  // The token at `target` of what b keeps in the 64 pieces of a chunk, with weights from low on; by every thread.
+  __device__ __forceinline__ int choose_of_chunk(int chunk, uint64_t target, uint64_t total, const Border& b, double low,
+                                                 float* prob) const {
+    if (threadIdx.x < 64) {
+      const int j = chunk * 64 + (int)threadIdx.x;
+      const vec x = load(j);
+      uint64_t we[E], own = 0;
+      weights<false>(x, j, b, low, we);
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int i = q * THREADS + threadIdx.x;
-      w[q] = upto[q] = 0;
-      if (q * THREADS < n) {
-        w[q] = i < n ? (uint64_t)weight(key_logit((uint32_t)sh.list[i])) : 0;
-        const uint64_t all = block_sum(w[q], q & 1, &upto[q]);
-        upto[q] += total;
-        total += all;
+      for (int e = 0; e < E; ++e) own += we[e];
+      const uint64_t upto = scan64(own), over = __ballot(upto > target);
+      if ((int)threadIdx.x == __builtin_ctzll(over)) {
+        uint64_t sum = upto - own;
+        bool done = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          sum += we[e];
+          if (!done && sum > target) {
+            done = true;
+            sh.found[0] = entry((float)x[e], j * E - lead + e);
+          }
+        }
       }
     }
-    const uint64_t target = target_of(share, total);
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if (upto[q] > target && upto[q] - w[q] <= target) sh.found[0] = sh.list[q * THREADS + threadIdx.x];
     lds_barrier();
     const uint64_t e = sh.found[0];
-    *prob = (float)(unrounded(key_logit((uint32_t)e)) / (double)total);
-    return (int)~(uint32_t)(e >> 32);
+    *prob = (float)(unrounded(entry_logit(e)) / (double)total);
+    return (int)~(uint32_t)e;
+  }
+
+  // The token at `share` of the first n entries of the list (in any order), which are what b keeps with weights
+  // from low on: their weights summed by chunk, in index order.
+  __device__ __forceinline__ int choose_of_list(int n, const Border& b, double low, float share, float* prob) const {
+    const int pieces = (lead + V + E - 1) / E, chunks = (pieces + 63) / 64, per = (chunks + THREADS - 1) / THREADS;
+    lds_barrier();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < chunks; i += THREADS) sh.chunks[i] = 0;
+    lds_barrier();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+      const uint64_t e = sh.list[i], w = whole(unrounded(entry_logit(e)));
+      atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunks[((int)~(uint32_t)e + lead) / (64 * E)]), (unsigned long long)w);
+    }
+    lds_barrier();
+    uint64_t mine = 0, upto;
+#pragma unroll 1
+    for (int i = threadIdx.x * per; i < (int)(threadIdx.x + 1) * per && i < chunks; ++i) mine += sh.chunks[i];
+    const uint64_t total = block_sum(mine, 0, &upto), target = target_of(share, total);
+    if (upto > target && upto - mine <= target) {
+      uint64_t left = target - (upto - mine);
+      int i = threadIdx.x * per;
+#pragma unroll 1
+      while (sh.chunks[i] <= left) left -= sh.chunks[i++];
+      sh.found[2] = i;
+      sh.found[3] = left;
+    }
+    lds_barrier();
+    return choose_of_chunk(__builtin_amdgcn_readfirstlane((int)sh.found[2]), lane64(sh.found[3], 0), total, b, low, prob);
   }
 
   // The token at `share` of all that b keeps with weights from low on.
@@ -475,7 +520,33 @@ struct SampleRow {
         for (int e = 0; e < E; ++e) mine += w[e];
       });
     } else {
-      each([&](vec x, int j) { mine += amount(x, j); });
+      // Only what b keeps is weighed: each wave lines its tokens up in LDS and takes 64 at a time.
+      float* queue = reinterpret_cast<float*>(sh.list) + wave * (kList * 2 / WAVES);  // of 1024; 64 E + 63 are used
+      int waiting = 0;
+      lds_barrier();
+      auto take = [&](int n) {  // the last n
+        __asm__ volatile("" ::: "memory");  // a wave's LDS accesses are done in order
+        waiting -= n;
+        const double v = unrounded(queue[waiting + (lane < n ? lane : 0)]);
+        mine += whole((lane < n) & (v >= low) ? v : 0.0);
+        __asm__ volatile("" ::: "memory");
+      };
+      each([&](vec x, int j) {
+        uint32_t in = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) in |= b.keeps((float)x[e], j * E - lead + e) ? 1u << e : 0u;
+        const int count = __popc(in), upto = wave_scan(count);
+        int at = waiting + upto - count;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (in >> e & 1) queue[at] = (float)x[e];
+          at += in >> e & 1;
+        }
+        waiting += __builtin_amdgcn_readlane(upto, 63);
+#pragma unroll 1
+        while (waiting >= 64) take(64);
+      });
+      if (waiting > 0) take(waiting);
     }
     lds_barrier();
     const uint64_t total = block_sum(mine, 0);
@@ -491,44 +562,20 @@ struct SampleRow {
       if (lane == 63) sh.list[u] = s;
     }
     lds_barrier();
-    if (wave == 0) {
-      int u = 0;
+    int u = 0;
 #pragma unroll 1
-      for (;; u += 64) {
-        const uint64_t chunks = scan64(u + lane < cw ? sh.list[u + lane] : 0), over = __ballot(chunks > target);
-        if (over != 0) {
-          const int first = __builtin_ctzll(over);
-          u += first;
-          target -= first > 0 ? lane64(chunks, first - 1) : 0;
-          break;
-        }
-        target -= lane64(chunks, 63);
-        if (u + 64 >= cw) break;  // not reached: the target is below the wave's sum
+    for (;; u += 64) {
+      const uint64_t sums = scan64(u + lane < cw ? sh.list[u + lane] : 0), over = __ballot(sums > target);
+      if (over != 0) {
+        const int first = __builtin_ctzll(over);
+        u += first;
+        target -= first > 0 ? lane64(sums, first - 1) : 0;
+        break;
       }
-      const int j = (w * cw + u) * 64 + lane;
-      const vec x = load(j);
-      uint64_t we[E], own = 0;
-      weights<false>(x, j, b, low, we);
-#pragma unroll
-      for (int e = 0; e < E; ++e) own += we[e];
-      const uint64_t upto = scan64(own), over = __ballot(upto > target);
-      if (lane == __builtin_ctzll(over)) {
-        uint64_t sum = upto - own;
-        bool done = false;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          sum += we[e];
-          if (!done && sum > target) {
-            done = true;
-            sh.found[0] = entry((float)x[e], j * E - lead + e);
-          }
-        }
-      }
+      target -= lane64(sums, 63);
+      if (u + 64 >= cw) break;  // not reached: the target is below the wave's sum
     }
-    lds_barrier();
-    const uint64_t e = sh.found[0];
-    *prob = (float)(unrounded(entry_logit(e)) / (double)total);
-    return (int)~(uint32_t)e;
+    return choose_of_chunk(w * cw + u, target, total, b, low, prob);
   }
 
   // cut() digit by digit over the logits' images, for many tokens of nearly one logit.
@@ -646,9 +693,7 @@ struct SampleRow {
       sh.counts[i] = 0;
     }
     lds_barrier();
-    each([&](vec x, int j) {
-      uint64_t w[E];
-      weights<false>(x, j, *b, 0.0, w);
+    auto count = [&](vec x, const uint64_t (&w)[E]) {
       int bin[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) bin[e] = bin_of((float)x[e]);
@@ -657,7 +702,20 @@ struct SampleRow {
         if (by_count) atomicAdd(&sh.counts[bin[e]], w[e] != 0 ? 1u : 0u);
         else atomicAdd(reinterpret_cast<unsigned long long*>(&sh.list[bin[e]]), (unsigned long long)w[e]);
       }
-    });
+    };
+    if (b->value == -INFINITY) {
+      each([&](vec x, int j) {
+        uint64_t w[E];
+        weights<true>(x, j, *b, 0.0, w);
+        count(x, w);
+      });
+    } else {
+      each([&](vec x, int j) {
+        uint64_t w[E];
+        weights<false>(x, j, *b, 0.0, w);
+        count(x, w);
+      });
+    }
     lds_barrier();
     uint64_t mine = 0, amount[PER];
 #pragma unroll
@@ -686,12 +744,16 @@ struct SampleRow {
     lds_barrier();
     if (bin == kBins) return;
     const Border old = *b;
+    // the bin's logits and, for its roundings, a little more
+    const float slack = 1e-5f * (fabsf((float)top) + range);
+    const float to = step > 0.f ? (float)top - (float)bin / step + slack : INFINITY;  // 0: an infinite range, one bin
+    const float from = step > 0.f && bin < kBins - 1 ? (float)top - (float)(bin + 1) / step - slack : -INFINITY;
     if (threadIdx.x == 0) sh.n = 0;
     lds_barrier();
     each([&](vec x, int j) {
       bool any = false;
 #pragma unroll
-      for (int e = 0; e < E; ++e) any |= bin_of((float)x[e]) == bin;
+      for (int e = 0; e < E; ++e) any |= ((float)x[e] >= from) & ((float)x[e] <= to);
       if (!any) return;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -699,13 +761,13 @@ struct SampleRow {
         const int i = j * E - lead + e;
         if (bin_of(l) == bin && old.keeps(l, i) && weight(l) > 0.0) {
           const int at = atomicAdd(&sh.n, 1);
-          if (at < kList) sh.list[at] = entry(l, i);
+          if (at < kSort) sh.list[at] = entry(l, i);
         }
       }
     });
     lds_barrier();
     const int n = __builtin_amdgcn_readfirstlane(sh.n);
-    if (n > kList) {
+    if (n > kSort) {
       lds_barrier();
       *b = digits(old, rank_at, least);
       return;
@@ -737,7 +799,7 @@ template <int THREADS>
 constexpr int kListK = THREADS * 600 / 1024;
 
 template <typename T, int THREADS, int NV>
-__global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
+__global__ __launch_bounds__(THREADS, 4) void sample_kernel(SampleArgs a) {
   typedef SampleRow<T, THREADS> Row;
   typedef typename Row::vec vec;
   constexpr int E = Row::E, WAVES = THREADS / 64;
@@ -857,17 +919,19 @@ __global__ __launch_bounds__(THREADS) void sample_kernel(SampleArgs a) {
         token = s.choose_of_few(n, cut ? 0 : k, cut ? 1.f : p, cut ? 0.0 : low, share, &prob);
         break;
       }
-      // (960 tokens found by a cut take 10 us by list, a pass over a row of 50000 12, of 131072 23)
-      if (n <= (cut ? Row::kList / 2 : Row::kList)) {
-        if (!cut) {
-          s.sort(n);
-          n = s.kept_of_list(n, k, p, low);
-        }
-        token = s.choose_of_list(n, share, &prob);
+      if (!cut && n <= Row::kSort) {
+        s.sort(n);
+        n = s.kept_of_list(n, k, p, low);
+        b = s.border_of(n - 1);
+      }
+      const bool listed = cut ? n <= Row::kList : b.value > -INFINITY;  // all that is kept, which b says
+      const double low_left = cut ? low : 0.0;
+      if (listed && s.chunks_fit()) {
+        token = s.choose_of_list(n, b, low_left, share, &prob);
         break;
       }
-      if (cut) {
-        token = s.choose_of_row(b, low, share, &prob);
+      if (cut || listed) {
+        token = s.choose_of_row(b, low_left, share, &prob);
         break;
       }
 #pragma unroll 1
