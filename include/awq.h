@@ -627,7 +627,8 @@ int awq_norm(const void* h, int32_t h_bytes, int64_t h_stride, const void* y, in
 /*
  * Rows in 8 bits: int8 codes in [-127, 127] and one fp32 scale a row,
  *   code[k] = rint(127 v[k] / max|v|)  exactly (half to even),  scale = max|v| / 127
- * (a row of zeros: codes and scale 0), the row standing for code * scale.
+ * (a row of zeros: codes and scale 0; one with an infinity or a NaN: codes 0, the
+ * scale infinite or NaN), the row standing for code * scale.
  *
  * awq_quantize_rows -- activations: v = x, or x / s (fp32, rounded once) with
  * the per-channel input scales s that awq_quantize finds.
@@ -637,7 +638,8 @@ int awq_norm(const void* h, int32_t h_bytes, int64_t h_stride, const void* y, in
  *   scales  device fp32 [M]      out
  * awq_pack_i8 -- weights: v = W, or W * s (fp32, rounded once).
  *   W       device fp16 [N][K];  codes int8 [N][K], scales fp32 [N]   out
- * Require K % AWQ_GROUP == 0, K <= 2^17, M and N in [1, 2^24].
+ * Require K % AWQ_GROUP == 0, K <= 2^17, M and N in [1, 2^24]; no output overlaps
+ * an input.
  */
 int awq_quantize_rows(const void* x, int64_t x_stride, const float* s, int64_t M, int64_t K, void* codes, float* scales,
                       void* stream);

@@ -206,3 +206,24 @@ def test_refusals():
                 lambda: awq.awq_gemm_i8(dx, dwc, dws.half())):
         with pytest.raises(TypeError):
             bad()
+
+
+@pytest.mark.parametrize("M,K", [(1, 256), (3, 4096), (1500, 4096), (5, 11008), (2, 20480)])
+def test_rows_with_infinities_and_nan(M, K):
+    """Such a row's codes are 0 and its scale is infinite or NaN, so its products are NaN; the other
+    rows are as without it."""
+    x = rows(M, K, seed=K)
+    for value in (np.inf, -np.inf, np.nan):
+        for at in (0, K // 2 + 5, K - 1):
+            bad = x.copy()
+            bad[M // 2, at] = value
+            codes, scales = awq.awq_quantize_rows(*dev(bad))
+            scales = scales.cpu().numpy()
+            assert not codes[M // 2].any()
+            assert np.isnan(scales[M // 2]) if np.isnan(value) else np.isposinf(scales[M // 2])
+            want, want_scales = codes_of(np.delete(x, M // 2, 0).astype(np.float32)) if M > 1 else (x[:0], x[:0, 0])
+            assert np.array_equal(np.delete(codes.cpu().numpy(), M // 2, 0), want)
+            assert np.array_equal(np.delete(scales, M // 2), want_scales)
+            wc, ws = weights(40, K, seed=1)
+            y = awq.awq_gemm_i8(*dev(bad, wc, ws))
+            assert y[M // 2].isnan().all() and not np.isnan(np.delete(y.cpu().numpy(), M // 2, 0)).any()

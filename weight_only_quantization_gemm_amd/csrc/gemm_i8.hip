@@ -258,11 +258,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
       return a.s ? v / *reinterpret_cast<const f32x8*>(a.s + k) : v;
     };
     float most = 0.f;
-    for (int k = threadIdx.x * 8; k < (int)a.K; k += 512 * NW) {
-      const f32x8 v = values(k);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) most = fmaxf(most, fabsf(v[u]));
-    }
+    for (int k = threadIdx.x * 8; k < (int)a.K; k += 512 * NW) most = largest_of(most, values(k));
     most = row_join<64 * NW>(most, part, MaxOp());
     top = most;
     const float by = 127.f / most;

@@ -139,8 +139,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     w[p] *= h[p];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(w[p][u]));
+    top = largest_of(top, w[p]);
   }
   top = row_join<L>(top, part + 4 * W, MaxOp());
   const float by = 127.f / top;

@@ -26,9 +26,15 @@ __device__ __forceinline__ float wave_join(float v, Op op) {
 struct AddOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
-struct MaxOp {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+struct MaxOp {  // NaN where either is
+  __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
 };
+// The largest of most and the |v|, NaN where one is.
+__device__ __forceinline__ float largest_of(float most, const f32x8& v) {
+  const f32x8 m = __builtin_elementwise_abs(v);
+  const MaxOp max;
+  return max(max(max(most, max(m[0], m[1])), max(m[2], m[3])), max(max(m[4], m[5]), max(m[6], m[7])));
+}
 
 // The same over the L threads of a row (L = 64: a wave, otherwise the whole block)
 // by way of part [L / 64], which no thread may still be reading: callers take
@@ -56,10 +62,11 @@ __device__ __forceinline__ float row_join(float v, float* part, Op op) {
 // is the wanted one unless it lies closer than that to a half; there (one value in
 // ten thousand) the quotient is formed in 64 bits, whose 53 can hold every half
 // and miss none: 127 v / top is a half itself or at least 2^-26 away from it.
+// A row with an infinity or a NaN has codes 0, and its scale says what it had.
 __device__ __forceinline__ float code_of(float v, float by, float top) {
   const float q = v * by, r = rintf(q);
   if (fabsf(q - r) <= 0.4999f) return r;  // false for a NaN too: by overflows where top is tiny
-  return top > 0.f ? (float)rint(127.0 * (double)v / (double)top) : 0.f;
+  return top > 0.f && top < INFINITY ? (float)rint(127.0 * (double)v / (double)top) : 0.f;
 }
 
 // Four codes as the bytes of a word.

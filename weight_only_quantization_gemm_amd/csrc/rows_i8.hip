@@ -41,10 +41,6 @@ __global__ __launch_bounds__(THREADS) void rows_i8_kernel(const f16* __restrict_
   const f16* row = x + m * stride;
   int8_t* to = codes + m * K;
   float top = 0.f;
-  auto largest = [&](const f32x8& v) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(v[u]));
-  };
   if constexpr (PER > 0) {
     f32x8 v[PER];
 #pragma unroll
@@ -54,7 +50,7 @@ __global__ __launch_bounds__(THREADS) void rows_i8_kernel(const f16* __restrict_
       if (k < K) v[p] = row_values<SCALING>(row, s, k);
     }
 #pragma unroll
-    for (int p = 0; p < PER; ++p) largest(v[p]);
+    for (int p = 0; p < PER; ++p) top = largest_of(top, v[p]);
     top = row_join<THREADS>(top, part, MaxOp());
     const float by = 127.f / top;
 #pragma unroll
@@ -63,7 +59,7 @@ __global__ __launch_bounds__(THREADS) void rows_i8_kernel(const f16* __restrict_
       if (k < K) store_codes(to + k, v[p], by, top);
     }
   } else {
-    for (int64_t k = threadIdx.x * 8; k < K; k += THREADS * 8) largest(row_values<SCALING>(row, s, k));
+    for (int64_t k = threadIdx.x * 8; k < K; k += THREADS * 8) top = largest_of(top, row_values<SCALING>(row, s, k));
     top = row_join<THREADS>(top, part, MaxOp());
     const float by = 127.f / top;
     for (int64_t k = threadIdx.x * 8; k < K; k += THREADS * 8)
