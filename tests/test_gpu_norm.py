@@ -223,3 +223,19 @@ def test_refusals():
         awq.awq_norm(h[:, 4:60], w[:56])
     with pytest.raises(TypeError):
         awq.awq_norm(h, w.float())
+
+
+def test_rows_in_8_bits_without_eps_and_not_finite():
+    """A row of zeros has scale 0 also where 1 / rms is infinite; one with a NaN or an infinity gives NaN."""
+    for N in (256, 4096, 16384):
+        d = make(5, N, seed=N)
+        d["h"][1] = d["y"][1] = 0
+        r = check(d, eps=0.0, quantize=True)
+        assert r["scales"][1].item() == 0.0 and not r["x"][1].any()
+        want = {k: v.clone() for k, v in r.items()}
+        d["h"][3, N // 2 + 3] = np.nan
+        d["y"][4, N - 1] = np.inf
+        dev = {k: torch.from_numpy(v).to(DEV) for k, v in d.items() if v is not None}
+        r = awq.awq_norm(**dev, eps=0.0, quantize=True)
+        assert r["scales"][3:].isnan().all()
+        assert torch.equal(r["x"][:3], want["x"][:3]) and torch.equal(r["scales"][:3], want["scales"][:3])

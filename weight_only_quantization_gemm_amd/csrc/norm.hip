@@ -152,7 +152,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
       *reinterpret_cast<u32x2*>(reinterpret_cast<int8_t*>(a.x) + t * a.N + at[p]) =
           u32x2{code_word(c[0], c[1], c[2], c[3]), code_word(c[4], c[5], c[6], c[7])};
     }
-  if (lane == 0) a.x_scales[t] = r * (top / 127.f);
+  if (lane == 0) a.x_scales[t] = top == 0.f ? 0.f : r * (top / 127.f);  // without eps r is infinite where h is 0
 }
 
 template <int L, int PER>
