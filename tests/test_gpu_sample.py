@@ -152,6 +152,25 @@ def test_settings_that_are_no_numbers_are_off():
     check(logits, u, temperature=nan)
 
 
+@pytest.mark.parametrize("V", [40, 700, 20011])
+def test_top_p_that_is_no_number_beside_other_settings(V):
+    logits, u = logits_of(6, V, seed=V, half=True)
+    nan = np.full(6, np.nan, np.float32)
+    for f in (dict(top_k=5), dict(top_k=90), dict(top_k=650), dict(min_p=0.02), dict(top_k=30, min_p=0.1)):
+        check(logits, u, top_p=nan, **f)
+
+
+@pytest.mark.parametrize("half", [True, False])
+def test_signalling_nan_is_never_chosen(half):
+    logits, u = logits_of(6, 5003, seed=8, half=half)
+    bits = logits.view(np.uint16 if half else np.uint32)
+    g = np.random.default_rng(4)
+    for v in (0x7C01, 0xFC01, 0x7DFF, 0x7E00) if half else (0x7F800001, 0xFF800001, 0x7FBFFFFF, 0x7FC00000):
+        bits[:, g.choice(5003, 500)] = v
+    for f in (dict(), dict(top_k=20), dict(top_p=0.8), dict(temperature=0.0)):
+        check(logits, u, **f)
+
+
 @pytest.mark.parametrize("half", [True, False])
 @pytest.mark.parametrize("stride", [1003, 1008, 1500, 1001])
 def test_strided_rows(half, stride):

@@ -815,7 +815,8 @@ __global__ __launch_bounds__(THREADS, 4) void sample_kernel(SampleArgs a) {
 
   const float t = a.temperature ? a.temperature[r] : a.temperature_value;
   const int32_t k = a.top_k ? a.top_k[r] : a.top_k_value;
-  const float p = a.top_p ? a.top_p[r] : a.top_p_value, m = a.min_p ? a.min_p[r] : a.min_p_value, share = a.u[r];
+  const float p_given = a.top_p ? a.top_p[r] : a.top_p_value, p = p_given < 1.f ? p_given : 1.f;  // 1 for a NaN
+  const float m = a.min_p ? a.min_p[r] : a.min_p_value, share = a.u[r];
 
   // the largest logit of each slot, and the smallest of all (NaN aside); NV pieces under way
   float slot[kSlots], lo = INFINITY;
