@@ -221,6 +221,7 @@ def test_refusals():
     l, u = torch.zeros(3, 50, device=DEV), torch.zeros(3, device=DEV)
     for bad in (lambda: awq.awq_sample(l, u[:2]), lambda: awq.awq_sample(l, u, top_k=torch.zeros(2, dtype=torch.int32, device=DEV)),
                 lambda: awq.awq_sample(l.t(), torch.zeros(50, device=DEV)), lambda: awq.awq_sample(l, u.cpu()),
+                lambda: awq.awq_sample(l, u, top_k=2 ** 32 + 1), lambda: awq.awq_sample(l, u, top_k=-2 ** 31 - 1),
                 lambda: awq.awq_sample(l, u, temperature=float("nan")), lambda: awq.awq_sample(l[:, :0], u)):
         with pytest.raises((ValueError, awq.AwqError)):
             bad()

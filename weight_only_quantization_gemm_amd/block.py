@@ -210,6 +210,8 @@ def _setting(v, name: str, dtype: torch.dtype, n: int, index: int):
     """(pointer, value) of a setting: a vector with an entry for each row, or a number for all."""
     if isinstance(v, torch.Tensor):
         return _vector(v, name, dtype, n, index), 0
+    if dtype is _I32 and not -2 ** 31 <= v < 2 ** 31:  # would wrap round
+        raise ValueError(f"{name}={v} does not fit 32 bits")
     return None, v
 
 
