@@ -152,7 +152,9 @@ struct SampleRow {
       const auto b = __builtin_elementwise_max(a.lo, a.hi);
       return fmaxf((float)b.x, (float)b.y);
     } else {
-      return fmaxf(fmaxf((float)x[0], (float)x[1]), fmaxf((float)x[2], (float)x[3]));
+      // A signalling NaN would take its neighbour along in the three-way maximum that this becomes.
+      auto quiet = [](float v) { return __builtin_canonicalizef(v); };
+      return fmaxf(fmaxf(quiet(x[0]), quiet(x[1])), fmaxf(quiet(x[2]), quiet(x[3])));
     }
   }
   // f(piece, its number) for this thread's pieces, two under way.
