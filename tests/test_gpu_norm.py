@@ -82,7 +82,7 @@ def check(d, layer=False, scale=1.0, eps=1e-5, on_gpu=None, **more):
         top = np.abs(v).max(1)
         want = np.rint(127 * v / np.where(top > 0, top, 1)[:, None])  # exact: see code_of
         assert np.array_equal(r["x"].cpu().numpy(), want.astype(np.int8))
-        scales = top / 127 / np.sqrt((h * h).mean(1) + eps)
+        scales = top / 127 / np.where(top > 0, np.sqrt((h * h).mean(1) + eps), 1)  # a row of zeros: 0
         assert np.all(np.abs(r["scales"].cpu().numpy() - scales) <= SLACK * scales)
     else:
         x, size = normed(h, f["weight"], f["bias"], layer, eps)

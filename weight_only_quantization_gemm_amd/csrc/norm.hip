@@ -4,8 +4,15 @@
 // A row stays in the registers of the L threads that share it from its one read to
 // its last write, so every byte moves once; two statistics (post-norm) make two
 // joins over the row, a layer norm's mean and variance two each, the second from
-// the differences to the mean, so nothing cancels.  Bound by memory, at a decoding
-// step's sizes by the launch and the chain load - join - store.
+// the differences to the mean, so nothing cancels.  The row is kept in its own types
+// and widened where it is used: half the registers, so that two blocks share a compute
+// unit up to N = 16384 (4000 rows of it 111 us, 131 as fp32) and rows of 32768 fit
+// at all (2000 rows 131 us; 1045 with registers spilled to memory).
+// Bound by memory: a row of each size, in and out of memory with y and post-norm,
+//   16000 x 1024 26 us, 8000 x 2048 27 us, 16384 x 4096 107 us, 16384 x 8192 233 to
+//   248 us (with a gate), i.e. 4.4 to 5.1 TB/s where a copy reaches 5.2;
+// at a decoding step's sizes by the launch and the chain load - join - store
+// (4 x 4096 2.7 us).
 #include "awq.h"
 #include "awq_internal.h"
 #include "row_common.h"
@@ -26,9 +33,17 @@ struct RowVec<float> {
 __device__ __forceinline__ f32x8 as_f32(f16x8 v) { return widen(v); }
 __device__ __forceinline__ f32x8 as_f32(f32x8 v) { return v; }
 
+// Widened numbers of v are not kept past this: for long rows they would not fit beside the next step's.
+template <typename V, int PER>
+__device__ __forceinline__ void narrow(V (&v)[PER]) {
+  if constexpr (PER >= 4 && sizeof(V) == 16)
+#pragma unroll
+    for (int p = 0; p < PER; ++p) __asm__("" : "+v"(v[p]));
+}
+
 // mean (0 unless layer) and 1 / sqrt(variance + eps) of the row v.
-template <int L, int PER>
-__device__ __forceinline__ void statistics(const f32x8 (&v)[PER], const bool (&live)[PER], int64_t N, bool layer,
+template <int L, typename V, int PER>
+__device__ __forceinline__ void statistics(V (&v)[PER], const bool (&live)[PER], int64_t N, bool layer,
                                            float eps, float* part, float* mean, float* r) {
   constexpr int W = L / 64;
   float sum = 0.f;
@@ -37,17 +52,19 @@ __device__ __forceinline__ void statistics(const f32x8 (&v)[PER], const bool (&l
 #pragma unroll
     for (int p = 0; p < PER; ++p)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) sum += v[p][u];  // 0 beyond the row
+      for (int u = 0; u < 8; ++u) sum += (float)v[p][u];  // 0 beyond the row
     *mean = row_join<L>(sum, part, AddOp()) / (float)N;
+    narrow(v);
   }
   sum = 0.f;
 #pragma unroll
   for (int p = 0; p < PER; ++p)
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const float d = live[p] ? v[p][u] - *mean : 0.f;
+      const float d = live[p] ? (float)v[p][u] - *mean : 0.f;
       sum = fmaf(d, d, sum);
     }
+  narrow(v);
   sum = row_join<L>(sum, part + W, AddOp());
   *r = 1.f / sqrtf(sum / (float)N + eps);
 }
@@ -62,12 +79,13 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
   if (t >= a.T) return;  // a whole wave of its own row (L = 64) or the whole block
   const bool layer = a.kind == AWQ_NORM_LAYER;
   // With one eight a thread and wide rows everything is under way before the first join: 16384 x 8192 with
-  // post-norm and gate 232 us, 247 with each vector read where it is used (x 4096: 106 and 111).  Otherwise
-  // the registers cost more than the wait (16000 x 1024: 28.0 and 25.9; 4000 x 16384: 146 and 131).
+  // post-norm and gate 232 us, 247 with each vector read where it is used (x 4096: 106 and 111).  Narrower
+  // rows do not gain by it (16000 x 1024: 28.0, and 26.1 without), and longer ones have no registers for it.
   constexpr bool EARLY = PER == 1 && L >= 512;
+  constexpr bool HELD = PER * sizeof(H) <= 8;  // the weights in registers before the first store, where they fit
   bool live[PER];
-  int64_t at[PER];
-  f32x8 h[PER];
+  int at[PER];
+  HV h[PER];  // in its own type: half the registers, and what is stored is what is normed
   f16x8 w_early[PER], pw_early[PER], g_early[PER];
   auto part_of = [&](const f16* v, int p) {
     return v != nullptr && live[p] ? *reinterpret_cast<const f16x8*>(v + at[p]) : f16x8{};
@@ -78,18 +96,18 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
   const f16* gate = adds && a.gate != nullptr ? a.gate + row * a.N : nullptr;
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    at[p] = (int64_t)(p * L + lane) * 8;
+    at[p] = (p * L + lane) * 8;
     live[p] = at[p] < a.N;
-    h[p] = f32x8{};
-    if (live[p]) h[p] = as_f32(*reinterpret_cast<const HV*>(reinterpret_cast<const H*>(a.h) + t * a.h_stride + at[p]));
+    h[p] = HV{};
+    if (live[p]) h[p] = *reinterpret_cast<const HV*>(reinterpret_cast<const H*>(a.h) + t * a.h_stride + at[p]);
   }
   float mean, r;
   if (a.y != nullptr) {
-    f32x8 y[PER];
+    f16x8 y[PER];
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      y[p] = f32x8{};
-      if (live[p]) y[p] = widen(*reinterpret_cast<const f16x8*>(a.y + t * a.y_stride + at[p]));
+      y[p] = f16x8{};
+      if (live[p]) y[p] = *reinterpret_cast<const f16x8*>(a.y + t * a.y_stride + at[p]);
     }
     if constexpr (EARLY)
 #pragma unroll
@@ -100,36 +118,39 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
       }
     if (a.post_weight != nullptr) {
       statistics<L>(y, live, a.N, layer, a.eps, part, &mean, &r);
-#pragma unroll
-      for (int p = 0; p < PER; ++p) {
-        y[p] = (y[p] - mean) * r * widen(EARLY ? pw_early[p] : part_of(a.post_weight, p));
-        if (a.post_bias != nullptr) y[p] += widen(part_of(a.post_bias, p));
-      }
     }
 #pragma unroll
     for (int p = 0; p < PER; ++p)
       if (live[p]) {
-        f32x8 g = f32x8{} + a.scale;
+        if (PER * sizeof(H) >= 16) __asm__ volatile("" ::: "memory");  // the vectors of one step at a time, likewise
+        f32x8 v = widen(y[p]), g = f32x8{} + a.scale;
+        if (a.post_weight != nullptr) {
+          v = (v - mean) * r * widen(EARLY ? pw_early[p] : part_of(a.post_weight, p));
+          if (a.post_bias != nullptr) v += widen(part_of(a.post_bias, p));
+        }
         if (gate != nullptr) g *= widen(EARLY ? g_early[p] : part_of(gate, p));
-        if (adds) h[p] += y[p] * g;
-        const HV kept = __builtin_convertvector(h[p], HV);
-        h[p] = as_f32(kept);
-        *reinterpret_cast<HV*>(reinterpret_cast<H*>(a.h_out) + t * a.N + at[p]) = kept;
+        if (adds) h[p] = __builtin_convertvector(as_f32(h[p]) + v * g, HV);
       }
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      if (live[p]) *reinterpret_cast<HV*>(reinterpret_cast<H*>(a.h_out) + t * a.N + at[p]) = h[p];
   } else if constexpr (EARLY) {
 #pragma unroll
     for (int p = 0; p < PER; ++p) w_early[p] = part_of(a.weight, p);
   }
   if (a.weight == nullptr) return;
+  narrow(h);
   statistics<L>(h, live, a.N, layer, a.eps, part + 2 * W, &mean, &r);
-  f32x8 w[PER];
+  f16x8 w_held[PER];
+  if constexpr (!EARLY && HELD)
 #pragma unroll
-  for (int p = 0; p < PER; ++p) w[p] = widen(EARLY ? w_early[p] : part_of(a.weight, p));
+    for (int p = 0; p < PER; ++p) w_held[p] = part_of(a.weight, p);
+  auto w = [&](int p) { return widen(EARLY ? w_early[p] : HELD ? w_held[p] : part_of(a.weight, p)); };
   if (a.x_scales == nullptr) {
 #pragma unroll
     for (int p = 0; p < PER; ++p)
       if (live[p]) {
-        f32x8 x = (h[p] - mean) * r * w[p];
+        f32x8 x = (as_f32(h[p]) - mean) * r * w(p);
         if (a.bias != nullptr) x += widen(part_of(a.bias, p));
         *reinterpret_cast<f16x8*>(reinterpret_cast<f16*>(a.x) + t * a.N + at[p]) = __builtin_convertvector(x, f16x8);
       }
@@ -137,18 +158,17 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
   }
   float top = 0.f;
 #pragma unroll
-  for (int p = 0; p < PER; ++p) {
-    w[p] *= h[p];
-    top = largest_of(top, w[p]);
-  }
+  for (int p = 0; p < PER; ++p) top = largest_of(top, as_f32(h[p]) * w(p));
+  narrow(h);
   top = row_join<L>(top, part + 4 * W, MaxOp());
   const float by = 127.f / top;
 #pragma unroll
   for (int p = 0; p < PER; ++p)
     if (live[p]) {
+      const f32x8 v = as_f32(h[p]) * w(p);
       float c[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) c[u] = code_of(w[p][u], by, top);
+      for (int u = 0; u < 8; ++u) c[u] = code_of(v[u], by, top);
       *reinterpret_cast<u32x2*>(reinterpret_cast<int8_t*>(a.x) + t * a.N + at[p]) =
           u32x2{code_word(c[0], c[1], c[2], c[3]), code_word(c[4], c[5], c[6], c[7])};
     }
