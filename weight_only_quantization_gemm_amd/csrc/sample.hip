@@ -271,10 +271,26 @@ struct SampleRow {
     lds_barrier();
   }
 
-  // list = the tokens that reach `least`, of what b keeps with weights from low on, in any order, and returns their
-  // number (more than kList: only some are in the list).  most: the largest logits of this thread's slots
-  // (slot q: pieces q, q + kSlots, .. of it).
-  __device__ __forceinline__ int gather(const float (&most)[kSlots], float least, const Border& b, double low) const {
+  // A piece's elements with bits in `in` to the list's end (sh.n, which counts on beyond MOST); by whole waves, with
+  // one access to it for each.
+  template <int MOST>
+  __device__ __forceinline__ void append(vec x, int j, uint32_t in) const {
+    if (!__any(in != 0)) return;
+    const int count = __popc(in), upto = wave_scan(count);
+    int at = 0;
+    if ((threadIdx.x & 63) == 0) at = atomicAdd(&sh.n, __builtin_amdgcn_readlane(upto, 63));
+    at = __builtin_amdgcn_readfirstlane(at) + upto - count;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if ((in >> e & 1) && at < MOST) sh.list[at] = entry((float)x[e], j * E - lead + e);
+      at += in >> e & 1;
+    }
+  }
+
+  // list = the tokens that reach `least` with weights from low on, in any order, and returns their number (more than
+  // kList: only some are in the list).  most: the largest logits of this thread's slots (slot q: pieces q, q + kSlots,
+  // .. of it).
+  __device__ __forceinline__ int gather(const float (&most)[kSlots], float least, double low) const {
     uint32_t slots = 0;
     const float finite = fmaxf(least, -3.4028235e38f);  // not -inf, a slot without a logit
 #pragma unroll
@@ -303,24 +319,11 @@ struct SampleRow {
           const vec x = load(j < end ? j : 0);
           uint32_t in = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float l = (float)x[e];
-            in |= (j < end) & (l >= finite) & b.keeps(l, j * E - lead + e) ? 1u << e : 0u;
-          }
+          for (int e = 0; e < E; ++e) in |= (j < end) & ((float)x[e] >= finite) ? 1u << e : 0u;
           if (low > 0.0)
 #pragma unroll
             for (int e = 0; e < E; ++e) in &= unrounded((float)x[e]) >= low ? ~0u : ~(1u << e);
-          // places for the wave's tokens by one access
-          const int count = __popc(in), upto = wave_scan(count), all = __builtin_amdgcn_readlane(upto, 63);
-          if (all == 0) continue;
-          int at = 0;
-          if ((threadIdx.x & 63) == 0) at = atomicAdd(&sh.n, all);
-          at = __builtin_amdgcn_readfirstlane(at) + upto - count;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if ((in >> e & 1) && at < kList) sh.list[at] = entry((float)x[e], j * E - lead + e);
-            at += in >> e & 1;
-          }
+          append<kList>(x, j, in);
         }
       }
     }
@@ -410,8 +413,9 @@ struct SampleRow {
     const uint64_t e = lane64(sh.list[i], 0);
     return {entry_logit(e), (int)~(uint32_t)e};
   }
-  // Whether the row's chunks have sums in choose_of_list.
-  __device__ __forceinline__ bool chunks_fit() const { return (lead + V + E - 1) / E <= 64 * (kFound / 2); }
+  // Whether sh.chunks holds a sum for each chunk of the row.
+  __device__ __forceinline__ int chunks() const { return ((lead + V + E - 1) / E + 63) / 64; }
+  __device__ __forceinline__ bool chunks_fit() const { return chunks() <= kFound / 2; }
 
   // Of the sorted list's first n entries, how many are kept.
   __device__ __forceinline__ int kept_of_list(int n, int k, float p, double low) const {
@@ -476,20 +480,24 @@ struct SampleRow {
   // The token at `share` of the first n entries of the list (in any order), which are what b keeps with weights
   // from low on: their weights summed by chunk, in index order.
   __device__ __forceinline__ int choose_of_list(int n, const Border& b, double low, float share, float* prob) const {
-    const int pieces = (lead + V + E - 1) / E, chunks = (pieces + 63) / 64, per = (chunks + THREADS - 1) / THREADS;
     lds_barrier();
 #pragma unroll 1
-    for (int i = threadIdx.x; i < chunks; i += THREADS) sh.chunks[i] = 0;
+    for (int i = threadIdx.x; i < chunks(); i += THREADS) sh.chunks[i] = 0;
     lds_barrier();
 #pragma unroll 1
     for (int i = threadIdx.x; i < n; i += THREADS) {
       const uint64_t e = sh.list[i], w = whole(unrounded(entry_logit(e)));
       atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunks[((int)~(uint32_t)e + lead) / (64 * E)]), (unsigned long long)w);
     }
+    return choose_of_chunks(b, low, share, prob);
+  }
+  // The same with the weights' sums by chunk in sh.chunks.
+  __device__ __forceinline__ int choose_of_chunks(const Border& b, double low, float share, float* prob) const {
+    const int per = (chunks() + THREADS - 1) / THREADS;
     lds_barrier();
     uint64_t mine = 0, upto;
 #pragma unroll 1
-    for (int i = threadIdx.x * per; i < (int)(threadIdx.x + 1) * per && i < chunks; ++i) mine += sh.chunks[i];
+    for (int i = threadIdx.x * per; i < (int)(threadIdx.x + 1) * per && i < chunks(); ++i) mine += sh.chunks[i];
     const uint64_t total = block_sum(mine, 0, &upto), target = target_of(share, total);
     if (upto > target && upto - mine <= target) {
       uint64_t left = target - (upto - mine);
@@ -683,8 +691,9 @@ struct SampleRow {
   }
 
   // Narrows b to the tokens up to the rank_at-th in order (rank_at > 0), or up to the first at which the
-  // weights reach the share p of all of b's; everything stays where that is not reached.
-  __device__ __forceinline__ void cut(Border* b, uint64_t rank_at, float p, float range) const {
+  // weights reach the share p of all of b's; everything stays where that is not reached.  With `sums` (chunks_fit)
+  // the weights from low on of what stays are left in sh.chunks where the result is true.
+  __device__ __forceinline__ bool cut(Border* b, uint64_t rank_at, float p, float range, bool sums, double low) const {
     constexpr int PER = kBins / THREADS;
     const bool by_count = rank_at > 0;
     const float step = fminf((float)kBins / range, 1e30f);
@@ -744,55 +753,90 @@ struct SampleRow {
     const int bin = __builtin_amdgcn_readfirstlane((int)sh.found[0]);
     const uint64_t above = lane64(sh.found[1], 0);
     lds_barrier();
-    if (bin == kBins) return;
+    if (bin == kBins) return false;
     const Border old = *b;
     // the bin's logits and, for its roundings, a little more
     const float slack = 1e-5f * (fabsf((float)top) + range);
     const float to = step > 0.f ? (float)top - (float)bin / step + slack : INFINITY;  // 0: an infinite range, one bin
-    const float from = step > 0.f && bin < kBins - 1 ? (float)top - (float)(bin + 1) / step - slack : -INFINITY;
+    const float from = step > 0.f ? (float)top - (float)(bin + 1) / step - slack : -INFINITY;  // below range: no weight
     if (threadIdx.x == 0) sh.n = 0;
     lds_barrier();
+    // The list takes the bin's tokens and some beside it; those above it stay for sure, and each wave lines a
+    // chunk's up in LDS and weighs 64 at a time.
+    static_assert(kSort + WAVES * 32 * E <= kList, "queues behind the list's first kSort");
+    const int lane = threadIdx.x & 63;
+    float* queue = reinterpret_cast<float*>(sh.list + kSort) + (threadIdx.x >> 6) * (64 * E);
     each([&](vec x, int j) {
-      bool any = false;
-#pragma unroll
-      for (int e = 0; e < E; ++e) any |= ((float)x[e] >= from) & ((float)x[e] <= to);
-      if (!any) return;
+      uint32_t in = 0, near = 0;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float l = (float)x[e];
-        const int i = j * E - lead + e;
-        if (bin_of(l) == bin && old.keeps(l, i) && weight(l) > 0.0) {
-          const int at = atomicAdd(&sh.n, 1);
-          if (at < kSort) sh.list[at] = entry(l, i);
-        }
+        const bool reaches = (l >= from) & old.keeps(l, j * E - lead + e);
+        in |= reaches ? 1u << e : 0u;
+        near |= reaches & (l <= to) ? 1u << e : 0u;
       }
+      append<kSort>(x, j, near);
+      if (!sums) return;
+      uint64_t sum = 0;
+      if (__any(in != 0)) {
+        const int count = __popc(in), upto = wave_scan(count), n = __builtin_amdgcn_readlane(upto, 63);
+        int at = upto - count;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (in >> e & 1) queue[at] = (float)x[e];
+          at += in >> e & 1;
+        }
+        __asm__ volatile("" ::: "memory");  // a wave's LDS accesses are done in order
+#pragma unroll 1
+        for (int q = lane; q - lane < n; q += 64) {
+          const float l = queue[q < n ? q : 0];
+          const double v = unrounded(l);
+          sum += whole((q < n) & (bin_of(l) < bin) & (v >= low) ? v : 0.0);
+        }
+        __asm__ volatile("" ::: "memory");
+        sum = scan64(sum);
+      }
+      if (lane == 63 && j / 64 < chunks()) sh.chunks[j / 64] = sum;
     });
     lds_barrier();
     const int n = __builtin_amdgcn_readfirstlane(sh.n);
     if (n > kSort) {
       lds_barrier();
       *b = digits(old, rank_at, least);
-      return;
+      return false;
     }
     sort(n);
-    // the entry at which it is reached
+    // the entry at which it is reached, among those of the bin; one of no weight cannot be chosen, kept or not
+    auto weight_of = [&](uint64_t e) { return bin_of(entry_logit(e)) == bin ? weight(entry_logit(e)) : 0.0; };
     uint64_t carry = above;
     for (int i0 = 0; i0 < n; i0 += THREADS) {
       const int i = i0 + threadIdx.x;
-      const uint64_t own = i >= n ? 0 : by_count ? 1 : (uint64_t)weight(entry_logit(sh.list[i]));
+      const double w = i < n ? weight_of(sh.list[i]) : 0.0;
+      const uint64_t own = !by_count ? (uint64_t)w : w > 0.0 ? 1 : 0;
       uint64_t to;
       const uint64_t all = block_sum(own, (i0 / THREADS) & 1, &to);
       to += carry;
-      if (i < n && reached(to) && (to == own || !reached(to - own))) sh.found[0] = sh.list[i];
+      if (own > 0 && reached(to) && (to == own || !reached(to - own))) {
+        sh.found[0] = sh.list[i];
+        sh.found[1] = i;
+      }
       carry += all;
     }
     lds_barrier();
-    const uint64_t e = sh.found[0];
+    const uint64_t e = lane64(sh.found[0], 0);
+    const int last = __builtin_amdgcn_readfirstlane((int)sh.found[1]);
     lds_barrier();
-    b->value = entry_logit(lane64(e, 0));
-    b->last = (int)~(uint32_t)lane64(e, 0);
+    b->value = entry_logit(e);
+    b->last = (int)~(uint32_t)e;
+    if (!sums) return false;
+    for (int i = threadIdx.x; i <= last; i += THREADS) {
+      const uint64_t at = sh.list[i];
+      const double w = weight_of(at);
+      if (w > 0.0 && unrounded(entry_logit(at)) >= low)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunks[((int)~(uint32_t)at + lead) / (64 * E)]), (unsigned long long)w);
+    }
+    return true;
   }
-
 };
 
 // top-k up to which a list is tried at once: of 1024 threads' maxima the k-th leaves about
@@ -899,50 +943,30 @@ __global__ __launch_bounds__(THREADS, 4) void sample_kernel(SampleArgs a) {
     const double low = m > 0.f ? (double)m * kWeightOne : 0.0;
     // logits whose weights are not 0: from hi down to -31 t, or to the smallest there is
     const float range = s.infinite ? 31.f * t : fminf(31.f * t, hi - lo);
-    // first a list of all that can be kept, where that is likely to be short; then a list of what is found to be
-    // kept; otherwise the row
+    // first a list of all that can be kept, where that is likely to be short
     Border b{-INFINITY, 0x7FFFFFFF};
-    float least = NAN;  // no list
-    double low_here = 0.0;
+    int n = Row::kList + 1;
     if (s.infinite) {
       // ties: no list
     } else if (ranked && k <= kListK<THREADS>) {
-      least = s.reached_by(k, mine, hi, range);
+      n = s.gather(slot, s.reached_by(k, mine, hi, range), 0.0);
     } else if (!cut_by_share && low > 0.0) {  // w >= m is l >= hi + t ln m, here a little less
-      least = fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY);
-      low_here = low;
+      n = s.gather(slot, fmaxf(hi + t * logf(m) - 1e-4f * (fabsf(hi) + t), -INFINITY), low);
     }
-    bool cut = false;
-#pragma unroll 1
-    for (;;) {
-      int n = Row::kList + 1;
-      if (least >= -INFINITY) n = s.gather(slot, least, b, low_here);
-      n = __builtin_amdgcn_readfirstlane(n);
-      if (n <= 64) {
-        token = s.choose_of_few(n, cut ? 0 : k, cut ? 1.f : p, cut ? 0.0 : low, share, &prob);
-        break;
-      }
-      if (!cut && n <= Row::kSort) {
-        s.sort(n);
-        n = s.kept_of_list(n, k, p, low);
-        b = s.border_of(n - 1);
-      }
-      const bool listed = cut ? n <= Row::kList : b.value > -INFINITY;  // all that is kept, which b says
-      const double low_left = cut ? low : 0.0;
-      if (listed && s.chunks_fit()) {
-        token = s.choose_of_list(n, b, low_left, share, &prob);
-        break;
-      }
-      if (cut || listed) {
-        token = s.choose_of_row(b, low_left, share, &prob);
-        break;
-      }
+    n = __builtin_amdgcn_readfirstlane(n);
+    if (n <= 64) {
+      token = s.choose_of_few(n, k, p, low, share, &prob);
+    } else if (n <= Row::kSort) {
+      s.sort(n);
+      n = s.kept_of_list(n, k, p, low);
+      b = s.border_of(n - 1);
+      token = s.chunks_fit() ? s.choose_of_list(n, b, 0.0, share, &prob) : s.choose_of_row(b, 0.0, share, &prob);
+    } else {
+      bool summed = false;
 #pragma unroll 1
       for (int by_weight = ranked ? 0 : 1; by_weight <= (cut_by_share ? 1 : 0); ++by_weight)
-        s.cut(&b, by_weight ? 0 : (uint64_t)k, p, range);
-      cut = true;
-      least = !s.infinite && b.value > -INFINITY ? b.value : NAN;
-      low_here = low;
+        summed = s.cut(&b, by_weight ? 0 : (uint64_t)k, p, range, by_weight == (cut_by_share ? 1 : 0) && s.chunks_fit(), low);
+      token = summed ? s.choose_of_chunks(b, low, share, &prob) : s.choose_of_row(b, low, share, &prob);
     }
   }
   if (tid == 0) {
