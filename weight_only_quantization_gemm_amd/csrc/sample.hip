@@ -8,19 +8,27 @@
 //   few tokens kept (top-k up to kListK, or min-p alone): a logit that at least k
 //   threads' own maxima reach leaves a list short enough to sort;
 //   otherwise: a histogram of the weights (or counts) over equal steps of the
-//   logit finds the border's bin, whose tokens are then sorted.  A bin with more
-//   tokens than the list holds (ties) is searched digit by digit instead.
-// The choice walks sums in index order: over the list where it holds all that is
-// kept, over the row otherwise.
+//   logit finds the border's bin; a further pass lists that bin's tokens, which are
+//   sorted, and sums the weights of those above it by chunks of 64 pieces.  A bin
+//   with more tokens than the list holds (ties) is searched digit by digit instead.
+// The choice walks sums in index order: of chunks, then of the chosen chunk's pieces.
 //
 // Weights are whole multiples of 2^-43, so their sums are exact in any order and
 // the result does not depend on timing; a row's sum stays below 2^63.
+//
+// Bounds and times (fp16 logits).  Lists: the chain of a first pass, 20 barriers and
+// a short sort; 1 x 32000 9.4 us, 61 x 50021 12 us, 512 x 131072 34 us with top-k 50,
+// top-p and min-p (its one read takes 26 us at a copy's rate).  Passes over all
+// weights: vector instructions, some 20 a token (a weight alone is 16 in 64 bits)
+// on the row's compute unit; unfiltered 20, 85 us for the two batches, top-p 0.9 46
+// and 189 us, of which histogram and border pass take 17 us each at 50021 tokens.
 #include "awq_internal.h"
 #include "row_common.h"
 
 namespace awq {
 
 constexpr double kWeightOne = 8796093022208.0;  // 2^43
+constexpr double kHalfUnit = 4503599627370496.0;  // 2^52, from where on a double's spacing is 1
 constexpr int kExpTable = 512, kSlots = 16;
 constexpr double kExpRate = 738.6598609351493;  // kExpTable log2(e)
 
@@ -92,12 +100,12 @@ __device__ __forceinline__ float wave_min(float v) { return -wave_max(-v); }
 
 template <int THREADS>
 struct SampleShared {
-  static constexpr int kList = 8 * THREADS, kSort = 2 * THREADS, kBins = 2 * THREADS, kFound = 5 * THREADS;
-  uint64_t list[kList];  // entries, or the bins' weights
+  static constexpr int kList = 5 * THREADS, kSort = 2 * THREADS, kBins = 2 * THREADS, kFound = 5 * THREADS;
+  uint64_t list[kList];  // up to kSort entries, the bins' weights, or tokens that wait to be weighed
   union {
     uint32_t counts[kBins];         // the bins' counts
     uint32_t slots[kFound];         // slots with tokens for the list
-    uint64_t chunks[kFound / 2];    // sums of the list's tokens, for each 64 pieces
+    uint64_t chunks[kFound / 2];    // sums of what is kept, for each 64 pieces
   };
   double table[kExpTable];  // exp_entry
   uint64_t part[2][THREADS / 64];
@@ -174,8 +182,8 @@ struct SampleRow {
   //   exp(z) = 2^(i / 512) (1 + g),  g = exp(f ln2 / 512) - 1 to the third power of f, |f| <= 1/2
   // (the fourth is below 2^-46).  Below z = -31 it is none, and for a NaN.  Whole parts are split off
   // by adding and subtracting 1.5 2^52 and 2^52.
-  __device__ __forceinline__ double unrounded(float x, double c3 = 4.1353783506767136e-10) const {
-    constexpr double c1 = 0.0013538030870311431, c2 = 9.163913992275265e-07;  // (ln2/512)^n / n!
+  __device__ __forceinline__ double unrounded(float x) const {
+    constexpr double c1 = 0.0013538030870311431, c2 = 9.163913992275265e-07, c3 = 4.1353783506767136e-10;  // (ln2/512)^n / n!
     constexpr double kWhole = 6755399441055744.0;
     const double y = fmax(((double)x - top) * rate, -31.0 * kExpRate);
     const double shifted = y + kWhole, f = y - (shifted - kWhole);
@@ -185,13 +193,11 @@ struct SampleRow {
     return fma(two, f * fma(f, fma(f, c3, c2), c1), two);
   }
   __device__ __forceinline__ double weight(float x) const {
-    constexpr double kHalfUnit = 4503599627370496.0;  // 2^52, where a double's spacing is 1
     return (unrounded(x) + kHalfUnit) - kHalfUnit;
   }
 
   // The same as a whole number: adding 2^52 leaves it in the double's low bits.
   static __device__ __forceinline__ uint64_t whole(double unrounded) {
-    constexpr double kHalfUnit = 4503599627370496.0;
     return (uint64_t)__double_as_longlong(unrounded + kHalfUnit) - (uint64_t)__double_as_longlong(kHalfUnit);
   }
   // Those of a piece, with ALL of every token, otherwise of what b keeps from low on (0 for others); side
@@ -271,24 +277,22 @@ struct SampleRow {
     lds_barrier();
   }
 
-  // A piece's elements with bits in `in` to the list's end (sh.n, which counts on beyond MOST); by whole waves, with
+  // A piece's elements with bits in `in` to the list's end (sh.n, which counts on beyond kSort); by whole waves, with
   // one access to it for each.
-  template <int MOST>
   __device__ __forceinline__ void append(vec x, int j, uint32_t in) const {
-    if (!__any(in != 0)) return;
     const int count = __popc(in), upto = wave_scan(count);
     int at = 0;
     if ((threadIdx.x & 63) == 0) at = atomicAdd(&sh.n, __builtin_amdgcn_readlane(upto, 63));
     at = __builtin_amdgcn_readfirstlane(at) + upto - count;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      if ((in >> e & 1) && at < MOST) sh.list[at] = entry((float)x[e], j * E - lead + e);
+      if ((in >> e & 1) && at < kSort) sh.list[at] = entry((float)x[e], j * E - lead + e);
       at += in >> e & 1;
     }
   }
 
   // list = the tokens that reach `least` with weights from low on, in any order, and returns their number (more than
-  // kList: only some are in the list).  most: the largest logits of this thread's slots (slot q: pieces q, q + kSlots,
+  // kSort: only some are in the list).  most: the largest logits of this thread's slots (slot q: pieces q, q + kSlots,
   // .. of it).
   __device__ __forceinline__ int gather(const float (&most)[kSlots], float least, double low) const {
     uint32_t slots = 0;
@@ -323,12 +327,12 @@ struct SampleRow {
           if (low > 0.0)
 #pragma unroll
             for (int e = 0; e < E; ++e) in &= unrounded((float)x[e]) >= low ? ~0u : ~(1u << e);
-          append<kList>(x, j, in);
+          if (__any(in != 0)) append(x, j, in);
         }
       }
     }
     lds_barrier();
-    const int n = slots_found <= kFound ? __builtin_amdgcn_readfirstlane(sh.n) : kList + 1;
+    const int n = slots_found <= kFound ? __builtin_amdgcn_readfirstlane(sh.n) : kSort + 1;
     lds_barrier();
     return n;
   }
@@ -531,7 +535,8 @@ struct SampleRow {
       });
     } else {
       // Only what b keeps is weighed: each wave lines its tokens up in LDS and takes 64 at a time.
-      float* queue = reinterpret_cast<float*>(sh.list) + wave * (kList * 2 / WAVES);  // of 1024; 64 E + 63 are used
+      float* queue = reinterpret_cast<float*>(sh.list) + wave * (kList * 2 / WAVES);
+      static_assert(64 * E + 63 <= kList * 2 / WAVES, "a wave's queue");
       int waiting = 0;
       lds_barrier();
       auto take = [&](int n) {  // the last n
@@ -761,42 +766,30 @@ struct SampleRow {
     const float from = step > 0.f ? (float)top - (float)(bin + 1) / step - slack : -INFINITY;  // below range: no weight
     if (threadIdx.x == 0) sh.n = 0;
     lds_barrier();
-    // The list takes the bin's tokens and some beside it; those above it stay for sure, and each wave lines a
-    // chunk's up in LDS and weighs 64 at a time.
-    static_assert(kSort + WAVES * 32 * E <= kList, "queues behind the list's first kSort");
-    const int lane = threadIdx.x & 63;
-    float* queue = reinterpret_cast<float*>(sh.list + kSort) + (threadIdx.x >> 6) * (64 * E);
+    // The list takes the bin's tokens and some beside it; the weights of those above, which stay for sure, are summed
+    // by chunk.
     each([&](vec x, int j) {
-      uint32_t in = 0, near = 0;
+      bool any = false;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float l = (float)x[e];
-        const bool reaches = (l >= from) & old.keeps(l, j * E - lead + e);
-        in |= reaches ? 1u << e : 0u;
-        near |= reaches & (l <= to) ? 1u << e : 0u;
-      }
-      append<kSort>(x, j, near);
-      if (!sums) return;
-      uint64_t sum = 0;
-      if (__any(in != 0)) {
-        const int count = __popc(in), upto = wave_scan(count), n = __builtin_amdgcn_readlane(upto, 63);
-        int at = upto - count;
+      for (int e = 0; e < E; ++e) any |= ((float)x[e] >= from) & ((float)x[e] <= to);
+      if (__any(any)) {
+        uint32_t near = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if (in >> e & 1) queue[at] = (float)x[e];
-          at += in >> e & 1;
+          const float l = (float)x[e];
+          near |= (l >= from) & (l <= to) & old.keeps(l, j * E - lead + e) ? 1u << e : 0u;
         }
-        __asm__ volatile("" ::: "memory");  // a wave's LDS accesses are done in order
-#pragma unroll 1
-        for (int q = lane; q - lane < n; q += 64) {
-          const float l = queue[q < n ? q : 0];
-          const double v = unrounded(l);
-          sum += whole((q < n) & (bin_of(l) < bin) & (v >= low) ? v : 0.0);
-        }
-        __asm__ volatile("" ::: "memory");
-        sum = scan64(sum);
+        append(x, j, near);
       }
-      if (lane == 63 && j / 64 < chunks()) sh.chunks[j / 64] = sum;
+      if (!sums) return;
+      double v[E];
+      uint64_t sum = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = unrounded((float)x[e]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum += whole(((float)x[e] > to) & (v[e] >= low) ? v[e] : 0.0);
+      sum = scan64(sum);
+      if ((threadIdx.x & 63) == 63 && j / 64 < chunks()) sh.chunks[j / 64] = sum;
     });
     lds_barrier();
     const int n = __builtin_amdgcn_readfirstlane(sh.n);
@@ -831,8 +824,8 @@ struct SampleRow {
     if (!sums) return false;
     for (int i = threadIdx.x; i <= last; i += THREADS) {
       const uint64_t at = sh.list[i];
-      const double w = weight_of(at);
-      if (w > 0.0 && unrounded(entry_logit(at)) >= low)
+      const double w = weight(entry_logit(at));
+      if (unrounded(entry_logit(at)) >= low)
         atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunks[((int)~(uint32_t)at + lead) / (64 * E)]), (unsigned long long)w);
     }
     return true;
@@ -857,7 +850,10 @@ __global__ __launch_bounds__(THREADS, 4) void sample_kernel(SampleArgs a) {
   const int lead = (int)((reinterpret_cast<uintptr_t>(start) & 15) / sizeof(T));
   const int pieces = (lead + (int)a.V + E - 1) / E, cw = (pieces + THREADS - 1) / THREADS;
   const int bytes = ((lead + (int)a.V) * (int)sizeof(T) + 3) & ~3;
-  Row s{sh, __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(start - lead), 0, bytes, 0x00020000), lead, (int)a.V, cw, false, 0.0, 0.0};
+  // a register of its own: as one of the arguments' sixteen it would bring all of them back in each step of a loop
+  int V;
+  __asm__("s_mov_b32 %0, %1" : "=s"(V) : "s"((int)a.V));
+  Row s{sh, __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(start - lead), 0, bytes, 0x00020000), lead, V, cw, false, 0.0, 0.0};
 
   const float t = a.temperature ? a.temperature[r] : a.temperature_value;
   const int32_t k = a.top_k ? a.top_k[r] : a.top_k_value;
@@ -936,7 +932,7 @@ __global__ __launch_bounds__(THREADS, 4) void sample_kernel(SampleArgs a) {
     token = sh.n;
     prob = 1.f;
   } else {
-    const bool ranked = k >= 1 && k < a.V, cut_by_share = p < 1.f;
+    const bool ranked = k >= 1 && k < V, cut_by_share = p < 1.f;
     s.infinite = hi == INFINITY;
     s.top = s.infinite ? 0.0 : (double)hi;
     s.rate = fmin(kExpRate / (double)t, 1e300);
@@ -945,7 +941,7 @@ __global__ __launch_bounds__(THREADS, 4) void sample_kernel(SampleArgs a) {
     const float range = s.infinite ? 31.f * t : fminf(31.f * t, hi - lo);
     // first a list of all that can be kept, where that is likely to be short
     Border b{-INFINITY, 0x7FFFFFFF};
-    int n = Row::kList + 1;
+    int n = Row::kSort + 1;
     if (s.infinite) {
       // ties: no list
     } else if (ranked && k <= kListK<THREADS>) {
@@ -980,9 +976,9 @@ static void sample_launch(const SampleArgs& a, int64_t B, hipStream_t st) {
   const int64_t pieces = (a.V + 2 * (16 / sizeof(T)) - 2) / (16 / sizeof(T));  // with any lead
   const dim3 grid((unsigned)B);
   // Rows of few pieces need few threads.  Where every row is cut to a short list, 512 threads: two rows share a
-  // compute unit, and fewer waves meet at the barriers (top-k 50, top-p, min-p: 512 x 131072 42.7 us, 47.4 with
-  // 1024; 1 x 32000 10.2 and 12.3).  Where rows may need passes over all weights, 1024 (mixed settings: 512 x
-  // 131072 139 us, 173 with 512).
+  // compute unit, and fewer waves meet at the barriers (top-k 50, top-p, min-p, before later steps: 512 x 131072
+  // 42.7 us, 47.4 with 1024; 1 x 32000 10.2 and 12.3).  Where rows may need passes over all weights, 1024 (mixed
+  // settings, likewise: 512 x 131072 139 us, 173 with 512).
   const bool lists = a.top_k == nullptr && a.top_k_value >= 1 && a.top_k_value <= kListK<512>;
   if (pieces <= 1024) sample_kernel<T, 256, 4><<<grid, dim3(256), 0, st>>>(a);
   else if (lists) sample_kernel<T, 512, 8><<<grid, dim3(512), 0, st>>>(a);
