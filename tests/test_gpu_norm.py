@@ -239,3 +239,11 @@ def test_rows_in_8_bits_without_eps_and_not_finite():
         r = awq.awq_norm(**dev, eps=0.0, quantize=True)
         assert r["scales"][3:].isnan().all()
         assert torch.equal(r["x"][:3], want["x"][:3]) and torch.equal(r["scales"][:3], want["scales"][:3])
+
+
+@pytest.mark.parametrize("N", [11000, 24576, 40000, 65528])
+@pytest.mark.parametrize("wide", [False, True])
+def test_long_rows_with_everything(N, wide):
+    check(make(5, N, seed=N, wide=wide, post=True, bias=True, gate="rows"), layer=True, scale=0.75)
+    check(make(3, N, seed=N + 1, wide=wide, post=True, gate="tokens"), quantize=True)
+    check(make(2, N, seed=N + 2, wide=wide, y=False, bias=True, offset=50.0), layer=True)
