@@ -195,6 +195,10 @@ static hipError_t norm_launch(const NormArgs& a, int h_bytes, hipStream_t st) {
   return hipGetLastError();
 }
 
+// By the row's length alone, so that a row's sums, and its result, do not depend on the rows beside it.  With post-norm,
+// beside the nearest other layout: 16000 x 512 16 us (31 with 256 threads a row); x 1024 27 (39; but 300 rows 4.2 and
+// 3.4); 8000 x 2048 27 (30 with a wave a row, and 4 rows 3.0 and 5.3); x 4096 52 (48 with 256 threads and two eights;
+// 4 rows 3.4 and 4.0); x 8192 107 (106 with 512; 4 rows 4.3 and 4.4); 4000 x 16384 112 (118 with 512).
 hipError_t launch_norm(const NormArgs& a, int h_bytes, hipStream_t st) {
   if (a.N <= 512) return norm_launch<64, 1>(a, h_bytes, st);
   if (a.N <= 1024) return norm_launch<64, 2>(a, h_bytes, st);

@@ -17,8 +17,8 @@
 // the result does not depend on timing; a row's sum stays below 2^63.
 //
 // Bounds and times (fp16 logits).  Lists: the chain of a first pass, 20 barriers and
-// a short sort; 1 x 32000 9.4 us, 61 x 50021 12 us, 512 x 131072 34 us with top-k 50,
-// top-p and min-p (its one read takes 26 us at a copy's rate).  Passes over all
+// a short sort; 1 x 32000 9.4 us, 61 x 50021 12 us, 512 x 131072 35 to 42 us with top-k
+// 50, top-p and min-p (its one read takes 26 us at a copy's rate).  Passes over all
 // weights: vector instructions, some 20 a token (a weight alone is 16 in 64 bits)
 // on the row's compute unit; unfiltered 20, 85 us for the two batches, top-p 0.9 46
 // and 189 us, of which histogram and border pass take 17 us each at 50021 tokens.
