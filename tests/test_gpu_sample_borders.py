@@ -1,0 +1,58 @@
+"""awq_sample at the border of min-p, where a weight and its nearest multiple of 2^-43 fall on different
+sides of m: w_i >= m is asked of the weight itself, whichever way a row's tokens are found.
+
+m is some 88 of the sums' units, 87.96 or 88.30 of them, and the packed logits' weights lie within a unit of it, so
+some round across it, either way.  The random number is 1, so the token is the last one kept that has a weight: a token wrongly kept or
+dropped is the answer itself.  The inputs have no weight within 2^-40 of m (relative), where 64 bits would not decide."""
+import numpy as np
+import pytest
+import torch
+
+import weight_only_quantization_gemm_amd as awq
+from test_gpu_sample import choose
+
+UNIT = 2.0 ** -43
+B, PACKED = 64, 24
+DEV = "cuda:0"
+
+
+def rows(first, V, m, t, seed):
+    """Logits [B][V]: `first` zeros, then -inf, and at the end packed ones whose weights at temperature t are
+    within a unit of m.  The first of them in order is a zero."""
+    g = np.random.default_rng(seed)
+    l = np.full((B, V), -np.inf, np.float32)
+    l[:, :first] = 0.0
+    w = (m / UNIT + g.uniform(-0.9, 0.9, (B, PACKED))) * UNIT
+    l[:, V - PACKED:] = np.float32(t) * np.log(w)
+    exact = np.exp(l[:, V - PACKED:].astype(np.longdouble) / np.longdouble(np.float32(t)))
+    assert np.abs(exact / np.longdouble(m) - 1).min() > 2.0 ** -40
+    rounded = np.rint((exact / UNIT).astype(np.float64)) * UNIT
+    crossing = (exact >= m) != (rounded >= m)
+    assert crossing.any(1).sum() > B // 4  # rows with a token that rounds across m
+    return l
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("units", [87.96, 88.30])
+@pytest.mark.parametrize("t", [1.0, 0.7, 1.9])
+@pytest.mark.parametrize("first,V,top_k", [
+    (1, 25, 0),            # one short list, cut by min-p
+    (1, 60, 25), (20, 50, 44), (1, 5003, 25),  # a short list of the top-k
+    (80, 5003, 104),       # a list to sort
+    (80, 50021, 590), (80, 50021, 650), (400, 50021, 424),   # lists, or a histogram, by the kernel's size
+    (80, 5003, 2000), (3000, 50021, 3024), (3000, 50021, 0),  # passes over the row
+])
+def test_min_p_is_asked_of_the_weight(first, V, top_k, t, units):
+    m = float(np.float32(units * UNIT))
+    logits = rows(first, V, m, t, seed=V + top_k)
+    u = np.ones(B, np.float32)
+    want = [choose(logits[b], t, top_k, 1.0, m, u[b]) for b in range(B)]
+    dl, du = torch.from_numpy(logits).to(DEV), torch.from_numpy(u).to(DEV)
+    every = lambda v, dtype: torch.full((B,), v, dtype=dtype, device=DEV)  # noqa: E731
+    for k in (top_k, every(top_k, torch.int32)):
+        for p in (m, every(m, torch.float32)):
+            r = awq.awq_sample(dl, du, temperature=t, top_k=k, min_p=p)
+            assert r["tokens"].tolist() == [token for token, _ in want]
+            prob = np.array([prob for _, prob in want])
+            # the quotient's rounding to fp32; a sum of at least 1 whose packed weights are within half a unit each
+            assert np.all(np.abs(r["probs"].cpu().numpy() - prob) <= (2.0 ** -24 + PACKED * 2.0 ** -44) * prob)

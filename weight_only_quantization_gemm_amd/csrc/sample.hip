@@ -369,11 +369,11 @@ struct SampleRow {
     return last == STEPS ? -INFINITY : least;
   }
 
-  // The token at `share` of the first n <= 64 entries of the sorted list, by the first wave: lane i has
-  // entry i (0 from n on).
-  __device__ __forceinline__ void choose_in_wave(uint64_t e, int n, float share) const {
+  // The token at `share` of those of the first n <= 64 entries of the sorted list with weights from low on, by the
+  // first wave: lane i has entry i (0 from n on).
+  __device__ __forceinline__ void choose_in_wave(uint64_t e, int n, double low, float share) const {
     const double exact = unrounded(entry_logit(e));
-    const uint64_t w = (int)threadIdx.x < n ? (uint64_t)weight(entry_logit(e)) : 0, total = lane64(scan64(w), 63);
+    const uint64_t w = ((int)threadIdx.x < n) & (exact >= low) ? whole(exact) : 0, total = lane64(scan64(w), 63);
     const uint64_t target = target_of(share, total);
     uint64_t sum = 0;  // of the tokens up to this one, by index
 #pragma unroll 2
@@ -406,8 +406,8 @@ struct SampleRow {
       const uint64_t w = lane < n ? (uint64_t)weight(entry_logit(e)) : 0;
       const uint64_t upto = scan64(w);
       const double least = (double)p * (double)lane64(upto, 63);
-      const bool in = lane < n && (lane == 0 || ((p >= 1.f || (double)(upto - w) < least) && (double)w >= low));
-      choose_in_wave(e, __popcll(__ballot(in)), share);
+      const bool in = lane < n && (lane == 0 || p >= 1.f || (double)(upto - w) < least);
+      choose_in_wave(e, __popcll(__ballot(in)), low, share);
     }
     return chosen_in_wave(prob);
   }
@@ -421,8 +421,9 @@ struct SampleRow {
   __device__ __forceinline__ int chunks() const { return ((lead + V + E - 1) / E + 63) / 64; }
   __device__ __forceinline__ bool chunks_fit() const { return chunks() <= kFound / 2; }
 
-  // Of the sorted list's first n entries, how many are kept.
-  __device__ __forceinline__ int kept_of_list(int n, int k, float p, double low) const {
+  // Of the sorted list's first n entries, how many top-k and top-p keep.  (min-p is asked of each token's unrounded
+  // weight wherever tokens are weighed for the choice, so that it does not depend on the way they were found.)
+  __device__ __forceinline__ int kept_of_list(int n, int k, float p) const {
     constexpr int Q = kSort / THREADS;
     if (k >= 1 && k < n) n = k;
     double w[Q];
@@ -444,7 +445,7 @@ struct SampleRow {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int i = q * THREADS + threadIdx.x;
-      const bool in = i < n && (p >= 1.f || (double)(upto[q] - (uint64_t)w[q]) < least) && w[q] >= low;
+      const bool in = i < n && (p >= 1.f || (double)(upto[q] - (uint64_t)w[q]) < least);
       kept += i == 0 || in ? 1 : 0;
     }
     lds_barrier();
@@ -481,7 +482,7 @@ struct SampleRow {
     return (int)~(uint32_t)e;
   }
 
-  // The token at `share` of the first n entries of the list (in any order), which are what b keeps with weights
+  // The token at `share` of the first n entries of the list (in any order), which are what b keeps, with weights
   // from low on: their weights summed by chunk, in index order.
   __device__ __forceinline__ int choose_of_list(int n, const Border& b, double low, float share, float* prob) const {
     lds_barrier();
@@ -490,7 +491,9 @@ struct SampleRow {
     lds_barrier();
 #pragma unroll 1
     for (int i = threadIdx.x; i < n; i += THREADS) {
-      const uint64_t e = sh.list[i], w = whole(unrounded(entry_logit(e)));
+      const uint64_t e = sh.list[i];
+      const double v = unrounded(entry_logit(e));
+      const uint64_t w = whole(v >= low ? v : 0.0);
       atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunks[((int)~(uint32_t)e + lead) / (64 * E)]), (unsigned long long)w);
     }
     return choose_of_chunks(b, low, share, prob);
@@ -954,9 +957,9 @@ __global__ __launch_bounds__(THREADS, 4) void sample_kernel(SampleArgs a) {
       token = s.choose_of_few(n, k, p, low, share, &prob);
     } else if (n <= Row::kSort) {
       s.sort(n);
-      n = s.kept_of_list(n, k, p, low);
+      n = s.kept_of_list(n, k, p);
       b = s.border_of(n - 1);
-      token = s.chunks_fit() ? s.choose_of_list(n, b, 0.0, share, &prob) : s.choose_of_row(b, 0.0, share, &prob);
+      token = s.chunks_fit() ? s.choose_of_list(n, b, low, share, &prob) : s.choose_of_row(b, low, share, &prob);
     } else {
       bool summed = false;
 #pragma unroll 1
