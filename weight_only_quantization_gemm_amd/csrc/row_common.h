@@ -59,9 +59,13 @@ __device__ __forceinline__ float row_join(float v, float* part, Op op) {
 
 // rint(127 v / top) exactly, for top = max |v| over the row; by = 127 / top rounded.
 // The product v * by is within 2^-15 of 127 v / top, so its nearest whole number
-// is the wanted one unless it lies closer than that to a half; there (one value in
-// ten thousand) the quotient is formed in 64 bits, whose 53 can hold every half
-// and miss none: 127 v / top is a half itself or at least 2^-26 away from it.
+// is the wanted one unless it lies closer than that to a half; within 10^-4 of one (one
+// value in five thousand) the quotient is formed in 64 bits.  With v = a 2^i and
+// top = b 2^(i + d), a and b whole and below 2^24, it differs from a half h / 2 by
+// (254 a - h b 2^d) / (b 2^(d + 1)).  A whole numerator that is not 0 is at least 1, and 2
+// where d > 0, as both of its terms are even then; d is at most 8 (254 a < 2^32, b >= 2^23,
+// and with h >= 1 a quotient next to a half has b 2^d near 254 a).  So what is no half is at least
+// 2^-32 away from one, and the 64-bit quotient's error, 127 2^-53, makes and misses none.
 // A row with an infinity or a NaN has codes 0, and its scale says what it had.
 __device__ __forceinline__ float code_of(float v, float by, float top) {
   const float q = v * by, r = rintf(q);
