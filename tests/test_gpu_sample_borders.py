@@ -56,3 +56,21 @@ def test_min_p_is_asked_of_the_weight(first, V, top_k, t, units):
             prob = np.array([prob for _, prob in want])
             # the quotient's rounding to fp32; a sum of at least 1 whose packed weights are within half a unit each
             assert np.all(np.abs(r["probs"].cpu().numpy() - prob) <= (2.0 ** -24 + PACKED * 2.0 ** -44) * prob)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("value", [-3.25, float("inf")])
+def test_the_largest_sum(value, half):
+    """A row of 2^20 equal logits: each weighs 2^43 units, their sum is 2^63.  Of n that are kept the token is the whole
+    part of u n, exactly, and its probability 1 / n to fp32's rounding."""
+    V = 1 << 20
+    u = np.array([0.0, 0.25, 0.5, 0.7, 1 - 2.0 ** -24, 1.0, 2.0], np.float32)
+    logits = torch.full((len(u), V), value, dtype=torch.float16 if half else torch.float32, device=DEV)
+    du = torch.from_numpy(u).to(DEV)
+    for given, n in ((dict(), V), (dict(top_p=0.5), V // 2), (dict(top_k=V - 1), V - 1), (dict(top_k=700000, top_p=0.5), 350000),
+                     (dict(min_p=1.0), V), (dict(top_p=0.75, min_p=0.5), 3 * V // 4)):
+        r = awq.awq_sample(logits, du, **given)
+        want = np.minimum(np.floor(u.astype(np.longdouble) * n), n - 1).astype(np.int64)  # 24 bits times 20
+        assert r["tokens"].tolist() == want.tolist(), given
+        assert np.all(np.abs(r["probs"].cpu().numpy() - 1 / n) <= 2.0 ** -24 / n)
