@@ -210,7 +210,7 @@ struct SampleRow {
     for (int e = 0; e < E; ++e) v[e] = unrounded((float)x[e]);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      if constexpr (!ALL) v[e] = b.keeps((float)x[e], j * E - lead + e) & (v[e] >= low) ? v[e] : 0.0;
+      if constexpr (!ALL) v[e] = (b.keeps((float)x[e], j * E - lead + e) & (v[e] >= low)) ? v[e] : 0.0;
       w[e] = whole(v[e]);
     }
   }
@@ -324,7 +324,7 @@ struct SampleRow {
           const vec x = load(j < end ? j : 0);
           uint32_t in = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e) in |= (j < end) & ((float)x[e] >= finite) ? 1u << e : 0u;
+          for (int e = 0; e < E; ++e) in |= ((j < end) & ((float)x[e] >= finite)) ? 1u << e : 0u;
           if (low > 0.0)
 #pragma unroll
             for (int e = 0; e < E; ++e) in &= unrounded((float)x[e]) >= low ? ~0u : ~(1u << e);
@@ -374,7 +374,7 @@ struct SampleRow {
   // first wave: lane i has entry i (0 from n on).
   __device__ __forceinline__ void choose_in_wave(uint64_t e, int n, double low, float share) const {
     const double exact = unrounded(entry_logit(e));
-    const uint64_t w = ((int)threadIdx.x < n) & (exact >= low) ? whole(exact) : 0, total = lane64(scan64(w), 63);
+    const uint64_t w = (((int)threadIdx.x < n) & (exact >= low)) ? whole(exact) : 0, total = lane64(scan64(w), 63);
     const uint64_t target = target_of(share, total);
     uint64_t sum = 0;  // of the tokens up to this one, by index
 #pragma unroll 2
@@ -547,7 +547,7 @@ struct SampleRow {
         __asm__ volatile("" ::: "memory");  // a wave's LDS accesses are done in order
         waiting -= n;
         const double v = unrounded(queue[waiting + (lane < n ? lane : 0)]);
-        mine += whole((lane < n) & (v >= low) ? v : 0.0);
+        mine += whole(((lane < n) & (v >= low)) ? v : 0.0);
         __asm__ volatile("" ::: "memory");
       };
       each([&](vec x, int j) {
@@ -781,7 +781,7 @@ struct SampleRow {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const float l = (float)x[e];
-          near |= (l >= from) & (l <= to) & old.keeps(l, j * E - lead + e) ? 1u << e : 0u;
+          near |= ((l >= from) & (l <= to) & old.keeps(l, j * E - lead + e)) ? 1u << e : 0u;
         }
         append(x, j, near);
       }
@@ -791,7 +791,7 @@ struct SampleRow {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = unrounded((float)x[e]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += whole(((float)x[e] > to) & (v[e] >= low) ? v[e] : 0.0);
+      for (int e = 0; e < E; ++e) sum += whole((((float)x[e] > to) & (v[e] >= low)) ? v[e] : 0.0);
       sum = scan64(sum);
       if ((threadIdx.x & 63) == 63 && j / 64 < chunks()) sh.chunks[j / 64] = sum;
     });
