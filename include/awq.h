@@ -616,6 +616,8 @@ int awq_kv_attention(const void* q, int64_t q_stride, const void* k_codes, const
  *                codes and scale 0
  * Requires T in [1, 2^24], N % 8 == 0, 8 <= N <= 65536, eps >= 0 and finite,
  * |scale| finite.  Apart from h_out = h no output overlaps an input or another.
+ * With eps = 0 a row of zeros (layer: of equal values) has no norm: P(y), and x as
+ * fp16, are then undefined.
  */
 #define AWQ_NORM_RMS 0
 #define AWQ_NORM_LAYER 1
@@ -679,8 +681,8 @@ int awq_gemm_i8_kernel(int64_t M, int64_t N, int64_t K, int32_t quantized, char*
  *   top-k     the first k (k < 1 or k >= V: all)
  *   top-p     of those, the ones before which the sum of weights is below p times
  *             their sum, and always the first (p >= 1 or NaN: all)
- *   min-p     of those, the ones with w_i >= m, and always the first (m <= 0 or
- *             NaN: all)
+ *   min-p     of those, the ones with w_i >= m (w_i as it is before it is rounded
+ *             for the sums), and always the first (m <= 0 or NaN: all)
  *   token     the first index i, in index order, of the remaining ones at which
  *             their weights' sum up to i exceeds u times their sum (u below 0 or
  *             NaN counts as 0; from 1 on the last one)

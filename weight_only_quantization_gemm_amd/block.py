@@ -5,6 +5,9 @@ As in serve.py: each wrapper checks dtypes, devices and shapes, allocates output
 with torch on the inputs' device, and calls libawq on torch's current stream of that device; all
 arithmetic happens in the library's HIP kernels.  A decoding step makes these calls on little
 data, so the wrappers are kept short.
+
+As everywhere in the library every tensor starts on 16 bytes, the small ones too: a slice such as
+u[i] of fp32 [steps][5] does not, and is refused by name; its clone does.
 """
 from __future__ import annotations
 

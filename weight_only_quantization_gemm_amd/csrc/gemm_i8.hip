@@ -16,8 +16,8 @@
 // the matrix cores busy for 60 % of the cycles at the 1.8 GHz that is left.  Waves of
 // 128 tokens x 64 channels, 2 x 4 of them: 1645 us; 4 x 2 of 64 x 128 1688; four of
 // 128 x 128 1860.  Few tokens are bound by the weights' one read: 32 x 50021 x 4096
-// 50 us, 4.1 TB/s (a copy: 5.2); 77 x 4096 x 11008 with 8 shares of K 14.4 us and 4
-// for their join, of which a block's start and end are the larger part.
+// 50 us, 4.1 TB/s (a read alone: 6.3; 391 blocks for 256 units); 77 x 4096 x 11008 with 7 shares of K
+// 14.3 us and 4 for their join, of which a block's start and end are the larger part (6 and 8 shares take as long).
 #include <cmath>
 
 #include "awq_internal.h"
@@ -219,8 +219,10 @@ __global__ __launch_bounds__(256) void gemm_i8_join_kernel(I8Args a) {
 // of a wave are under way while DEPTH are multiplied, across the groups' ends; TT tiles of 16 tokens come
 // from the caches again for every group.
 // FUSED: x is one fp16 row, which each block quantises to LDS itself (one launch instead of two), while its
-// first weights are under way.  11008 x 4096: 15.1 us with the row's codes, 13 from the caches (3.0 and 3.5 TB/s);
-// 28 with a launch for the codes and without DEPTH.  24 tokens x 4096 x 4096: 8.2 us.
+// first weights are under way.  11008 x 4096: 15.4 us with the row's codes (28 with a launch for them and without DEPTH), 12.0
+// for a row that is in 8 bits already; a bare kernel's read of these 45 MB that ends each block with a store takes 8.7.
+// Open: more than one batch of weights under way while the row is quantised, and blocks of equal numbers of
+// groups (688 of them on 256 units).  24 tokens x 4096 x 4096: 8.2 us.
 template <int TT, int NW, int DEPTH, bool FUSED, typename Y>
 __global__ __launch_bounds__(64 * NW) void gemm_i8_skinny_kernel(I8Args a) {
   extern __shared__ __align__(16) unsigned char rows[];  // FUSED: the row's codes
@@ -347,7 +349,7 @@ static bool i8_fused(int64_t M, int64_t K, bool quantized) { return !quantized &
 // and 28672 x 8192, M = 1 .. 5000; the kernel picked is on average 2 % slower than the best.  E.g.
 //   8 x 4096 x 4096:   few tokens' kernel 6.1, 32 x 64 tiles with 4 shares 10.0
 //   32 x 50021 x 4096: few tokens' kernel 82, 32 x 128 tiles 49.6, 64 x 128 52.7
-//   77 x 4096 x 11008: 64 x 64 tiles with 4 shares 20.5, 128 x 128 with 8 19.4, with 1 share 38
+//   77 x 4096 x 11008: 64 x 64 tiles with 4 shares 20.5, 128 x 128 with 6 to 8 20, with 1 share 38
 //   512 x 28672 x 8192: 256 x 256 tiles 135, 128 x 128 168
 struct I8Plan {
   int tile;    // index of kI8Tiles; -1: the kernel for few tokens

@@ -17,12 +17,12 @@
 // the result does not depend on timing.  A row's sum is at most 2^63 (2^20 equal logits), which takes
 // the 64 bits without a sign.
 //
-// Bounds and times (fp16 logits).  Lists: the chain of a first pass, 20 barriers and
-// a short sort; 1 x 32000 9.4 us, 61 x 50021 12 us, 512 x 131072 35 to 42 us with top-k
-// 50, top-p and min-p (its one read takes 26 us at a copy's rate).  Passes over all
-// weights: vector instructions, some 20 a token (a weight alone is 16 in 64 bits)
-// on the row's compute unit; unfiltered 20, 85 us for the two batches, top-p 0.9 46
-// and 189 us, of which histogram and border pass take 17 us each at 50021 tokens.
+// Bounds and times (fp16 logits, out of the caches; 61 x 50021 and 512 x 131072, whose one read takes 2.6 and 21 us in
+// a kernel that only reads).  Lists: the chain of a first pass, 20 barriers and a short sort: top-k 50, top-p
+// and min-p 14 and 42 us (1 x 32000 9.5), min-p alone 13 and 48; greedy, a first pass and a search, 8 and 45.
+// Passes over all weights: vector instructions, some 20 a token (a weight alone is 16 in 64 bits) on the row's compute
+// unit: unfiltered 20 and 92 us, top-p 0.9 45 and 181, of which histogram and border pass take 17 us each at
+// 50021 tokens; top-k 3000 and top-p 70 and 273.
 #include "awq_internal.h"
 #include "row_common.h"
 
