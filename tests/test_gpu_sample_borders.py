@@ -59,6 +59,24 @@ def test_min_p_is_asked_of_the_weight(first, V, top_k, t, units):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("units", [87.96, 88.30])
+@pytest.mark.parametrize("first,top_k", [(1, 25), (80, 104), (80, 650), (400, 424), (3000, 3024), (3000, 0)])
+def test_min_p_in_the_longest_rows(first, top_k, units):
+    """The same in rows of 2^20, whose chunks are too many for sums of each to be kept."""
+    V, short, t = 1 << 20, first + PACKED, 1.0
+    m = float(np.float32(units * UNIT))
+    logits = rows(first, short, m, t, seed=first)
+    want = [choose(logits[b], t, top_k, 1.0, m, np.float32(1)) for b in range(B)]
+    dl = torch.full((B, V), -np.inf, device=DEV)
+    dl[:, :first] = 0.0
+    dl[:, V - PACKED:] = torch.from_numpy(logits[:, first:]).to(DEV)
+    du = torch.ones(B, device=DEV)
+    for k in (top_k, torch.full((B,), top_k, dtype=torch.int32, device=DEV)):
+        tokens = awq.awq_sample(dl, du, temperature=t, top_k=k, min_p=m)["tokens"].tolist()
+        assert tokens == [token if token < first else token + V - short for token, _ in want]
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("half", [True, False])
 @pytest.mark.parametrize("value", [-3.25, float("inf")])
 def test_the_largest_sum(value, half):
